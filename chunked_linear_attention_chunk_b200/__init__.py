@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libkda_debug.so" if os.environ.get("KDA_DEBUG_CHE
 
 KDA_BF16 = 0
 KDA_F32 = 1
+KDA_E4M3 = 2
 KDA_CHUNK = 64
 KDA_TILE = 16
 KDA_G_MIN_LOWEST = -5.4
@@ -67,6 +68,12 @@ EXPORTS = (
     "kda_chunk_fwd_segmented_workspace",
     "kda_chunk_fwd_segmented",
     "kda_chunk_bwd_recorded",
+    "kda_mla_fwd",
+    "kda_mla_bwd_workspace",
+    "kda_mla_bwd",
+    "kda_mla_decode_workspace",
+    "kda_mla_decode",
+    "kda_mla_cache_append",
 )
 
 
@@ -142,6 +149,18 @@ def lib() -> ctypes.CDLL:
     L.kda_chunk_fwd_segmented.restype = I
     L.kda_chunk_bwd_recorded.argtypes = L.kda_chunk_bwd.argtypes
     L.kda_chunk_bwd_recorded.restype = I
+    L.kda_mla_fwd.argtypes = [I, P, P, I, I, I, I, I, I, I, I, F, P, P, P, P, P, P]
+    L.kda_mla_fwd.restype = I
+    L.kda_mla_bwd_workspace.argtypes = [I, I, I, I, I, I, I]
+    L.kda_mla_bwd_workspace.restype = S
+    L.kda_mla_bwd.argtypes = [I, P, P, I, I, I, I, I, I, I, I, F, P, P, P, P, P, P, P, P, P, P, S, P]
+    L.kda_mla_bwd.restype = I
+    L.kda_mla_decode_workspace.argtypes = [I, I, I, I, I, I]
+    L.kda_mla_decode_workspace.restype = S
+    L.kda_mla_decode.argtypes = [I, I, I, I, I, I, I, F, P, I, P, P, I, I, P, I, P, P, P, P, S, P]
+    L.kda_mla_decode.restype = I
+    L.kda_mla_cache_append.argtypes = [I, P, I, I, I, I, I, P, P, P, I, I, P, P, I, I, P]
+    L.kda_mla_cache_append.restype = I
     _lib = L
     return L
 
@@ -537,6 +556,160 @@ def kda_decode_step(q, k, v, a, beta, S, g_min: float = -5.0, o=None):
                                float(g_min), _ptr(S), _ptr(o), _stream(q.device))
     _raise(st, "kda_decode_step")
     return o
+
+
+MLA_DIMS = (128, 64, 128)     # dn, dr, dv of the expanded latent attention
+MLA_CACHE_DIMS = (512, 64)    # dl, dr of a cached row
+
+
+def _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale):
+    dn, dr, dv = MLA_DIMS
+    if any(t.dtype != torch.bfloat16 for t in (q, kv, k_rope)):
+        raise TypeError("q, kv, k_rope must be bfloat16")
+    if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32:
+        raise TypeError("cu_q and cu_k must be int32")
+    if q.dim() != 3 or kv.dim() != 3 or q.shape[-1] != dn + dr or kv.shape[1:] != (q.shape[1], dn + dv) or \
+            k_rope.shape != (kv.shape[0], dr) or cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.numel() < 2:
+        raise ValueError("shape mismatch: q [Tq,H,192], kv [Tk,H,256], k_rope [Tk,64], cu_q and cu_k [N+1]")
+    return (cu_q.numel() - 1, q.shape[0], kv.shape[0], q.shape[1],
+            (dn + dr) ** -0.5 if scale is None else float(scale))
+
+
+def _same_device(*ts):
+    dev = next(t.device for t in ts if t is not None)
+    if any(t is not None and t.device != dev for t in ts):
+        raise ValueError("all tensors must be on one device")
+    return dev
+
+
+def _out(t, shape, dtype, dev, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
+    return t
+
+
+def kda_mla_fwd(q, kv, k_rope, cu_q, cu_k=None, scale=None, causal: bool = True, o=None, lse=None):
+    """Expanded latent attention over packed sequences (bf16).  q [Tq,H,192] (128 numbers and
+    64 rotated ones), kv [Tk,H,256] (a head's key part, then its value), k_rope [Tk,64]; cu_q and
+    cu_k (default cu_q) int32 [N+1] on the device.  ``causal``: the last query of a sequence sees
+    all its keys, the one before it all but the last, and so on.  ``scale`` defaults to
+    192 ** -0.5.  Returns (o [Tq,H,128] bf16, lse [Tq,H] float32)."""
+    cu_k = cu_q if cu_k is None else cu_k
+    _check_cuda(q, kv, k_rope, cu_q, cu_k, o, lse)
+    dev = _same_device(q, kv, k_rope, cu_q, cu_k, o, lse)
+    N, Tq, Tk, H, scale = _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale)
+    o = _out(o, (Tq, H, MLA_DIMS[2]), torch.bfloat16, dev, "o")
+    lse = _out(lse, (Tq, H), torch.float32, dev, "lse")
+    with torch.cuda.device(dev):
+        st = lib().kda_mla_fwd(N, _ptr(cu_q), _ptr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _ptr(q),
+                               _ptr(kv), _ptr(k_rope), _ptr(o), _ptr(lse), _stream(dev))
+    _raise(st, "kda_mla_fwd")
+    return o, lse
+
+
+def kda_mla_bwd_workspace(Tq: int, Tk: int, H: int) -> int:
+    return int(lib().kda_mla_bwd_workspace(Tq, Tk, H, *MLA_DIMS, KDA_BF16))
+
+
+def kda_mla_bwd(q, kv, k_rope, o, lse, dO, cu_q, cu_k=None, scale=None, causal: bool = True, workspace=None, out=None):
+    """Gradients of ``kda_mla_fwd`` given its o and lse and dO [Tq,H,128] bf16.  Returns a dict
+    of bf16 tensors dq [Tq,H,192], dkv [Tk,H,256], dk_rope [Tk,64] (summed over the heads);
+    ``out`` may supply some of them."""
+    cu_k = cu_q if cu_k is None else cu_k
+    out = dict(out or {})
+    _check_cuda(q, kv, k_rope, o, lse, dO, cu_q, cu_k, workspace, *out.values())
+    dev = _same_device(q, kv, k_rope, o, lse, dO, cu_q, cu_k, workspace, *out.values())
+    N, Tq, Tk, H, scale = _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale)
+    for name, t in (("o", o), ("dO", dO)):
+        _out(t, (Tq, H, MLA_DIMS[2]), torch.bfloat16, dev, name)
+    _out(lse, (Tq, H), torch.float32, dev, "lse")
+    g = {name: _out(out.get(name), t.shape, torch.bfloat16, dev, name)
+         for name, t in (("dq", q), ("dkv", kv), ("dk_rope", k_rope))}
+    if workspace is None:
+        workspace = torch.empty(kda_mla_bwd_workspace(Tq, Tk, H), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = lib().kda_mla_bwd(N, _ptr(cu_q), _ptr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _ptr(q),
+                               _ptr(kv), _ptr(k_rope), _ptr(o), _ptr(lse), _ptr(dO), _ptr(g["dq"]), _ptr(g["dkv"]),
+                               _ptr(g["dk_rope"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                               _stream(dev))
+    _raise(st, "kda_mla_bwd")
+    return g
+
+
+def _mla_cache(cache, cache_scale, block_table, kv_lens):
+    if cache.dim() != 4 or cache.shape[-1] != sum(MLA_CACHE_DIMS):
+        raise ValueError("cache must be [num_pages, page_size, G, 576]")
+    if cache.dtype == torch.bfloat16:
+        code = KDA_BF16
+    elif cache.dtype == torch.float8_e4m3fn:
+        code = KDA_E4M3
+    else:
+        raise TypeError("cache must be bfloat16 or float8_e4m3fn")
+    if (code == KDA_E4M3) != (cache_scale is not None):
+        raise ValueError("cache_scale goes with a float8_e4m3fn cache, and only with one")
+    if cache_scale is not None and (cache_scale.dtype != torch.float32 or
+                                    cache_scale.shape != (cache.shape[0], cache.shape[2])):
+        raise ValueError("cache_scale must be float32 [num_pages, G]")
+    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32:
+        raise TypeError("block_table and kv_lens must be int32")
+    if block_table.dim() != 2 or kv_lens.shape != block_table.shape[:1]:
+        raise ValueError("shape mismatch: block_table [N, max_pages], kv_lens [N]")
+    return code
+
+
+def kda_mla_decode_workspace(N: int, Sq: int, H: int, G: int = 1) -> int:
+    return int(lib().kda_mla_decode_workspace(N, Sq, H, G, *MLA_CACHE_DIMS))
+
+
+def kda_mla_decode(q, cache, block_table, kv_lens, scale=None, cache_scale=None, o=None, lse=None, workspace=None):
+    """Absorbed latent attention of new tokens over the paged cache.  q [N,Sq,H,576] bf16 (the
+    query in the latent space, then its rotated part); cache [num_pages,page_size,G,576] bf16, or
+    float8_e4m3fn with cache_scale float32 [num_pages,G]; block_table int32 [N,max_pages];
+    kv_lens int32 [N], the new tokens counted (token i sees the first kv_lens - Sq + 1 + i rows).
+    ``scale`` defaults to 192 ** -0.5.  Returns (o [N,Sq,H,512] bf16, lse [N,Sq,H] float32)."""
+    _check_cuda(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
+    dev = _same_device(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
+    code = _mla_cache(cache, cache_scale, block_table, kv_lens)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if q.dim() != 4 or q.shape[0] != block_table.shape[0] or q.shape[-1] != sum(MLA_CACHE_DIMS):
+        raise ValueError("q must be [N, Sq, H, 576]")
+    N, Sq, H, _ = q.shape
+    P, ps, G, _ = cache.shape
+    o = _out(o, (N, Sq, H, MLA_CACHE_DIMS[0]), torch.bfloat16, dev, "o")
+    lse = _out(lse, (N, Sq, H), torch.float32, dev, "lse")
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(kda_mla_decode_workspace(N, Sq, H, G), dtype=torch.uint8, device=dev)
+        st = lib().kda_mla_decode(N, Sq, H, G, *MLA_CACHE_DIMS, KDA_BF16,
+                                  sum(MLA_DIMS[:2]) ** -0.5 if scale is None else float(scale), _ptr(q), code,
+                                  _ptr(cache), _ptr(cache_scale), P, ps, _ptr(block_table), block_table.shape[1],
+                                  _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(dev))
+    _raise(st, "kda_mla_decode")
+    return o, lse
+
+
+def kda_mla_cache_append(kv_new, cu_new, kv_lens, block_table, cache, cache_scale=None) -> None:
+    """Write the rows kv_new [T_new,G,576] (bf16; sequence n's are cu_new[n] .. cu_new[n+1]-1)
+    into the cache behind the kv_lens[n] rows sequence n holds, in place.  A float8_e4m3fn cache
+    keeps one power-of-two scale for each page and group in cache_scale [num_pages,G], which grows
+    (and the page's earlier rows are rounded anew) where new rows need it."""
+    _check_cuda(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
+    dev = _same_device(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
+    code = _mla_cache(cache, cache_scale, block_table, kv_lens)
+    P, ps, G, dc = cache.shape
+    if kv_new.dtype != torch.bfloat16 or cu_new.dtype != torch.int32:
+        raise TypeError("kv_new must be bfloat16, cu_new int32")
+    if kv_new.dim() != 3 or kv_new.shape[1:] != (G, dc) or cu_new.shape != (kv_lens.shape[0] + 1,):
+        raise ValueError("shape mismatch: kv_new [T_new,G,576], cu_new [N+1]")
+    with torch.cuda.device(dev):
+        st = lib().kda_mla_cache_append(kv_lens.shape[0], _ptr(cu_new), kv_new.shape[0], G, *MLA_CACHE_DIMS, KDA_BF16,
+                                        _ptr(kv_new), _ptr(kv_lens), _ptr(block_table), block_table.shape[1], code,
+                                        _ptr(cache), _ptr(cache_scale), P, ps, _stream(dev))
+    _raise(st, "kda_mla_cache_append")
 
 
 def kda_device_status(device=None) -> int:

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "api_checks.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
@@ -37,60 +38,6 @@ unsigned int *device_status_ptr()
     return static_cast<unsigned int *>(p);
 }
 
-namespace {
-
-constexpr int64_t kMaxElems = (int64_t)1 << 40;
-constexpr int kMaxPackedTokens = 0x7fffffff - 64;  // packed axis; cu_seqlens are int32
-
-struct Range {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi)
-    Range() = default;
-    Range(const void *p, int64_t bytes) : lo((uintptr_t)p), hi((uintptr_t)p + (uintptr_t)(bytes > 0 ? bytes : 0)) {}
-    bool empty() const { return lo == 0 || hi <= lo; }
-};
-
-bool overlaps(const Range &x, const Range &y)
-{
-    if (x.empty() || y.empty())
-        return false;
-    return x.lo < y.hi && y.lo < x.hi;
-}
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// beta is read one element at a time: its natural alignment is enough.
-bool beta_aligned(const void *beta, int es) { return ((uintptr_t)beta % (uintptr_t)es) == 0; }
-
-int elem_size(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
-
-bool dtype_ok(kda_dtype dt) { return dt == KDA_BF16 || dt == KDA_F32; }
-
-kda_status check_gmin(float g_min)
-{
-    if (!std::isfinite(g_min) || !(g_min < 0.0f))
-        return KDA_ERR_INVALID_ARG;
-    if (g_min < KDA_G_MIN_LOWEST)
-        return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
-}
-
-kda_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
-
-// Product of non-negative ints with an overflow bound; -1 when it exceeds kMaxElems.
-int64_t safe_prod(std::initializer_list<int64_t> xs)
-{
-    int64_t p = 1;
-    for (int64_t x : xs) {
-        if (x < 0)
-            return -1;
-        if (x != 0 && p > kMaxElems / x)
-            return -1;
-        p *= x;
-    }
-    return p;
-}
-
-}  // namespace
 }  // namespace kda
 
 using namespace kda;
@@ -207,14 +154,6 @@ kda_status check_gate(kda_gate gate, float g_min, kda_dtype dtype)
     if (gate == KDA_GATE_LOGSIGMOID)
         return dtype == KDA_BF16 ? KDA_OK : KDA_ERR_UNSUPPORTED;
     return KDA_ERR_INVALID_ARG;
-}
-
-bool all_aligned(std::initializer_list<const void *> ps)
-{
-    for (const void *p : ps)
-        if (p && !aligned16(p))
-            return false;
-    return true;
 }
 
 kda_status check_workspace(const ChunkShape &sh, const void *workspace, size_t ws_bytes)

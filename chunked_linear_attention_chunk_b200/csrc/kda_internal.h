@@ -94,4 +94,23 @@ kda_status dispatch_chunk_fwd(int B, int T, int H, int dk, kda_dtype dtype, cons
 cudaError_t launch_decode(int N, int H, int D, kda_dtype dt, const void *q, const void *k, const void *v,
                           const void *a, const void *beta, float g_min, float *S, void *o, cudaStream_t s);
 
+// Latent attention.  Expanded form over packed sequences (head dims 128 + 64 and 128): forward
+// and gradients; absorbed form over a paged cache of 512 + 64 numbers a row; writing that cache.
+cudaError_t launch_mla_fwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, bool causal,
+                           float scale, const void *q, const void *kv, const void *k_rope, void *o, float *lse,
+                           cudaStream_t s);
+size_t mla_bwd_workspace(int Tq, int Tk, int H);
+cudaError_t launch_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, bool causal,
+                           float scale, const void *q, const void *kv, const void *k_rope, const void *o,
+                           const float *lse, const void *dO, void *dq, void *dkv, void *dk_rope, void *workspace,
+                           cudaStream_t s);
+size_t mla_decode_workspace(int N, int Sq, int H, int G);
+cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const void *q, bool e4m3, const void *cache,
+                              const float *cache_scale, int num_pages, int page_size, const int32_t *block_table,
+                              int max_pages, const int32_t *kv_lens, void *o, float *lse, void *workspace,
+                              cudaStream_t s);
+cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, const void *kv_new,
+                              const int32_t *kv_lens, const int32_t *block_table, int max_pages, bool e4m3, void *cache,
+                              float *cache_scale, int num_pages, int page_size, cudaStream_t s);
+
 }  // namespace kda

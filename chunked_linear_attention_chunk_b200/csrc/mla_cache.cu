@@ -1,0 +1,194 @@
+// mla_cache.cu -- writing new rows into the paged latent cache (bfloat16, or e4m3 with a
+// power-of-two scale for each page and latent group).
+//
+// Bound by bytes: a new row is read once (1152 B) and written once (1152 or 576 B); a page that
+// held earlier rows and whose scale grows is read and written once more.  One CTA takes one
+// (page that receives rows, group): the page is where the scale lives, so one CTA sees all that
+// decides it and no two CTAs write the same page.  Its new rows stay in registers between the
+// maximum and the rounding when they fit (kKeep vectors a thread), else they are read again
+// (from L2).
+#include <cuda_fp8.h>
+
+#include "mla_common.cuh"
+
+namespace kda {
+
+namespace {
+
+using namespace mla;
+
+constexpr int kThreads = 256;
+constexpr int kVecs = kDC / 8;  // 16-byte vectors of a bfloat16 row
+constexpr int kKeep = 18;       // 64 rows of a group over 256 threads
+
+struct AppendArgs {
+    int N, T_new, G, max_pages, num_pages, page_size;
+    const int32_t *cu, *kv_lens, *block_table;
+    const __nv_bfloat16 *x;
+    void *cache;
+    float *cache_scale;
+    unsigned int *status;
+};
+
+__device__ __forceinline__ float amax8(uint4 v)
+{
+    // |x| of two bfloat16 a word, compared as integers: NaN is above infinity, which is above all
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    return __uint_as_float(m);
+}
+
+// Two floats to two e4m3 codes, to nearest even (saturating; the caller's scale leaves |x| <= 448).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint2 quantise8(uint4 v, float inv)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_bf16x2(w[i]);
+        c[i] = e4m3x2(f.x * inv, f.y * inv);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The smallest power of two s >= 2^-100 with amax <= 448 s; NaN for an infinite or NaN amax.
+__device__ __forceinline__ float scale_for(float amax)
+{
+    const uint32_t b = __float_as_uint(amax);
+    if (b >= 0x7f800000u)
+        return __uint_as_float(0x7fc00000u);
+    // amax = 1.f 2^(E - 127); 448 = 1.75 2^8
+    const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
+}
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
+{
+    __shared__ int sh[36];
+    __shared__ float s_max[kThreads / 32];
+    const int tid = threadIdx.x, ps = a.page_size;
+    if (!offsets_ok<kThreads>(a.cu, a.N, a.T_new)) {
+        if (tid == 0)
+            report_device_error(a.status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    // sequence n touches the pages of its places [len, len + new rows)
+    auto touched = [&](int n) {
+        const int m = a.cu[n + 1] - a.cu[n], len = a.kv_lens[n];
+        if (m == 0)
+            return 0;
+        if (len < 0)
+            return 1;  // refused below
+        return (int)(((int64_t)len % ps + m + ps - 1) / ps);
+    };
+    Item it;
+    if (!find_item<kThreads>(a.N, blockIdx.x, touched, it, sh))
+        return;
+    const int n = it.seq, g = blockIdx.y, len = a.kv_lens[n], m = a.cu[n + 1] - a.cu[n];
+    const int64_t p_idx = len < 0 ? -1 : (int64_t)len / ps + it.k;
+    const int page = p_idx >= 0 && p_idx < a.max_pages ? a.block_table[(int64_t)n * a.max_pages + p_idx] : -1;
+    if (page < 0 || page >= a.num_pages) {
+        if (tid == 0)
+            report_device_error(a.status, KDA_ERR_INVALID_ARG);
+        return;
+    }
+    const int slot0 = it.k == 0 ? len % ps : 0;                         // first slot written
+    const int64_t first = it.k == 0 ? 0 : (int64_t)it.k * ps - len % ps;  // its row among the sequence's
+    const int rows = (int)min((int64_t)(ps - slot0), m - first);
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.x + ((a.cu[n] + first) * a.G + g) * kDC);
+    const int64_t src_row = (int64_t)a.G * kVecs;  // 16-byte vectors from a row to the next
+    const int64_t dst0 = (((int64_t)page * ps + slot0) * a.G + g) * kDC;
+    const int nvec = rows * kVecs;
+    if constexpr (!kE4M3) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + dst0);
+        for (int v = tid; v < nvec; v += kThreads)
+            dst[v / kVecs * src_row + v % kVecs] = src[v / kVecs * src_row + v % kVecs];
+        return;
+    }
+    uint4 keep[kKeep];
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int v = tid + i * kThreads;
+        if (v < nvec) {
+            keep[i] = src[v / kVecs * src_row + v % kVecs];
+            mx = __uint_as_float(max(__float_as_uint(mx), __float_as_uint(amax8(keep[i]))));
+        }
+    }
+    for (int v = tid + kKeep * kThreads; v < nvec; v += kThreads)
+        mx = __uint_as_float(max(__float_as_uint(mx), __float_as_uint(amax8(src[v / kVecs * src_row + v % kVecs]))));
+    uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+    if ((tid & 31) == 0)
+        s_max[tid >> 5] = __uint_as_float(mb);
+    float *sp = a.cache_scale + (int64_t)page * a.G + g;
+    const float old = slot0 > 0 ? *sp : 0.0f;  // read by all before one thread writes it (barrier between)
+    __syncthreads();
+    mb = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        mb = max(mb, __float_as_uint(s_max[w]));
+    const float need = scale_for(__uint_as_float(mb));
+    // a NaN scale (new or held) stays NaN
+    const float now = slot0 > 0 ? (need != need || old != old ? __uint_as_float(0x7fc00000u) : fmaxf(need, old)) : need;
+    if (tid == 0)
+        *sp = now;
+    unsigned char *codes = static_cast<unsigned char *>(a.cache);
+    if (slot0 > 0 && !(now == old)) {  // earlier rows of the page, at the larger scale
+        const float f = old / now;
+        const int64_t base = ((int64_t)page * ps * a.G + g) * kDC;
+        for (int v = tid; v < slot0 * kVecs; v += kThreads) {
+            uint2 *p = reinterpret_cast<uint2 *>(codes + base + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8);
+            const uint2 u = *p;
+            const uint32_t w[2] = {u.x, u.y};
+            uint32_t r[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3);
+                const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> 16), __NV_E4M3);
+                const float2 f0 = __half22float2(__half2(h0)), f1 = __half22float2(__half2(h1));
+                r[i] = e4m3x2(f0.x * f, f0.y * f) | (e4m3x2(f1.x * f, f1.y * f) << 16);
+            }
+            *p = make_uint2(r[0], r[1]);
+        }
+    }
+    // 1 / now as a power of two's exact reciprocal (now >= 2^-100)
+    const float inv = 1.0f / now;
+    unsigned char *dst = codes + dst0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int v = tid + i * kThreads;
+        if (v < nvec)
+            *reinterpret_cast<uint2 *>(dst + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8) = quantise8(keep[i], inv);
+    }
+    for (int v = tid + kKeep * kThreads; v < nvec; v += kThreads)
+        *reinterpret_cast<uint2 *>(dst + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8) =
+            quantise8(src[v / kVecs * src_row + v % kVecs], inv);
+}
+
+}  // namespace
+
+cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, const void *kv_new,
+                              const int32_t *kv_lens, const int32_t *block_table, int max_pages, bool e4m3, void *cache,
+                              float *cache_scale, int num_pages, int page_size, cudaStream_t s)
+{
+    AppendArgs a{N, T_new, G, max_pages, num_pages, page_size, cu_new, kv_lens, block_table,
+                 static_cast<const __nv_bfloat16 *>(kv_new), cache, cache_scale, device_status_ptr()};
+    if (!a.status)
+        return cudaErrorInvalidDevice;
+    // a sequence of m > 0 rows touches at most (m - 1) / page_size + 2 pages, and no more than m
+    const int64_t most = (int64_t)T_new / page_size + 2 * (int64_t)N;
+    const dim3 grid((unsigned)(most < T_new ? most : T_new), G);
+    (e4m3 ? mla_append_kernel<true> : mla_append_kernel<false>)<<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

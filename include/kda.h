@@ -56,7 +56,8 @@ typedef struct CUstream_st *kda_stream_t;
 
 typedef enum {
     KDA_BF16 = 0, /* bfloat16 token tensors, float32 state and accumulation */
-    KDA_F32 = 1   /* float32 everywhere (CUDA-core debug path)              */
+    KDA_F32 = 1,  /* float32 everywhere (CUDA-core debug path)              */
+    KDA_E4M3 = 2  /* 8-bit e4m3 codes with scales: a latent cache only (kda_mla_decode) */
 } kda_dtype;
 
 typedef enum {
@@ -396,6 +397,109 @@ kda_status kda_decode_step(int N, int H, int dk, int dv, kda_dtype dtype, const 
                            float g_min, float *S, void *o, kda_stream_t stream);
 
 /*
+ * Latent attention (MLA): the softmax-attention layers that a hybrid model interleaves with the
+ * KDA layers above ("Trillion-Parameter MoE ... Engineering" section 3.1, "Trillion-Scale ..."
+ * section 2.1: KDA and gated latent attention; the output gate and the projections live
+ * upstream).  Keys and values of a token come from one latent vector of dl = 512 numbers and one
+ * rotated key of dr = 64 that the heads share.  Two forms of the same attention:
+ *   expanded (kda_mla_fwd, kda_mla_bwd): the caller has multiplied the latents out to per-head
+ *     keys and values; prefill and training over packed sequences;
+ *   absorbed (kda_mla_decode): queries are carried into the latent space by the caller, so that
+ *     every head of a group attends to the same cached rows; decode steps over a paged cache,
+ *     which kda_mla_cache_append fills.
+ * Token tensors are bfloat16; scores, softmax statistics and sums are float32, a softmax weight
+ * is rounded to bfloat16 where it enters a matrix product.
+ *
+ * kda_mla_fwd -- attention of packed sequences in the expanded form.  Sequence n has the queries
+ * [cu_q[n], cu_q[n+1]) and the keys [cu_k[n], cu_k[n+1]) of its packed axis (cu_k beyond cu_q:
+ * tokens that were there before the call, as in a chunked prefill):
+ *     s_ij = scale (q_i[0:dn] . k_j + q_i[dn:dn+dr] . k_rope_j),   o_i = sum_j softmax_j(s_i) v_j
+ * over all keys of the sequence, or with `causal` over the keys j <= i + lk - lq (places within
+ * the sequence; the last query sees every key).  A query that sees no key gets o = 0, lse = -inf.
+ *   N          sequences (1 .. 65535); cu_q, cu_k: DEVICE int32 [N + 1], 4-byte aligned, first
+ *              entry 0, non-decreasing, last entry at most Tq (Tk).  Rows behind the last
+ *              sequence are neither read nor written.  Checked on the device: an invalid array
+ *              records KDA_ERR_INVALID_ARG in the device status word and nothing is written.
+ *   Tq, Tk     rows of the packed axes (0 .. 2^31 - 65); H heads (1 .. 65535).
+ *   dn, dr, dv (128, 64, 128).  dtype: KDA_BF16.  scale: finite, > 0.
+ *   q          [Tq, H, dn + dr];  kv: [Tk, H, dn + dv], a head's key part, then its value (the
+ *              up-projection's output as it is);  k_rope: [Tk, dr].  No row behind cu_k[N] is read.
+ *   o          [Tq, H, dv] out;  lse: [Tq, H] float32 out, the natural logarithm of sum_j e^{s_ij},
+ *              or NULL.  They overlap neither each other nor an input.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, ALIAS, CUDA.  Tq == 0 does nothing.
+ *
+ * kda_mla_bwd -- its gradients, given o and lse as kda_mla_fwd wrote them and dO = dL/do:
+ *     p_ij = e^{s_ij - lse_i},  dS_ij = scale p_ij (dO_i . v_j - dO_i . o_i),
+ *     dq_i = sum_j dS_ij [k_j, k_rope_j],  dk_j = sum_i dS_ij q_i[0:dn],  dv_j = sum_i p_ij dO_i,
+ *     dk_rope_j = sum over heads and i of dS_ij q_i[dn:dn+dr]
+ *   dq         [Tq, H, dn + dr], dkv: [Tk, H, dn + dv], dk_rope: [Tk, dr] out, bfloat16 (each
+ *              summed in float32, dk_rope over the heads in order, and rounded once).  Sums are
+ *              taken in an order that the shapes alone fix: equal calls give equal bits.
+ *   workspace  >= kda_mla_bwd_workspace(...) bytes, 16-byte aligned.
+ * Other arguments, checks and errors as kda_mla_fwd, and WORKSPACE.
+ */
+kda_status kda_mla_fwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, int dn, int dr, int dv,
+                       kda_dtype dtype, int causal, float scale, const void *q, const void *kv, const void *k_rope,
+                       void *o, float *lse, kda_stream_t stream);
+size_t kda_mla_bwd_workspace(int Tq, int Tk, int H, int dn, int dr, int dv, kda_dtype dtype);
+kda_status kda_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, int dn, int dr, int dv,
+                       kda_dtype dtype, int causal, float scale, const void *q, const void *kv, const void *k_rope,
+                       const void *o, const float *lse, const void *dO, void *dq, void *dkv, void *dk_rope,
+                       void *workspace, size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * The latent cache: a pool of num_pages pages of page_size tokens, [num_pages, page_size, G, dl + dr],
+ * each token a row of dl latent numbers and dr rotated ones for each of G latent groups (1 in the
+ * plain form; query head h reads group h / (H / G)).  Place p of sequence n lives in page
+ * block_table[n, p / page_size], slot p % page_size.
+ *   KDA_BF16   rows are bfloat16; cache_scale is NULL.
+ *   KDA_E4M3   rows are e4m3 codes; a row stands for code * cache_scale[page, group] (float32
+ *              [num_pages, G], powers of two; kda_mla_cache_append writes them).
+ *   page_size  16, 32, or a multiple of 64 up to 65536.
+ *   block_table DEVICE int32 [N, max_pages]; entries past a sequence's last page are not read.  kv_lens:
+ *              DEVICE int32 [N].  Both 4-byte aligned.
+ *
+ * kda_mla_decode -- Sq new tokens for each of N sequences in the absorbed form:
+ *     s_j = scale q . c_j,  o = sum_j softmax_j(s) c_j[0:dl]
+ *   over the first kv_lens[n] - Sq + 1 + i places of sequence n for its i-th new token (kv_lens
+ *   counts the new tokens, whose rows are in the cache already).  A token that sees no row gets
+ *   o = 0, lse = -inf.
+ *   q          [N, Sq, H, dl + dr] bfloat16 (1 <= Sq, H a multiple of G);  dl, dr: (512, 64).
+ *   o          [N, Sq, H, dl] bfloat16 out;  lse: [N, Sq, H] float32 out or NULL.
+ *   workspace  >= kda_mla_decode_workspace(N, Sq, H, G, dl, dr) bytes, 16-byte aligned: partial
+ *              results of sequences that several CTAs share.  Nothing in it outlives the call; two
+ *              calls whose work overlaps need two.
+ *   A kv_lens entry outside 0 .. max_pages * page_size, or a page number outside the pool at a
+ *   place that is read, records KDA_ERR_INVALID_ARG in the device status word; that sequence's
+ *   outputs are then unspecified, and nothing outside the buffers is touched.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, ALIAS, WORKSPACE, CUDA.
+ *
+ * kda_mla_cache_append -- writes the rows kv_new [cu_new[n], cu_new[n+1]) to the places
+ * kv_lens[n], kv_lens[n] + 1, ... of sequence n (kv_lens: the lengths BEFORE the call, not changed).
+ *   KDA_BF16   copies the rows.
+ *   KDA_E4M3   a page's scale for a group becomes the larger of the smallest power of two s >= 2^-100
+ *              with |x| <= 448 s for the new rows x of that page and, if the page held earlier rows of
+ *              the sequence, its old scale; those rows' codes are rounded anew where the scale grew,
+ *              and the new rows are stored as x / s, rounded to nearest even.  An infinity or a NaN
+ *              among a page's new rows makes its scale NaN (and the attention over it).
+ *   kv_new     [T_new, G, dl + dr] bfloat16;  cu_new: DEVICE int32 [N + 1] as cu_q above (rows
+ *              behind the last sequence are not read).
+ *   Pages named twice among the written places give unspecified rows.  Invalid cu_new, a kv_lens
+ *   entry below 0, places past max_pages * page_size or page numbers outside the pool record
+ *   KDA_ERR_INVALID_ARG in the device status word; what they would reach is not written.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, ALIAS, CUDA.  T_new == 0 does nothing.
+ */
+size_t kda_mla_decode_workspace(int N, int Sq, int H, int G, int dl, int dr);
+kda_status kda_mla_decode(int N, int Sq, int H, int G, int dl, int dr, kda_dtype dtype, float scale, const void *q,
+                          kda_dtype cache_dtype, const void *cache, const float *cache_scale, int num_pages,
+                          int page_size, const int32_t *block_table, int max_pages, const int32_t *kv_lens, void *o,
+                          float *lse, void *workspace, size_t ws_bytes, kda_stream_t stream);
+kda_status kda_mla_cache_append(int N, const int32_t *cu_new, int T_new, int G, int dl, int dr, kda_dtype dtype,
+                                const void *kv_new, const int32_t *kv_lens, const int32_t *block_table, int max_pages,
+                                kda_dtype cache_dtype, void *cache, float *cache_scale, int num_pages, int page_size,
+                                kda_stream_t stream);
+
+/*
  * kda_chunk_fwd_noalloc -- kda_chunk_fwd for callers that cannot allocate device memory.
  * The pages have no counterpart to this call; it exists for the library's users.
  * Code that runs during CUDA graph capture (allocation is not allowed there), serving
@@ -431,7 +535,8 @@ size_t kda_chunk_fwd_noalloc_max_scratch(void);
  * kda_device_status -- synchronise `stream`, then return and clear the current
  * device's kernel status word: KDA_OK; KDA_ERR_DEVICE_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call; KDA_ERR_INVALID_ARG if kda_chunk_fwd_varlen found
- * its cu_seqlens invalid; KDA_ERR_DEVICE_BOUNDS if a debug-build index check failed;
+ * its cu_seqlens invalid or a kda_mla_* call its offsets, lengths or
+ * pages; KDA_ERR_DEVICE_BOUNDS if a debug-build index check failed;
  * KDA_ERR_CUDA if the synchronisation failed.  The first error
  * recorded since the last call is the one reported.
  */

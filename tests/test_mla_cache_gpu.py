@@ -1,0 +1,291 @@
+"""The paged latent cache on the GPU: kda_mla_decode against 64-bit arithmetic,
+kda_mla_cache_append against the row-by-row definition, and a layer's prefill, append and decode
+together."""
+import math
+
+import pytest
+import torch
+
+import chunked_linear_attention_chunk_b200 as kda
+import mla_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def table_for(lens, ps, g, spare=2):
+    need = [-(-n // ps) for n in lens]
+    order = torch.randperm(sum(need) + spare, generator=g, device="cuda").to(torch.int32)
+    t = torch.full((len(lens), max(1, max(need))), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, k in enumerate(need):
+        t[i, :k] = order[at:at + k]
+        at += k
+    return t, sum(need) + spare
+
+
+def make(lens, Sq, H, G, ps, e4m3, seed, std=0.6):
+    """Queries and a cache whose rows behind each sequence's end are NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    table, pages = table_for(lens, ps, g)
+    c = torch.randn(pages, ps, G, 576, generator=g, device="cuda").to(torch.bfloat16)
+    scale = None
+    if e4m3:
+        scale = torch.exp2(torch.randint(-9, -6, (pages, G), generator=g, device="cuda").float())
+        c = (c.float() / scale[:, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    live = torch.zeros(pages, ps, dtype=torch.bool, device="cuda")
+    for i, n in enumerate(lens):
+        for j in range(-(-n // ps)):
+            live[int(table[i, j]), :min(ps, n - j * ps)] = True
+    if e4m3:
+        c.view(torch.uint8)[~live] = 0x7F
+        scale[~live.any(1)] = math.nan
+    else:
+        c[~live] = math.nan
+    q = (torch.randn(len(lens), Sq, H, 576, generator=g, device="cuda") * std).to(torch.bfloat16)
+    return q, c, scale, table, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+CASES = [
+    # lens, Sq, H, G, page size
+    ([1], 1, 1, 1, 64),
+    ([64], 1, 16, 1, 64),
+    ([63, 65, 0, 1, 128], 1, 16, 1, 64),
+    ([1000], 1, 32, 1, 64),
+    ([5, 700, 33], 2, 32, 1, 16),
+    ([130, 0, 2], 3, 5, 1, 32),                # fewer rows than new tokens; 15 columns
+    ([200, 97], 1, 64, 1, 128),
+    ([150, 31], 1, 128, 1, 64),                # more columns than one tile
+    ([300, 77, 500], 1, 24, 2, 32),            # two latent groups
+    ([90], 4, 32, 2, 16),
+    ([3000, 10, 2500], 1, 16, 1, 192),         # sequences that several CTAs share
+    ([260] * 40, 1, 16, 1, 64),
+    ([70], 70, 3, 1, 64),                      # many new tokens
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,Sq,H,G,ps", CASES)
+def test_decode_matches_64_bits(lens, Sq, H, G, ps, e4m3):
+    q, c, sc, table, kv_lens = make(lens, Sq, H, G, ps, e4m3, seed=60 + len(lens) + H)
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, lens, 192 ** -0.5)
+    ref.close(o, ro, mag, "o")
+    ref.lse_close(lse, rl, 32.0)
+    assert kda.kda_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("std", [0.0, 6.0])
+def test_decode_flat_and_peaked(std, e4m3):
+    q, c, sc, table, kv_lens = make([900, 350], 2, 16, 1, 64, e4m3, seed=70, std=std)
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, [900, 350], 192 ** -0.5)
+    # |q| |c| summed over a row: 576 * std * 3 or so, times the softmax scale
+    s_abs = 576 * 3 * max(std, 0.1) * 192 ** -0.5
+    ref.close(o, ro, mag * (1 + 2 ** 8 * math.expm1(576 * 2.0 ** -24 * s_abs)), "o")
+    ref.lse_close(lse, rl, max(32.0, s_abs))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_repeatable_captured_and_on_another_stream(e4m3):
+    lens = [1500, 3, 700]
+    q, c, sc, table, kv_lens = make(lens, 1, 32, 1, 64, e4m3, seed=71)
+    first = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    again = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first[0], again[0])
+    graph = torch.cuda.CUDAGraph()
+    fixed_q, fixed_lens = q.clone(), kv_lens.clone()
+    with torch.cuda.graph(graph):
+        cap = kda.kda_mla_decode(fixed_q, c, table, fixed_lens, cache_scale=sc)
+    for new in (lens, [1400, 0, 640], lens):
+        fixed_lens.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = kda.kda_mla_decode(q, c, table, fixed_lens.clone(), cache_scale=sc)
+        assert torch.equal(cap[0], want[0]) and torch.equal(cap[1], want[1])
+
+
+def test_two_decodes_at_once():
+    """Calls on two streams with a workspace each."""
+    a = make([2000, 90], 1, 16, 1, 64, False, seed=72)
+    b = make([100, 1700, 64], 1, 32, 1, 32, True, seed=73)
+    want = [kda.kda_mla_decode(x[0], x[1], x[3], x[4], cache_scale=x[2]) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(kda.kda_mla_decode(x[0], x[1], x[3], x[4], cache_scale=x[2]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
+
+
+def test_decode_records_bad_lengths_and_pages():
+    """Recorded in the status word; the other sequences' results stand."""
+    lens = [100, 40, 64]
+    q, c, sc, table, kv_lens = make(lens, 1, 16, 1, 64, False, seed=74)
+    good = kda.kda_mla_decode(q, c, table, kv_lens)
+    for bad_len in (-1, table.shape[1] * 64 + 1):
+        l2 = kv_lens.clone()
+        l2[1] = bad_len
+        o, _ = kda.kda_mla_decode(q, c, table, l2)
+        assert kda.kda_device_status() == 1
+        assert torch.equal(o[0], good[0][0]) and torch.equal(o[2], good[0][2])
+    for page in (-1, c.shape[0]):
+        t2 = table.clone()
+        t2[0, 1] = page
+        o, _ = kda.kda_mla_decode(q, c, t2, kv_lens)
+        assert kda.kda_device_status() == 1
+        assert torch.equal(o[1], good[0][1]) and torch.equal(o[2], good[0][2])
+
+
+APPENDS = [
+    # rows held, rows new, G, page size
+    ([0], [1], 1, 64),
+    ([63, 64, 65, 0, 10], [1, 1, 1, 0, 130], 1, 64),
+    ([5, 0, 31], [40, 100, 2], 2, 32),
+    ([15, 16, 100], [1, 17, 33], 1, 16),
+    ([100, 7], [300, 1], 2, 192),
+    ([i % 70 for i in range(300)], [i % 3 for i in range(300)], 1, 64),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("held,new,G,ps", APPENDS)
+def test_append_matches_the_definition(held, new, G, ps, e4m3):
+    """Codes, scales and untouched rows, bit for bit; magnitudes that make some scales grow."""
+    g = torch.Generator(device="cuda").manual_seed(80 + len(held))
+    table, pages = table_for([a + b for a, b in zip(held, new)], ps, g)
+    cu = [0]
+    for m in new:
+        cu.append(cu[-1] + m)
+    rows = torch.randn(cu[-1] + 3, G, 576, generator=g, device="cuda")
+    rows *= torch.exp2(torch.randint(-4, 5, (cu[-1] + 3, G, 1), generator=g, device="cuda").float())
+    rows = rows.to(torch.bfloat16)
+    if cu[-1] > 2:
+        rows[1] = 0.0
+    c = torch.randn(pages, ps, G, 576, generator=g, device="cuda").to(torch.bfloat16)
+    sc = None
+    if e4m3:
+        sc = torch.exp2(torch.randint(-9, -5, (pages, G), generator=g, device="cuda").float())
+        c = (c.float() / sc[:, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    held_t = torch.tensor(held, dtype=torch.int32, device="cuda")
+    want_c, want_s = c.cpu().clone(), None if sc is None else sc.cpu().clone()
+    ref.append(rows.cpu(), cu, held, table.cpu(), want_c, want_s)
+    kda.kda_mla_cache_append(rows, cu_t, held_t, table, c, cache_scale=sc)
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == 0
+    assert torch.equal(c.cpu().view(torch.uint8), want_c.view(torch.uint8))
+    if e4m3:
+        assert torch.equal(sc.cpu(), want_s)
+    # the same rows again change nothing
+    before = c.clone()
+    kda.kda_mla_cache_append(rows, cu_t, held_t, table, c, cache_scale=sc)
+    assert torch.equal(c.view(torch.uint8), before.view(torch.uint8))
+
+
+def test_append_extremes():
+    """All zeros, the largest and smallest numbers, and a NaN or an infinity, which make the
+    scale NaN and the attention over the page NaN."""
+    ps = 64
+    table = torch.arange(6, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    rows = torch.zeros(6, 1, 576, dtype=torch.bfloat16, device="cuda")
+    rows[1, 0, 3] = 3.3895313892515355e38
+    rows[2, 0, 5] = 1e-38
+    rows[3, 0, 7] = math.nan
+    rows[4, 0, 9] = -math.inf
+    rows[5, 0, :] = 448.0
+    c = torch.zeros(6, ps, 1, 576, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.full((6, 1), 5.0, device="cuda")
+    cu = torch.arange(7, dtype=torch.int32, device="cuda")
+    held = torch.zeros(6, dtype=torch.int32, device="cuda")
+    kda.kda_mla_cache_append(rows, cu, held, table, c, cache_scale=sc)
+    s = sc[:, 0].cpu().tolist()
+    assert s[0] == s[2] == 2.0 ** -100 and s[1] == 2.0 ** 120 and s[5] == 1.0
+    assert math.isnan(s[3]) and math.isnan(s[4])
+    q = torch.ones(6, 1, 16, 576, dtype=torch.bfloat16, device="cuda")
+    o, lse = kda.kda_mla_decode(q, c, table, held + 1, cache_scale=sc)
+    assert torch.isnan(o[3]).all() and torch.isnan(o[4]).all()
+    assert (o[0] == 0).all() and (o[5] == 448).all() and (o[2] == 0).all()
+    # behind a NaN page's rows the scale stays NaN
+    kda.kda_mla_cache_append(rows[:1].expand(6, -1, -1).contiguous(), cu, held + 1, table, c, cache_scale=sc)
+    assert math.isnan(float(sc[3, 0])) and float(sc[5, 0]) == 1.0
+
+
+def test_append_refuses_bad_tables():
+    ps = 64
+    g = torch.Generator(device="cuda").manual_seed(81)
+    rows = torch.randn(6, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 3, 6], dtype=torch.int32, device="cuda")
+    good = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for table, held, offs in (
+            (torch.tensor([[0], [2]], dtype=torch.int32, device="cuda"), zero, cu),      # no such page
+            (torch.tensor([[0], [-1]], dtype=torch.int32, device="cuda"), zero, cu),
+            (good, torch.tensor([0, 64], dtype=torch.int32, device="cuda"), cu),         # behind the table
+            (good, torch.tensor([0, -5], dtype=torch.int32, device="cuda"), cu)):
+        c = torch.zeros(2, ps, 1, 576, dtype=torch.bfloat16, device="cuda")
+        kda.kda_mla_cache_append(rows, offs, held, table, c)
+        assert kda.kda_device_status() == 1
+        assert torch.equal(c[0, :3], rows[:3]) and (c[1] == 0).all()
+    for bad in ([0, 4, 3], [0, 3, 7], [1, 3, 6]):
+        c = torch.zeros(2, ps, 1, 576, dtype=torch.bfloat16, device="cuda")
+        kda.kda_mla_cache_append(rows, torch.tensor(bad, dtype=torch.int32, device="cuda"), zero, good, c)
+        assert kda.kda_device_status() == 1
+        assert (c == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_prefill_append_decode_together(e4m3):
+    """A latent-attention layer as a hybrid model runs it: the prompt through the expanded form,
+    its latents into the cache, then tokens one at a time in the absorbed form.  Each token's
+    result equals attention over the cached rows in 64 bits, with the value projection behind
+    it; the prompt's last row equals a decode of the same token up to the projections' roundings."""
+    H, ps, lens, steps = 4, 32, [70, 33], 3
+    g = torch.Generator(device="cuda").manual_seed(90)
+    w_uk = (torch.randn(H, 128, 512, generator=g, device="cuda") / 512 ** 0.5).to(torch.bfloat16)
+    w_uv = (torch.randn(H, 128, 512, generator=g, device="cuda") / 512 ** 0.5).to(torch.bfloat16)
+    total = [n + steps for n in lens]
+    table, pages = table_for(total, ps, g)
+    cache = torch.zeros(pages, ps, 1, 576, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16, device="cuda")
+    sc = torch.zeros(pages, 1, device="cuda") if e4m3 else None
+    cu = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device="cuda")
+    lat = torch.randn(sum(lens), 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(sum(lens), H, 192, generator=g, device="cuda").to(torch.bfloat16)
+    up = lambda w: torch.einsum("td,hcd->thc", lat[:, 0, :512].float(), w.float())
+    kv = torch.cat([up(w_uk), up(w_uv)], -1).to(torch.bfloat16)
+    o, lse = kda.kda_mla_fwd(q, kv, lat[:, 0, 512:].contiguous(), cu)
+    kda.kda_mla_cache_append(lat, cu, torch.zeros(2, dtype=torch.int32, device="cuda"), table, cache, cache_scale=sc)
+    kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def absorbed(qt):  # [N, H, 192] -> [N, 1, H, 576]
+        return torch.cat([torch.einsum("nhc,hcd->nhd", qt[..., :128].float(), w_uk.float()), qt[..., 128:].float()],
+                         -1).to(torch.bfloat16)[:, None]
+
+    last = q[cu[1:].long() - 1]
+    od, _ = kda.kda_mla_decode(absorbed(last), cache, table, kv_lens, cache_scale=sc)
+    od = torch.einsum("nhd,hcd->nhc", od[:, 0].float(), w_uv.float())
+    want = o[cu[1:].long() - 1].float()
+    # both sides round q or k, v and o to bfloat16 (about 2^-8 each, averaged over the row); the
+    # 8-bit cache rounds every latent number by up to 2^-4
+    assert float((od - want).norm() / want.norm()) <= (0.08 if e4m3 else 0.02)
+    one = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    for _ in range(steps):
+        new = torch.randn(2, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+        qt = absorbed(torch.randn(2, H, 192, generator=g, device="cuda").to(torch.bfloat16))
+        kda.kda_mla_cache_append(new, one, kv_lens, table, cache, cache_scale=sc)
+        kv_lens = kv_lens + 1
+        od, ld = kda.kda_mla_decode(qt, cache, table, kv_lens, cache_scale=sc)
+        ro, rl, mag = ref.decode(qt, cache, sc, table, kv_lens.tolist(), 192 ** -0.5)
+        ref.close(od, ro, mag, "o")
+        ref.lse_close(ld, rl, 32.0)
+    assert kda.kda_device_status() == 0
