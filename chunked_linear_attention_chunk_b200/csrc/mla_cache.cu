@@ -73,7 +73,7 @@ __device__ __forceinline__ float scale_for(float amax)
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
 {
-    __shared__ int sh[36];
+    __shared__ int64_t sh[40];
     __shared__ float s_max[kThreads / 32];
     const int tid = threadIdx.x, ps = a.page_size;
     if (!offsets_ok<kThreads>(a.cu, a.N, a.T_new)) {
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
             return 0;
         if (len < 0)
             return 1;  // refused below
-        return (int)(((int64_t)len % ps + m + ps - 1) / ps);
+        return (len % ps + m - 1) / ps + 1;
     };
     Item it;
     if (!find_item<kThreads>(a.N, blockIdx.x, touched, it, sh))

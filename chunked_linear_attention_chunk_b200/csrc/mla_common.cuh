@@ -29,31 +29,48 @@ __device__ __forceinline__ bool offsets_ok(const int32_t *__restrict__ cu, int N
     return __syncthreads_or(bad) == 0;
 }
 
+// A sum over the CTA; all threads call it.  `sh` is 40 int64 of shared memory.
+template <int kThreads>
+__device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *sh)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+    if ((threadIdx.x & 31) == 0)
+        sh[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w)
+        total += sh[w];
+    __syncthreads();
+    return total;
+}
+
 // Work item x of the list that has count(0) items for sequence 0, then count(1) for sequence 1,
 // and so on: its sequence and its place among that sequence's items.  False past the end.  All
-// threads of the CTA call it; `sh` is 36 ints of shared memory.
+// threads of the CTA call it; `sh` is 40 int64 of shared memory.
 struct Item {
     int seq, k;
 };
 template <int kThreads, class Count>
-__device__ __forceinline__ bool find_item(int N, int64_t x, Count count, Item &it, int *sh)
+__device__ __forceinline__ bool find_item(int N, int64_t x, Count count, Item &it, int64_t *sh)
 {
     static_assert(kThreads % 32 == 0 && kThreads <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t base = 0;
     for (int s0 = 0; s0 < N; s0 += kThreads) {
         const int s = s0 + tid;
-        const int c = s < N ? count(s) : 0;
-        int inc = c;
+        const int64_t c = s < N ? count(s) : 0;
+        int64_t inc = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, d);
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
             inc += lane >= d ? y : 0;
         }
         if (lane == 31)
             sh[warp] = inc;
         __syncthreads();
-        int before = 0, total = 0;
+        int64_t before = 0, total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             before += w < warp ? sh[w] : 0;
             total += sh[w];
@@ -61,17 +78,25 @@ __device__ __forceinline__ bool find_item(int N, int64_t x, Count count, Item &i
         const int64_t rel = x - base - before - (inc - c);
         if (rel >= 0 && rel < c) {
             sh[33] = s;
-            sh[34] = (int)rel;
+            sh[34] = rel;
         }
         __syncthreads();
         base += total;
         if (x < base) {
-            it.seq = sh[33];
-            it.k = sh[34];
+            it.seq = (int)sh[33];
+            it.k = (int)sh[34];
             return true;
         }
     }
     return false;
+}
+
+// 2^x by the hardware's approximation (2 ulp; results below the normal range flush to 0).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 }  // namespace mla
