@@ -34,8 +34,9 @@ namespace {
 
 using namespace mla;
 
+constexpr int kConv = 8;  // warps that turn codes into bfloat16 rows
 template <bool kE4M3>
-constexpr int kThreads = kE4M3 ? 384 : 256;
+constexpr int kThreads = kE4M3 ? 256 + kConv * 32 : 256;
 constexpr int kTok = 64;                    // cached rows a tile
 constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 64 numbers, 128-byte swizzle
 constexpr uint32_t kPair = 2 * kBlk;        // 128 latent numbers: the M of one O^T product
@@ -53,6 +54,14 @@ struct DecArgs {
     float *part_o, *part_lse;  // [CTA][2][NC][512], [CTA][2][NC]
     int2 *meta;                // [unit][CT]: first share, 2 * shares + (the first starts inside its share)
     unsigned int *status;
+};
+
+// The cache as [block of 64 numbers][pool row][group][64], so that one copy brings a pair of
+// blocks (or the rope block) of up to 64 rows as the products read them; and q as [block][row][64].
+struct DecMaps {
+    CUtensorMap pair, rope, q;
+    int rows;    // pool rows a copy: min(page_size, 64)
+    int q_rows;  // rows of q a copy
 };
 
 // Tiles of a sequence; 0 for a length that is refused.
@@ -89,15 +98,15 @@ struct Pieces {
 
 template <int NC, bool kE4M3>
 struct DecSmem {
-    // pairs and rope blocks of bfloat16 rows held, and blocks of codes in flight
-    static constexpr int kRing = kE4M3 ? (NC == 64 ? 7 : 8) : (NC == 64 ? 8 : 10);
-    static constexpr int kRopes = kE4M3 ? (NC == 64 ? 1 : 2) : (NC == 64 ? 2 : 3);
-    static constexpr int kStage = kE4M3 ? (NC == 64 ? 6 : 10) : 1;
+    // pairs and rope blocks of bfloat16 rows held, and pairs of blocks of codes in flight
+    static constexpr int kRing = kE4M3 ? (NC == 64 ? 5 : 7) : (NC == 64 ? 8 : 10);
+    static constexpr int kRopes = kE4M3 ? 1 : (NC == 64 ? 2 : 3);
+    static constexpr int kStage = kE4M3 ? (NC == 64 ? 6 : 8) : 1;
     alignas(1024) unsigned char pair[kRing][kPair];
     alignas(1024) unsigned char rope[kRopes][kBlk];
     alignas(1024) unsigned char q[kDC / 64][NC * 128];
     alignas(1024) unsigned char p[kTok * NC * 2];
-    alignas(1024) unsigned char stage[kStage][kE4M3 ? kBlk / 2 : 16];
+    alignas(1024) unsigned char stage[kStage][kE4M3 ? kBlk : 16];
     float red[4][NC];  // per warp: column maxima, then column sums
     float fac[NC];     // per column: rescaling factor, then 1 / sum
     uint64_t full_pair[kRing], empty_pair[kRing], full_rope[kRopes], empty_rope[kRopes];
@@ -109,43 +118,18 @@ struct DecSmem {
     int first[3];      // n, g, t of its first tile
 };
 
-// Four e4m3 codes as bfloat16 pairs (exact).  A code's exponent and mantissa, moved to the top of
-// a bfloat16's mantissa and the foot of its exponent, are the value times 2^-120 (subnormals
-// included); the product with 2^120 is exact.  NaN codes are the caller's business.
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t &lo, uint32_t &hi)
+// Four e4m3 codes as bfloat16 pairs: exact, NaN codes stay NaN.
+__device__ __forceinline__ uint2 decode4(uint32_t w)
 {
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));
-    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
-    const __nv_bfloat162 u = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), up);
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), up);
-    lo = *reinterpret_cast<const uint32_t *>(&u);
-    hi = *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Sixteen codes to bfloat16; a NaN code (0x7f, 0xff) becomes NaN.
-__device__ __forceinline__ void decode16(uint4 c, uint4 &lo, uint4 &hi)
-{
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8], nan = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        decode4(w[i], r[2 * i], r[2 * i + 1]);
-        nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-    }
-    if (nan & 0x80808080u) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (((w[i >> 2] >> (i & 3) * 8) & 0x7f) == 0x7f)
-                r[i >> 1] |= 0x7fffu << (i & 1) * 16;
-    }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+    return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
 }
 
 template <int NC, bool kE4M3>
 __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
-    mla_decode_kernel(const __grid_constant__ CUtensorMap cache_map, DecArgs a, int box_rows)
+    mla_decode_kernel(const __grid_constant__ DecMaps maps, DecArgs a)
 {
     extern __shared__ unsigned char raw[];
     using SM = DecSmem<NC, kE4M3>;
@@ -157,16 +141,16 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 
     if (tid == 0) {
         for (int i = 0; i < SM::kRing; ++i) {
-            mbar_init(&sm.full_pair[i], kE4M3 ? 128 : 1);
+            mbar_init(&sm.full_pair[i], kE4M3 ? kConv * 32 : 1);
             mbar_init(&sm.empty_pair[i], 1);
         }
         for (int i = 0; i < SM::kRopes; ++i) {
-            mbar_init(&sm.full_rope[i], kE4M3 ? 128 : 1);
+            mbar_init(&sm.full_rope[i], kE4M3 ? kConv * 32 : 1);
             mbar_init(&sm.empty_rope[i], 1);
         }
         for (int i = 0; i < SM::kStage; ++i) {
             mbar_init(&sm.full_stage[i], 1);
-            mbar_init(&sm.empty_stage[i], 4);
+            mbar_init(&sm.empty_stage[i], kConv);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
@@ -174,7 +158,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
         mbar_init(&sm.p_full, 128);
         mbar_init(&sm.pv_done, 1);
-        mbar_init(&sm.q_full, 32);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
         fence_mbar_init_cluster();
     }
@@ -226,202 +210,224 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 
     if (warp == 4) {
         // ---------------- copies
-        const int ppt = kTok / box_rows;  // boxes a block
+        const int ppt = kTok / maps.rows;  // copies a block
         int batch_n = -1, batch_0 = 0, ids = 0;
-        uint32_t np = 0, nr = 0;  // pairs and ropes so far
+        Ring<SM::kRing> rp;
+        Ring<SM::kRopes> rr;
+        Ring<SM::kStage> rst;
         for (; w.take > 0 && !wait.dead; w.next(a)) {
             const int len = a.kv_lens[w.n], pages = (len + a.page_size - 1) / a.page_size;
             const int32_t *row = a.block_table + (int64_t)w.n * a.max_pages;
+            int e = w.t * kTok / a.page_size, off = w.t * kTok % a.page_size;  // page entry, slot in it
             for (int t = w.t; t < w.t + w.take && !wait.dead; ++t) {
-                // the token rows of the tile's boxes (at most four), from the table 32 entries at a time
+                // the pool rows of the tile's copies, from the table 32 entries at a time
                 int at[4], live = 0;
-                for (int b = 0; b < ppt; ++b) {
-                    const int p0 = t * kTok + b * box_rows;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
                     at[b] = -1;
-                    if (p0 >= len)
-                        continue;
-                    const int e = p0 / a.page_size;
-                    if (w.n != batch_n || e < batch_0 || e >= batch_0 + 32) {
-                        batch_n = w.n;
-                        batch_0 = e;
-                        ids = e + lane < pages ? row[e + lane] : 0;
-                    }
-                    const int page = __shfl_sync(0xffffffffu, ids, e - batch_0);
-                    if (page < 0 || page >= a.num_pages) {
-                        if (lane == 0)
+                    if (b < ppt && e < pages) {
+                        if (w.n != batch_n || e < batch_0 || e >= batch_0 + 32) {
+                            batch_n = w.n;
+                            batch_0 = e;
+                            ids = e + lane < pages ? row[e + lane] : 0;
+                        }
+                        const int page = __shfl_sync(0xffffffffu, ids, e - batch_0);
+                        if (page >= 0 && page < a.num_pages) {
+                            at[b] = page * a.page_size + off;
+                            ++live;
+                        } else if (lane == 0) {
                             report_device_error(a.status, KDA_ERR_INVALID_ARG);
-                        continue;
+                        }
+                        off += maps.rows;
+                        if (off >= a.page_size) {
+                            off = 0;
+                            ++e;
+                        }
                     }
-                    at[b] = page * a.page_size + p0 % a.page_size;
-                    ++live;
                 }
-                if (lane == 0) {
-                    // 64 numbers of each live box's rows
-                    auto block = [&](unsigned char *dst, int x, uint64_t *bar) {
-                        for (int b = 0; b < ppt; ++b)
+                constexpr uint32_t kRow = kE4M3 ? 64 : 128;  // bytes of a block's row
+                const uint32_t bytes = (uint32_t)(live * maps.rows) * kRow;
+                // n blocks from `block` on; pages of 64 rows and more take one copy
+                auto copy = [&](unsigned char *dst, int block, int n, uint64_t *bar) {
+                    mbar_arrive_expect_tx(bar, n * bytes);
+                    if (ppt == 1) {
+                        if (at[0] >= 0)
+                            tma_load_4d(dst, n == 2 ? &maps.pair : &maps.rope, 0, w.g, at[0], block, bar);
+                        return;
+                    }
+                    for (int i = 0; i < n; ++i)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
                             if (at[b] >= 0)
-                                tma_load_3d(dst + b * box_rows * (kE4M3 ? 64 : 128), &cache_map, x, w.g, at[b], bar);
-                    };
-                    const uint32_t bytes = (uint32_t)live * box_rows * (kE4M3 ? 64u : 128u);
-                    if constexpr (kE4M3) {
-                        for (int j = 0; j < kDC / 64; ++j, ++np) {
-                            const uint32_t s = np % SM::kStage;
-                            if (np >= SM::kStage)
-                                wait(&sm.empty_stage[s], (np / SM::kStage - 1) & 1);
-                            if (wait.dead)
-                                break;
-                            mbar_arrive_expect_tx(&sm.full_stage[s], bytes);
-                            block(sm.stage[s], j == 0 ? kDL : (j - 1) * 64, &sm.full_stage[s]);
-                        }
-                    } else {
-                        const uint32_t r = nr % SM::kRopes;
-                        if (nr >= SM::kRopes)
-                            wait(&sm.empty_rope[r], (nr / SM::kRopes - 1) & 1);
-                        ++nr;
-                        if (!wait.dead) {
-                            mbar_arrive_expect_tx(&sm.full_rope[r], bytes);
-                            block(sm.rope[r], kDL, &sm.full_rope[r]);
-                        }
-                        for (int j = 0; j < kPairs; ++j, ++np) {
-                            const uint32_t s = np % SM::kRing;
-                            if (np >= SM::kRing)
-                                wait(&sm.empty_pair[s], (np / SM::kRing - 1) & 1);
-                            if (wait.dead)
-                                break;
-                            mbar_arrive_expect_tx(&sm.full_pair[s], 2 * bytes);
-                            block(sm.pair[s], j * 128, &sm.full_pair[s]);
-                            block(sm.pair[s] + kBlk, j * 128 + 64, &sm.full_pair[s]);
-                        }
+                                tma_load_4d(dst + i * kTok * kRow + b * maps.rows * kRow, &maps.rope, 0, w.g, at[b],
+                                            block + i, bar);
+                };
+                if constexpr (kE4M3) {
+#pragma unroll
+                    for (int j = 0; j <= kPairs; ++j, rst.step()) {
+                        if (rst.round > 0)
+                            wait(&sm.empty_stage[rst.slot], (rst.round - 1) & 1);
+                        if (!wait.dead && elect())
+                            copy(sm.stage[rst.slot], j == 0 ? 2 * kPairs : 2 * (j - 1), j == 0 ? 1 : 2,
+                                 &sm.full_stage[rst.slot]);
+                    }
+                } else {
+                    if (rr.round > 0)
+                        wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
+                    if (!wait.dead && elect())
+                        copy(sm.rope[rr.slot], 2 * kPairs, 1, &sm.full_rope[rr.slot]);
+                    rr.step();
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j, rp.step()) {
+                        if (rp.round > 0)
+                            wait(&sm.empty_pair[rp.slot], (rp.round - 1) & 1);
+                        if (!wait.dead && elect())
+                            copy(sm.pair[rp.slot], 2 * j, 2, &sm.full_pair[rp.slot]);
                     }
                 }
-                wait.dead = __shfl_sync(0xffffffffu, (int)wait.dead, 0) != 0;
+                wait.dead = __any_sync(0xffffffffu, wait.dead);
             }
         }
     } else if (warp == 5) {
         // ---------------- S^T = C Q^T, block by block as the tile arrives (rope first)
-        if (lane == 0) {
-            const uint32_t id = tc::idesc_bf16(64, NC, false, false);
-            uint32_t np = 0, nr = 0, nt = 0, nq = 0;
-            for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
-                wait(&sm.q_full, nq & 1);
-                for (int t = 0; t < w.take && !wait.dead; ++t, ++nt) {
-                    const uint32_t sb = nt & 1;
-                    if (nt >= 2)
-                        wait(&sm.s_empty[sb], (nt / 2 - 1) & 1);
-                    tc::fence_after_sync();
-                    const uint32_t d = tmem + sb * NC;
-                    auto block = [&](const unsigned char *c, const unsigned char *qb, bool first) {
+        constexpr uint32_t id = tc::idesc_bf16(64, NC, false, false);
+        const Desc rope(smem_u32(sm.rope[0]), 16, 1024, tc::kSw128), pair(smem_u32(sm.pair[0]), 16, 1024, tc::kSw128),
+            qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128);
+        Ring<SM::kRing> rp;
+        Ring<SM::kRopes> rr;
+        Ring<2> rs;
+        uint32_t nq = 0;
+        for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
+            wait(&sm.q_full, nq & 1);
+            for (int t = 0; t < w.take && !wait.dead; ++t, rs.step()) {
+                if (rs.round > 0)
+                    wait(&sm.s_empty[rs.slot], (rs.round - 1) & 1);
+                const uint32_t d = tmem + rs.slot * NC;
+                wait(&sm.full_rope[rr.slot], rr.round & 1);
+                tc::fence_after_sync();
+                if (elect()) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc::mma_bf16(d, tc::smem_desc(smem_u32(c) + ks * 32, 16, 1024, tc::kSw128),
-                                         tc::smem_desc(smem_u32(qb) + ks * 32, 16, 1024, tc::kSw128), id,
-                                         first && ks == 0 ? 0u : 1u);
-                    };
-                    const uint32_t rs = nr % SM::kRopes;
-                    wait(&sm.full_rope[rs], (nr / SM::kRopes) & 1);
-                    block(sm.rope[rs], sm.q[kDC / 64 - 1], true);
-                    tc::commit(&sm.empty_rope[rs]);
-                    ++nr;
-                    for (int j = 0; j < kPairs; ++j, ++np) {
-                        const uint32_t s = np % SM::kRing;
-                        wait(&sm.full_pair[s], (np / SM::kRing) & 1);
-                        block(sm.pair[s], sm.q[2 * j], false);
-                        block(sm.pair[s] + kBlk, sm.q[2 * j + 1], false);
-                    }
-                    tc::commit(&sm.s_full[sb]);
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc::mma_bf16(d, rope.at(rr.slot * kBlk + ks * 32), qd.at((kDC / 64 - 1) * NC * 128 + ks * 32), id,
+                                     ks > 0 ? 1u : 0u);
+                    tc::commit(&sm.empty_rope[rr.slot]);
                 }
-                tc::commit(&sm.q_empty);
+                rr.step();
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j, rp.step()) {
+                    wait(&sm.full_pair[rp.slot], rp.round & 1);
+                    tc::fence_after_sync();
+                    if (elect()) {
+                        const uint32_t c0 = rp.slot * kPair;
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc::mma_bf16(d, pair.at(c0 + (ks >> 2) * kBlk + (ks & 3) * 32),
+                                         qd.at((2 * j + (ks >> 2)) * NC * 128 + (ks & 3) * 32), id, 1u);
+                    }
+                }
+                if (elect())
+                    tc::commit(&sm.s_full[rs.slot]);
             }
+            if (elect())
+                tc::commit(&sm.q_empty);
         }
-        __syncwarp();
     } else if (warp == 6) {
         // ---------------- O^T += C^T P^T, 128 latent numbers at a time
-        if (lane == 0) {
-            const uint32_t id = tc::idesc_bf16(128, NC, true, true);
-            uint32_t np = 0, nt = 0;
-            for (; w.take > 0 && !wait.dead; w.next(a))
-                for (int t = 0; t < w.take && !wait.dead; ++t, ++nt) {
-                    wait(&sm.p_full, nt & 1);
-                    tc::fence_after_sync();
-                    for (int j = 0; j < kPairs; ++j, ++np) {
-                        const uint32_t s = np % SM::kRing;
+        constexpr uint32_t id = tc::idesc_bf16(128, NC, true, true);
+        const Desc pair(smem_u32(sm.pair[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p));
+        Ring<SM::kRing> rp;
+        uint32_t nt = 0;
+        for (; w.take > 0 && !wait.dead; w.next(a))
+            for (int t = 0; t < w.take && !wait.dead; ++t, ++nt) {
+                wait(&sm.p_full, nt & 1);
+                tc::fence_after_sync();
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j, rp.step())
+                    if (elect()) {
+                        const uint32_t c0 = rp.slot * kPair;
 #pragma unroll
                         for (int ks = 0; ks < kTok / 16; ++ks)
-                            tc::mma_bf16(tmem + (2 + j) * NC,
-                                         tc::smem_desc(smem_u32(sm.pair[s]) + ks * 2048, kBlk, 1024, tc::kSw128),
-                                         p_desc<NC>(smem_u32(sm.p), ks), id, t > 0 || ks > 0 ? 1u : 0u);
-                        tc::commit(&sm.empty_pair[s]);
+                            tc::mma_bf16(tmem + (2 + j) * NC, pair.at(c0 + ks * 2048), pd.at(ks * kPStep<NC>), id,
+                                         t > 0 || ks > 0 ? 1u : 0u);
+                        tc::commit(&sm.empty_pair[rp.slot]);
+                        if (j == kPairs - 1)
+                            tc::commit(&sm.pv_done);
                     }
-                    tc::commit(&sm.pv_done);
-                }
-        }
-        __syncwarp();
+            }
     } else if (warp == 7) {
-        // ---------------- Q of each piece: NC columns (token, head) x 576, K-major blocks of 64
+        // ---------------- Q of each piece: NC columns (token, head) x 576, K-major blocks of 64.
+        // Columns behind the last hold other rows of q or nothing; they stay columns of their own.
         uint32_t nq = 0;
         for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
             if (nq > 0)
                 wait(&sm.q_empty, (nq - 1) & 1);
-            for (int c = 0; c < NC; ++c) {
-                const int cg = ct * NC + c;
-                const bool live = cg < cols;
-                const int64_t r = live ? ((int64_t)w.n * a.Sq + cg / Hg) * a.H + w.g * Hg + cg % Hg : 0;
-                const __nv_bfloat16 *src = a.q + r * kDC;
-                for (int v = lane; v < kDC / 8; v += 32)
-                    cp_async_16_zfill(sm.q[v >> 3] + c * 128 + (((v & 7) ^ (c & 7)) << 4), src + v * 8, live);
+            if (wait.dead)
+                break;
+            const int left = cols - ct * NC;
+            if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
+                if (elect()) {
+                    mbar_arrive_expect_tx(&sm.q_full, kDC / 64 * NC * 128);
+                    tma_load_3d(sm.q[0], &maps.q, 0, w.n * cols + ct * NC, 0, &sm.q_full);
+                }
+            } else {
+                const int n = (min(left, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
+                if (elect())
+                    mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n * maps.q_rows) * kDC * 2);
+                __syncwarp();
+                for (int i = lane; i < n * (kDC / 64); i += 32) {
+                    const int c = i / (kDC / 64) * maps.q_rows, blk = i % (kDC / 64), cg = ct * NC + c;
+                    const int r = (w.n * a.Sq + cg / Hg) * a.H + w.g * Hg + cg % Hg;
+                    tma_load_3d(sm.q[blk] + c * 128, &maps.q, 0, r, blk, &sm.q_full);
+                }
+                __syncwarp();
             }
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            mbar_arrive(&sm.q_full);
         }
     } else if (kE4M3 && warp >= 8) {
         // ---------------- codes to bfloat16 rows: 8 rows x 4 vectors of 16 codes a warp, so that
         // both the swizzled reads and the swizzled writes touch every bank once
+        static_assert(kConv * 8 == kTok, "one pass of the warps covers a block's rows");
         const int chunk = lane >> 3;
-        uint32_t nb = 0, np = 0, nr = 0;
+        Ring<SM::kRing> rp;
+        Ring<SM::kRopes> rr;
+        Ring<SM::kStage> rst;
         for (; w.take > 0 && !wait.dead; w.next(a)) {
             const int len = a.kv_lens[w.n];
             for (int t = w.t; t < w.t + w.take && !wait.dead; ++t) {
                 const int rows = len - t * kTok;
-                for (int j = 0; j < kDC / 64; ++j, ++nb) {
-                    const uint32_t st = nb % SM::kStage;
-                    unsigned char *dst;
-                    uint64_t *full;
-                    if (j == 0) {
-                        const uint32_t r = nr % SM::kRopes;
-                        if (nr >= SM::kRopes)
-                            wait(&sm.empty_rope[r], (nr / SM::kRopes - 1) & 1);
-                        dst = sm.rope[r];
-                        full = &sm.full_rope[r];
-                        ++nr;
-                    } else {
-                        const uint32_t s = np % SM::kRing;
-                        if (np >= SM::kRing)
-                            wait(&sm.empty_pair[s], (np / SM::kRing - 1) & 1);
-                        dst = sm.pair[s] + (j & 1 ? 0 : kBlk);
-                        full = &sm.full_pair[s];
-                        np += (j & 1) ^ 1;
-                    }
-                    wait(&sm.full_stage[st], (nb / SM::kStage) & 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = (i * 4 + warp - 8) * 8 + (lane & 7);
-                        const uint4 c = *reinterpret_cast<const uint4 *>(sm.stage[st] + row * 64 +
-                                                                         ((chunk ^ ((row >> 1) & 3)) << 4));
-                        uint4 lo, hi;
-                        decode16(c, lo, hi);
+                for (int j = 0; j <= kPairs; ++j, rst.step()) {  // the rope block, then the pairs
+                    unsigned char *dst = j == 0 ? sm.rope[rr.slot] : sm.pair[rp.slot];
+                    if (j == 0 && rr.round > 0)
+                        wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
+                    if (j > 0 && rp.round > 0)
+                        wait(&sm.empty_pair[rp.slot], (rp.round - 1) & 1);
+                    wait(&sm.full_stage[rst.slot], rst.round & 1);
+                    uint4 c[2];
+#pragma unroll
+                    for (int i = 0; i < (j == 0 ? 1 : 2); ++i) {
+                        const int row = (warp - 8) * 8 + (lane & 7);
+                        c[i] = *reinterpret_cast<const uint4 *>(sm.stage[rst.slot] + i * kBlk / 2 + row * 64 +
+                                                                ((chunk ^ ((row >> 1) & 3)) << 4));
                         if (row >= rows)  // behind the sequence's end: anything may be there
-                            lo = hi = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(dst + row * 128 + (((2 * chunk) ^ (row & 7)) << 4)) = lo;
-                        *reinterpret_cast<uint4 *>(dst + row * 128 + (((2 * chunk + 1) ^ (row & 7)) << 4)) = hi;
+                            c[i] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < (j == 0 ? 1 : 2); ++i) {
+                        const int row = (warp - 8) * 8 + (lane & 7);
+                        const uint2 x = decode4(c[i].x), y = decode4(c[i].y), z = decode4(c[i].z), u = decode4(c[i].w);
+                        unsigned char *p = dst + i * kBlk + row * 128;
+                        *reinterpret_cast<uint4 *>(p + (((2 * chunk) ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+                        *reinterpret_cast<uint4 *>(p + (((2 * chunk + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, u.x, u.y);
                     }
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(&sm.empty_stage[st]);
+                        mbar_arrive(&sm.empty_stage[rst.slot]);
                     fence_proxy_async_smem();
-                    if (!(j & 1))  // the rope block, or a pair's second block
-                        mbar_arrive(full);
+                    mbar_arrive(j == 0 ? &sm.full_rope[rr.slot] : &sm.full_pair[rp.slot]);
+                    if (j == 0)
+                        rr.step();
+                    else
+                        rp.step();
                 }
             }
         }
@@ -435,8 +441,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             const int len = a.kv_lens[w.n];
             float m[2 * J], l[2 * J];
 #pragma unroll
-            for (int i = 0; i < 2 * J; ++i)
-                m[i] = -INFINITY, l[i] = 0.0f;
+            for (int i = 0; i < 2 * J; ++i) {
+                // columns behind the last: weights 0, and no say in when to rescale
+                m[i] = ct * NC + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1) < cols ? -INFINITY : INFINITY;
+                l[i] = 0.0f;
+            }
             for (int t = w.t; t < w.t + w.take; ++t, ++nt, np += kPairs) {
                 const uint32_t sb = nt & 1;
                 float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
@@ -676,7 +685,7 @@ DecPlan plan(int N, int Sq, int H, int G)
 }
 
 template <int NC, bool kE4M3>
-cudaError_t launch_nc(const CUtensorMap &map, const DecArgs &a, int box_rows, cudaStream_t s)
+cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
 {
     const size_t smem = sizeof(DecSmem<NC, kE4M3>) + 1024;
     static_assert(sizeof(DecSmem<NC, kE4M3>) + 1024 <= 232448, "shared memory of one CTA");
@@ -684,7 +693,14 @@ cudaError_t launch_nc(const CUtensorMap &map, const DecArgs &a, int box_rows, cu
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    kernel<<<a.shares * a.CT, kThreads<kE4M3>, smem, s>>>(map, a, box_rows);
+    // q: runs of columns that are consecutive rows
+    const int Hg = a.H / a.G;
+    maps.q_rows = a.G == 1 ? NC : Hg % 8 == 0 ? 8 : 1;
+    const int64_t extent[3] = {64, (int64_t)a.N * a.Sq * a.H, kDC / 64}, stride[2] = {kDC * 2, 128};
+    const int box[3] = {64, maps.q_rows, maps.q_rows == NC ? kDC / 64 : 1};
+    if ((e = make_map(&maps.q, a.q, 2, 3, extent, stride, box)) != cudaSuccess)
+        return e;
+    kernel<<<a.shares * a.CT, kThreads<kE4M3>, smem, s>>>(maps, a);
     mla_decode_join_kernel<NC><<<dim3(a.N * a.G * a.CT, NC / 8), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
@@ -706,18 +722,20 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
               reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int2 *>(ws), device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;
-    const int box_rows = page_size < kTok ? page_size : kTok;
-    // [576 numbers][G groups][token rows of the pool], boxes of 64 numbers of one group's rows
-    CUtensorMap map;
-    const int64_t rows = (int64_t)num_pages * page_size;
-    const int es = e4m3 ? 1 : 2;
-    const cudaError_t e =
-        make_map_3d(&map, cache, es, kDC, G, rows, (int64_t)kDC * es, (int64_t)G * kDC * es, 64, 1, box_rows);
+    DecMaps maps;
+    maps.rows = page_size < kTok ? page_size : kTok;
+    const int64_t es = e4m3 ? 1 : 2;
+    const int64_t extent[4] = {64, G, (int64_t)num_pages * page_size, kDC / 64};
+    const int64_t stride[3] = {kDC * es, G * kDC * es, 64 * es};
+    const int pair_box[4] = {64, 1, maps.rows, 2}, rope_box[4] = {64, 1, maps.rows, 1};
+    cudaError_t e = make_map(&maps.pair, cache, (int)es, 4, extent, stride, pair_box);
+    if (e == cudaSuccess)
+        e = make_map(&maps.rope, cache, (int)es, 4, extent, stride, rope_box);
     if (e != cudaSuccess)
         return e;
     if (e4m3)
-        return p.nc == 32 ? launch_nc<32, true>(map, a, box_rows, s) : launch_nc<64, true>(map, a, box_rows, s);
-    return p.nc == 32 ? launch_nc<32, false>(map, a, box_rows, s) : launch_nc<64, false>(map, a, box_rows, s);
+        return p.nc == 32 ? launch_nc<32, true>(maps, a, s) : launch_nc<64, true>(maps, a, s);
+    return p.nc == 32 ? launch_nc<32, false>(maps, a, s) : launch_nc<64, false>(maps, a, s);
 }
 
 }  // namespace kda
