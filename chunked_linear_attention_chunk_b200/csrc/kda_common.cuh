@@ -240,6 +240,15 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
 // Tiled tensor copies (TMA) of one box of a tensor map in this GPU's memory into this CTA's
 // shared memory, completing on `bar` (no multicast).  Coordinates are in elements, innermost
 // first; the innermost one times the element size is a multiple of 16 bytes at every call.
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *tm, int x, int y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, int x, int y, int z, uint64_t *bar)
 {
     asm volatile(

@@ -1,9 +1,23 @@
 // mla_fwd.cu -- expanded latent attention over packed sequences, forward.
 //
 //   s_ij = scale (q_i . [k_j, k_rope_j]),  o_i = sum_j e^{s_ij - lse_i} v_j
-// with the running maximum and sum of the softmax in float32.  One warp per (query, head): its
-// lanes hold the query row, walk the visible keys and keep o in registers.
+// with the running maximum and sum of the softmax in float32, in base 2 (scale log2(e) is folded
+// into the exponent's multiply-add).  Bound by the tensor cores: 640 flops a (query, key) pair and
+// head against 2 x 256 B of K and V a key that 256 queries share.
+//
+// One CTA takes 256 queries of one head as two tiles of 128, so that one tile's softmax runs
+// while the tensor cores work for the other, and walks the keys 96 at a time:
+//   S = Q K^T        (M = 128, N = 96, K = 192; K and the heads' shared k_rope side by side)
+//   O += P V         (M = 128, N = 128, K = 96; P in tensor memory, V read MN-major)
+// 96 keys is the widest tile whose K and V double-buffer beside 96 KB of Q in shared memory (N =
+// 128 would leave V one stage); a 128 x 96 x 16 product takes about 58 cycles against 48 ideal.
+// Tensor memory: two S tiles (P overwrites its first half), two O tiles.
+//
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1, one row a thread, no exchange between threads; O is
+// rescaled only when a row's maximum grows by more than 2^8 (float32 sums and a bfloat16 weight
+// hold as well); 8 copies (TMA); 9 issues the products.
 #include "mla_common.cuh"
+#include "mla_tc.cuh"
 
 namespace kda {
 
@@ -11,58 +25,291 @@ namespace {
 
 using namespace mla;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;
+constexpr int kRows = 128;               // queries a tile
+constexpr int kTiles = 2;                // tiles a CTA
+constexpr int kKeys = 96;                // keys a step
+constexpr uint32_t kQBlk = kRows * 128;  // 64 numbers of 128 rows
+constexpr uint32_t kKBlk = kKeys * 128;
+constexpr float kGrow = 8.0f;            // log2 by which a maximum may grow without rescaling
 
-__global__ void __launch_bounds__(kThreads)
-    mla_fwd_kernel(int N, const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int Tq, int Tk, int H,
-                   bool causal, float scale, const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ kv,
-                   const __nv_bfloat16 *__restrict__ kr, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
-                   unsigned int *status)
+struct FwdArgs {
+    int N, Tq, Tk, H;
+    bool causal;
+    float scale_log2;
+    const int32_t *cu_q, *cu_k;
+    __nv_bfloat16 *o;
+    float *lse;
+    unsigned int *status;
+};
+
+// q, kv and k_rope as [block of 64 numbers][head][row][64]; a box is all blocks of an operand.
+struct FwdMaps {
+    CUtensorMap q, kv, kr;
+};
+
+struct FwdSmem {
+    alignas(1024) unsigned char q[kTiles][3 * kQBlk];
+    alignas(1024) unsigned char k[2][3 * kKBlk];
+    alignas(1024) unsigned char v[2][2 * kKBlk];
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_tail;
+    uint64_t s_full[kTiles], p_full[kTiles], pv_done[kTiles];
+    uint32_t tmem_slot;
+    int64_t find[40];
+};
+
+// Keys [0, last] are visible to query i of a sequence.
+__device__ __forceinline__ int last_key(int i, int lq, int lk, bool causal)
 {
-    const bool okq = offsets_ok<kThreads>(cu_q, N, Tq), okk = offsets_ok<kThreads>(cu_k, N, Tk);
+    return causal ? min(lk - 1, i + lk - lq) : lk - 1;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_fwd_kernel(const __grid_constant__ FwdMaps maps, FwdArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    FwdSmem &sm = *reinterpret_cast<FwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % a.H;
+    const bool okq = offsets_ok<kThreads>(a.cu_q, a.N, a.Tq), okk = offsets_ok<kThreads>(a.cu_k, a.N, a.Tk);
     if (!okq || !okk) {
-        if (threadIdx.x == 0)
-            report_device_error(status, KDA_ERR_INVALID_ARG);
+        if (tid == 0)
+            report_device_error(a.status, KDA_ERR_INVALID_ARG);
         return;
     }
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int64_t row = unit / H;
-    const int h = (int)(unit % H);
-    if (row >= cu_q[N])
+    Item it;
+    if (!find_item<kThreads>(
+            a.N, blockIdx.x / a.H,
+            [&](int n) { return (a.cu_q[n + 1] - a.cu_q[n] + kTiles * kRows - 1) / (kTiles * kRows); }, it, sm.find))
         return;
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_q[mid] <= row)
-            lo = mid;
-        else
-            hi = mid;
+    const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
+    // with a causal mask the last queries see the most keys: they go first
+    const int i0 = ((lq + kTiles * kRows - 1) / (kTiles * kRows) - 1 - it.k) * kTiles * kRows;
+    int steps[kTiles], n_steps = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int first = i0 + t * kRows, last = min(lq, first + kRows) - 1;
+        steps[t] = first < lq ? max(0, last_key(last, lq, lk, a.causal) + kKeys) / kKeys : 0;
+        n_steps = max(n_steps, steps[t]);
     }
-    const int lq = cu_q[lo + 1] - cu_q[lo], lk = cu_k[lo + 1] - cu_k[lo], i = (int)(row - cu_q[lo]);
-    const int last = causal ? min(lk, max(0, i + lk - lq + 1)) : lk;
-    float qf[6], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.0f;
-    for (int c = 0; c < 6; ++c)
-        qf[c] = __bfloat162float(q[(row * H + h) * kDQ + c * 32 + lane]) * scale;
-    for (int j = 0; j < last; ++j) {
-        const int64_t t = cu_k[lo] + j;
-        const __nv_bfloat16 *kvr = kv + (t * H + h) * kDKV;
-        float s = 0.0f;
-        for (int c = 0; c < 4; ++c)
-            s += qf[c] * __bfloat162float(kvr[c * 32 + lane]);
-        for (int c = 0; c < 2; ++c)
-            s += qf[4 + c] * __bfloat162float(kr[t * kDR + c * 32 + lane]);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), r = expf(m - mn), p = expf(s - mn);
-        l = l * r + p;
-        m = mn;
-        for (int c = 0; c < 4; ++c)
-            acc[c] = acc[c] * r + p * __bfloat162float(kvr[kDN + c * 32 + lane]);
+
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.v_tail, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], kRows);
+            mbar_init(&sm.pv_done[i], 1);
+        }
+        fence_mbar_init_cluster();
     }
-    for (int c = 0; c < 4; ++c)
-        o[(row * H + h) * kDV + c * 32 + lane] = __float2bfloat16(last > 0 ? acc[c] / l : 0.0f);
-    if (lse && lane == 0)
-        lse[row * H + h] = last > 0 ? m + logf(l) : -INFINITY;
+    if (warp == 8)
+        tc::tmem_alloc(&sm.tmem_slot, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem_slot;
+    Waits wait{a.status, false};
+
+    if (warp == 8) {
+        // ---------------- copies
+        if (n_steps > 0) {
+            if (elect()) {
+                mbar_arrive_expect_tx(&sm.q_full, kTiles * 3 * kQBlk);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+                    tma_load_4d(sm.q[t], &maps.q, 0, q0 + i0 + t * kRows, h, 0, &sm.q_full);
+            }
+            for (int j = 0; j < n_steps && !wait.dead; ++j) {
+                const int s = j & 1, key = k0 + j * kKeys, live = lk - j * kKeys;
+                if (j >= 2)
+                    wait(&sm.k_empty[s], (j / 2 - 1) & 1);
+                if (!wait.dead && elect()) {
+                    mbar_arrive_expect_tx(&sm.k_full[s], 3 * kKBlk);
+                    tma_load_4d(sm.k[s], &maps.kv, 0, key, h, 0, &sm.k_full[s]);
+                    tma_load_2d(sm.k[s] + 2 * kKBlk, &maps.kr, 0, key, &sm.k_full[s]);
+                }
+                if (j >= 2)
+                    wait(&sm.v_empty[s], (j / 2 - 1) & 1);
+                uint64_t *bar = live < kKeys ? &sm.v_tail : &sm.v_full[s];
+                if (!wait.dead && elect()) {
+                    mbar_arrive_expect_tx(bar, 2 * kKBlk);
+                    tma_load_4d(sm.v[s], &maps.kv, 0, key, h, 2, bar);
+                }
+                if (live < kKeys) {
+                    // rows behind the sequence's end may hold anything (0 * NaN): zeros for O
+                    wait(&sm.v_tail, 0);
+                    for (int i = lane; i < (kKeys - live) * 16; i += 32)
+                        *reinterpret_cast<uint4 *>(sm.v[s] + (i & 8 ? kKBlk : 0) + (live + i / 16) * 128 + (i & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect())
+                        mbar_arrive(&sm.v_full[s]);
+                }
+            }
+        }
+    } else if (warp == 9) {
+        // ---------------- products
+        constexpr uint32_t id_s = tc::idesc_bf16(kRows, kKeys, false, false), id_o = tc::idesc_bf16(kRows, kDV, false, true);
+        const Desc qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128), kd(smem_u32(sm.k[0]), 16, 1024, tc::kSw128),
+            vd(smem_u32(sm.v[0]), kKBlk, 1024, tc::kSw128);
+        auto scores = [&](int t, int j) {
+            if (elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kDQ / 16; ++ks)
+                    tc::mma_bf16(tmem + t * 128, qd.at(t * 3 * kQBlk + (ks >> 2) * kQBlk + (ks & 3) * 32),
+                                 kd.at((j & 1) * 3 * kKBlk + (ks >> 2) * kKBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                tc::commit(&sm.s_full[t]);
+            }
+        };
+        if (n_steps > 0) {
+            wait(&sm.q_full, 0);
+            wait(&sm.k_full[0], 0);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                if (steps[t] > 0)
+                    scores(t, 0);
+            if (elect())
+                tc::commit(&sm.k_empty[0]);
+        }
+        for (int j = 0; j < n_steps && !wait.dead; ++j) {
+            const int s = j & 1;
+            wait(&sm.v_full[s], (j / 2) & 1);
+            if (j + 1 < n_steps)
+                wait(&sm.k_full[s ^ 1], ((j + 1) / 2) & 1);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (j < steps[t]) {
+                    wait(&sm.p_full[t], j & 1);
+                    tc::fence_after_sync();
+                    if (elect()) {
+#pragma unroll
+                        for (int ks = 0; ks < kKeys / 16; ++ks)
+                            tc::mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8,
+                                            vd.at(s * 2 * kKBlk + ks * 2048), id_o, j > 0 || ks > 0 ? 1u : 0u);
+                        tc::commit(&sm.pv_done[t]);
+                    }
+                }
+                if (t == kTiles - 1 && elect())
+                    tc::commit(&sm.v_empty[s]);
+                // S takes the place of the P that the products just issued read: they run in order
+                if (j + 1 < steps[t])
+                    scores(t, j + 1);
+            }
+            if (j + 1 < n_steps && elect())
+                tc::commit(&sm.k_empty[s ^ 1]);
+        }
+    } else {
+        // ---------------- softmax: one row a thread
+        const int t = warp >> 2, row = i0 + t * kRows + (warp & 3) * 32 + lane;
+        const int last = last_key(row, lq, lk, a.causal);
+        const int last_0 = last_key(i0 + t * kRows, lq, lk, a.causal);  // the tile's first row sees the fewest keys
+        const uint32_t s_addr = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, t * 128), o_addr = s_addr + 256;
+        const int n = t == 0 ? steps[0] : steps[1];
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            wait(&sm.s_full[t], j & 1);
+            tc::fence_after_sync();
+            uint32_t x[3][32];
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+                tc::ld_32x32b_x32(s_addr + c * 32, x[c]);
+            tc::wait_ld();
+            if ((j + 1) * kKeys - 1 > last_0) {
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (j * kKeys + c * 32 + i > last)
+                            x[c][i] = __float_as_uint(-INFINITY);
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[c][i]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const bool grow = top > m + kGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float mn = grow ? top : m, f = grow ? ex2(m - mn) : 1.0f;
+                m = mn;
+                l *= f;
+                if (j > 0) {
+                    wait(&sm.pv_done[t], (j - 1) & 1);
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t y[32];
+                        tc::ld_32x32b_x32(o_addr + c * 32, y);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                        tc::st_32x32b_x32(o_addr + c * 32, y);
+                    }
+                }
+            }
+            const float sub = m == -INFINITY ? 0.0f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t p[48];
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float e0 = ex2(fmaf(__uint_as_float(x[c][i]), a.scale_log2, -sub));
+                    const float e1 = ex2(fmaf(__uint_as_float(x[c][i + 1]), a.scale_log2, -sub));
+                    sum[i & 2] += e0;
+                    sum[(i & 2) + 1] += e1;
+                    p[c * 16 + i / 2] = pack_bf16x2(e0, e1);
+                }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc::st_32x32b_x32(s_addr, *reinterpret_cast<const uint32_t(*)[32]>(p));
+            tc::st_32x32b_x16(s_addr + 32, *reinterpret_cast<const uint32_t(*)[16]>(p + 32));
+            tc::wait_st();
+            tc::fence_before_sync();
+            mbar_arrive(&sm.p_full[t]);
+        }
+        // ---- the row's result
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t r = (int64_t)(q0 + row) * a.H + h;
+        if (n > 0) {
+            wait(&sm.pv_done[t], (n - 1) & 1);
+            tc::fence_after_sync();
+        }
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            if (n > 0) {
+                tc::ld_32x32b_x32(o_addr + c * 32, y);
+                tc::wait_ld();
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = l == 0.0f ? 0u
+                                 : pack_bf16x2(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
+            if (row < lq) {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.o + r * kDV + c * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+        }
+        if (a.lse && row < lq)
+            a.lse[r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 8)
+        tc::tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -71,14 +318,25 @@ cudaError_t launch_mla_fwd(int N, const int32_t *cu_q, const int32_t *cu_k, int 
                            float scale, const void *q, const void *kv, const void *k_rope, void *o, float *lse,
                            cudaStream_t s)
 {
-    unsigned int *status = device_status_ptr();
-    if (!status)
+    FwdArgs a{N, Tq, Tk, H, causal, scale * kLog2e, cu_q, cu_k, static_cast<__nv_bfloat16 *>(o), lse, device_status_ptr()};
+    if (!a.status)
         return cudaErrorInvalidDevice;
-    const int64_t units = (int64_t)Tq * H, grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-    mla_fwd_kernel<<<(unsigned)grid, kThreads, 0, s>>>(
-        N, cu_q, cu_k, Tq, Tk, H, causal, scale, static_cast<const __nv_bfloat16 *>(q),
-        static_cast<const __nv_bfloat16 *>(kv), static_cast<const __nv_bfloat16 *>(k_rope),
-        static_cast<__nv_bfloat16 *>(o), lse, status);
+    FwdMaps maps{};
+    cudaError_t e = make_rows_map(&maps.q, q, kDQ, H, Tq, kRows, 3);
+    if (e == cudaSuccess && Tk > 0)
+        e = make_rows_map(&maps.kv, kv, kDKV, H, Tk, kKeys, 2);
+    if (e == cudaSuccess && Tk > 0)
+        e = make_rows_map(&maps.kr, k_rope, kDR, 0, Tk, kKeys, 1);
+    const size_t smem = sizeof(FwdSmem) + 1024;
+    static_assert(sizeof(FwdSmem) + 1024 <= 232448, "shared memory of one CTA");
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mla_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t items = (int64_t)Tq / (kTiles * kRows) + N;  // at least the tile pairs of any N sequences
+    if (items * H > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    mla_fwd_kernel<<<(unsigned)(items * H), kThreads, smem, s>>>(maps, a);
     return cudaGetLastError();
 }
 

@@ -151,5 +151,22 @@ inline cudaError_t make_map(CUtensorMap *m, const void *base, int elem, int rank
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Rows of `numbers` bfloat16 for each of H heads ([rows, H, numbers]; H = 0: [rows, numbers]) as
+// [block of 64 numbers][head][row][64] (or [row][64]), boxes of box_rows rows and `blocks` blocks
+// of one head.
+inline cudaError_t make_rows_map(CUtensorMap *m, const void *base, int numbers, int H, int64_t rows, int box_rows,
+                                 int blocks)
+{
+    const int64_t nb = (int64_t)numbers * 2;
+    if (H == 0) {
+        const int64_t extent[2] = {numbers, rows}, stride[1] = {nb};
+        const int box[2] = {64, box_rows};
+        return make_map(m, base, 2, 2, extent, stride, box);
+    }
+    const int64_t extent[4] = {64, rows, H, numbers / 64}, stride[3] = {H * nb, nb, 128};
+    const int box[4] = {64, box_rows, 1, blocks};
+    return make_map(m, base, 2, 4, extent, stride, box);
+}
+
 }  // namespace mla
 }  // namespace kda
