@@ -1,9 +1,30 @@
 // mla_bwd.cu -- gradients of the expanded latent attention over packed sequences.
 //
-//   p_ij = e^{s_ij - lse_i},  dS_ij = scale p_ij (dO_i . v_j - D_i),  D_i = dO_i . o_i
-// One warp per (query, head) sums dq over its keys; one per (key, head) sums dk, dv and its
-// head's part of dk_rope over its queries; the parts are then added over the heads in order.
+//   p_ij = e^{s_ij - lse_i},  D_i = dO_i . o_i,  e_ij = p_ij (dO_i . v_j - D_i)
+//   dq_i = scale sum_j e_ij [k_j, k_rope_j];  dk_j = scale sum_i e_ij q_i;  dv_j = sum_i p_ij dO_i
+// Bound by the tensor cores.  Sums over queries and sums over keys are taken by two launches of
+// one kernel, each keeping its sums in tensor memory: a single pass would have to add dq across
+// CTAs with atomics (an order of its own every time) and needs 128 + 192 + 192 accumulator columns
+// beside S and dP, more than there are.  The price is S and dP twice: 1152 multiply-adds a pair
+// for the 832 of the formulas.
+//
+// Both launches hold a 128-row tile (X: queries for dq, keys for dk and dv) and step through the
+// other side (Y) 96 rows at a time:
+//   S = X1 Y1^T (K = 192),  dP = X2 Y2^T (K = 128),  acc1 += e Y1 (N = 192),
+//   keys only: acc2 += p Y2 (N = 128)
+// with X1, Y1 the q and [k, k_rope] rows and X2, Y2 the dO and v rows.  A Y tile serves as K-major
+// operand of the first two products and MN-major operand of the last two; p and e go back to
+// tensor memory as their A operands, over the S and dP they came from.  The products are issued
+//   acc2(i), S(i + 1), acc1(i), dP(i + 1)
+// so that the threads always have two products' time for p(i + 1) and two for e(i), without a
+// second S or dP buffer.
+//
+// Warps: 0-7 elementwise (row = tensor-memory lane; warps 0-3 take columns 0-47, 4-7 48-95);
+// 8 copies (TMA); 9 issues the products.  The launch for dq computes D first and leaves D and lse
+// in base 2, head by head, for the other.  dk_rope's parts are added over the heads, in order, by
+// a third launch.
 #include "mla_common.cuh"
+#include "mla_tc.cuh"
 
 namespace kda {
 
@@ -11,152 +32,489 @@ namespace {
 
 using namespace mla;
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ int seq_of(const int32_t *__restrict__ cu, int N, int64_t row)
-{
-    int lo = 0, hi = N;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= row)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ float at(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
+constexpr int kThreads = 320;
+constexpr int kRows = 128;               // X rows of a CTA
+constexpr int kStep = 96;                // Y rows a step
+constexpr int kHalf = kStep / 2;         // columns of a warp
+constexpr int kY1 = 3, kY2 = 1;          // stages
+constexpr uint32_t kXBlk = kRows * 128;  // 64 numbers of the rows
+constexpr uint32_t kYBlk = kStep * 128;
+constexpr uint32_t kColS = 0, kColP = kStep, kCol2 = 2 * kStep, kCol1 = kCol2 + 128;  // tensor memory columns
+static_assert(kCol1 + kDQ <= 512, "tensor memory");
 
 struct BwdArgs {
     int N, Tq, Tk, H;
     bool causal;
     float scale;
     const int32_t *cu_q, *cu_k;
-    const __nv_bfloat16 *q, *kv, *kr, *o, *dO;
+    const __nv_bfloat16 *o, *dO;
     const float *lse;
     __nv_bfloat16 *dq, *dkv, *dkr;
-    float *delta, *part;
+    float *delta, *lse2;  // [H][Tq]
+    float *part;          // [H][Tk][64]
     unsigned int *status;
 };
 
-__device__ __forceinline__ bool axes_ok(const BwdArgs &a)
+// x1, x2: boxes of kRows rows; y1, y2: of kStep rows.  The key side is two maps (kv and k_rope).
+struct BwdMaps {
+    CUtensorMap x1, x1r, x2, y1, y1r, y2;
+};
+
+struct BwdSmem {
+    alignas(1024) unsigned char x1[3 * kXBlk];
+    alignas(1024) unsigned char x2[2 * kXBlk];
+    alignas(1024) unsigned char y1[kY1][3 * kYBlk];
+    alignas(1024) unsigned char y2[kY2][2 * kYBlk];
+    float col[kY1][2][kStep];  // keys: lse in base 2 and D of a step's queries
+    float dsum[2][kRows];      // queries: halves of D
+    uint64_t x_full, y1_full[kY1], y1_empty[kY1], y2_full[kY2], y2_empty[kY2], tail;
+    uint64_t s_full, p_full, dp_full, e_full, done;
+    uint32_t tmem_slot;
+    int64_t find[40];
+};
+
+__device__ __forceinline__ void row_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// kHalf columns of this thread's lane as bfloat16 pairs.
+__device__ __forceinline__ void store_half(uint32_t taddr, const float (&x)[kHalf])
 {
+    uint32_t w[kHalf / 2];
+#pragma unroll
+    for (int i = 0; i < kHalf / 2; ++i)
+        w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    tc::st_32x32b_x16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(w));
+    tc::st_32x32b_x8(taddr + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 16));
+    tc::wait_st();
+}
+
+__device__ __forceinline__ void load_half(uint32_t taddr, float (&x)[kHalf])
+{
+    uint32_t a[32], b[16];
+    tc::ld_32x32b_x32(taddr, a);
+    tc::ld_32x32b_x16(taddr + 32, b);
+    tc::wait_ld();
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i)
+        x[i] = __uint_as_float(i < 32 ? a[i] : b[i - 32]);
+}
+
+// Columns of this thread's lane, times f, to bfloat16 (zeros where `none`).
+__device__ __forceinline__ void write_out(uint32_t taddr, int columns, float f, bool none, bool live, __nv_bfloat16 *dst)
+{
+#pragma unroll 1
+    for (int c = 0; c < columns; c += 32) {
+        uint32_t y[32];
+        if (!none) {
+            tc::ld_32x32b_x32(taddr + c, y);
+            tc::wait_ld();
+        }
+        if (live)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = none ? 0u
+                                : pack_bf16x2(__uint_as_float(y[i + 2 * k]) * f, __uint_as_float(y[i + 2 * k + 1]) * f);
+                *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+    }
+}
+
+template <bool kKeys>  // X rows are keys (dk, dv), else queries (dq)
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_bwd_kernel(const __grid_constant__ BwdMaps maps, BwdArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    BwdSmem &sm = *reinterpret_cast<BwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % a.H;
     const bool okq = offsets_ok<kThreads>(a.cu_q, a.N, a.Tq), okk = offsets_ok<kThreads>(a.cu_k, a.N, a.Tk);
     if (!okq || !okk) {
-        if (threadIdx.x == 0)
+        if (tid == 0)
             report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        return false;
+        return;
     }
-    return true;
+    const int32_t *cu_x = kKeys ? a.cu_k : a.cu_q;
+    Item it;
+    if (!find_item<kThreads>(
+            a.N, blockIdx.x / a.H, [&](int n) { return (cu_x[n + 1] - cu_x[n] + kRows - 1) / kRows; }, it, sm.find))
+        return;
+    const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
+    const int lx = kKeys ? lk : lq, ly = kKeys ? lq : lk;
+    // with a causal mask the first keys and the last queries have the most to do: they go first
+    const int r0 = (kKeys ? it.k : (lx + kRows - 1) / kRows - 1 - it.k) * kRows, rows = min(kRows, lx - r0);
+    const int off = lk - lq;  // causal: key j is visible to query i from i = j - off on
+    // Y rows [y_first, y_end)
+    const int y_first = kKeys && a.causal ? max(0, r0 - off) : 0;
+    const int y_end = !kKeys && a.causal ? min(ly, r0 + rows + off) : ly;
+    const int steps = y_first < y_end ? (y_end - y_first + kStep - 1) / kStep : 0;
+
+    if (tid == 0) {
+        mbar_init(&sm.x_full, 1);
+        mbar_init(&sm.tail, 1);
+        for (int i = 0; i < kY1; ++i) {
+            mbar_init(&sm.y1_full[i], kKeys ? 33 : 1);
+            mbar_init(&sm.y1_empty[i], 1);
+        }
+        for (int i = 0; i < kY2; ++i) {
+            mbar_init(&sm.y2_full[i], 1);
+            mbar_init(&sm.y2_empty[i], 1);
+        }
+        mbar_init(&sm.s_full, 1);
+        mbar_init(&sm.dp_full, 1);
+        mbar_init(&sm.p_full, 256);
+        mbar_init(&sm.e_full, 256);
+        mbar_init(&sm.done, 1);
+        fence_mbar_init_cluster();
+    }
+    if (warp == 8)
+        tc::tmem_alloc(&sm.tmem_slot, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem_slot;
+    Waits wait{a.status, false};
+
+    if (warp == 8) {
+        // ---------------- copies
+        if (steps > 0 && elect()) {
+            mbar_arrive_expect_tx(&sm.x_full, 5 * kXBlk);
+            const int x = (kKeys ? k0 : q0) + r0;
+            tma_load_4d(sm.x1, &maps.x1, 0, x, h, 0, &sm.x_full);
+            if (kKeys)
+                tma_load_2d(sm.x1 + 2 * kXBlk, &maps.x1r, 0, x, &sm.x_full);
+            tma_load_4d(sm.x2, &maps.x2, 0, x, h, kKeys ? 2 : 0, &sm.x_full);
+        }
+        __syncwarp();
+        Ring<kY1> r1;
+        Ring<kY2> r2;
+        uint32_t tails = 0;
+        // rows behind the sequence's end may hold anything (0 * NaN): zeros
+        auto zero_tail = [&](unsigned char *p, int blocks, int live, uint64_t *full) {
+            wait(&sm.tail, tails++ & 1);
+            for (int i = lane; i < (kStep - live) * 8 * blocks; i += 32)
+                *reinterpret_cast<uint4 *>(p + i % blocks * kYBlk + (live + i / (8 * blocks)) * 128 +
+                                           i / blocks % 8 * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect())
+                mbar_arrive(full);
+        };
+        for (int i = 0; i < steps && !wait.dead; ++i, r1.step(), r2.step()) {
+            const int first = y_first + i * kStep, live = ly - first, y = (kKeys ? q0 : k0) + first;
+            float cl[kStep / 32], cd[kStep / 32];
+            if (kKeys)
+#pragma unroll
+                for (int c = 0; c < kStep / 32; ++c) {
+                    const bool in = c * 32 + lane < live;
+                    cl[c] = in ? a.lse2[(int64_t)h * a.Tq + y + c * 32 + lane] : INFINITY;
+                    cd[c] = in ? a.delta[(int64_t)h * a.Tq + y + c * 32 + lane] : 0.0f;
+                }
+            if (r1.round > 0)
+                wait(&sm.y1_empty[r1.slot], (r1.round - 1) & 1);
+            if (wait.dead)
+                break;
+            uint64_t *bar = live < kStep ? &sm.tail : &sm.y1_full[r1.slot];
+            if (elect()) {
+                mbar_arrive_expect_tx(bar, 3 * kYBlk);
+                tma_load_4d(sm.y1[r1.slot], &maps.y1, 0, y, h, 0, bar);
+                if (!kKeys)
+                    tma_load_2d(sm.y1[r1.slot] + 2 * kYBlk, &maps.y1r, 0, y, bar);
+            }
+            __syncwarp();
+            if (kKeys) {
+#pragma unroll
+                for (int c = 0; c < kStep / 32; ++c) {
+                    sm.col[r1.slot][0][c * 32 + lane] = cl[c];
+                    sm.col[r1.slot][1][c * 32 + lane] = cd[c];
+                }
+                mbar_arrive(&sm.y1_full[r1.slot]);
+            }
+            if (live < kStep)
+                zero_tail(sm.y1[r1.slot], 3, live, &sm.y1_full[r1.slot]);
+            if (r2.round > 0)
+                wait(&sm.y2_empty[r2.slot], (r2.round - 1) & 1);
+            if (wait.dead)
+                break;
+            bar = live < kStep ? &sm.tail : &sm.y2_full[r2.slot];
+            if (elect()) {
+                mbar_arrive_expect_tx(bar, 2 * kYBlk);
+                tma_load_4d(sm.y2[r2.slot], &maps.y2, 0, y, h, kKeys ? 0 : 2, bar);
+            }
+            __syncwarp();
+            if (live < kStep)
+                zero_tail(sm.y2[r2.slot], 2, live, &sm.y2_full[r2.slot]);
+        }
+    } else if (warp == 9) {
+        // ---------------- products
+        constexpr uint32_t id_s = tc::idesc_bf16(kRows, kStep, false, false), id_1 = tc::idesc_bf16(kRows, kDQ, false, true),
+                           id_2 = tc::idesc_bf16(kRows, kDV, false, true);
+        const Desc x1(smem_u32(sm.x1), 16, 1024, tc::kSw128), x2(smem_u32(sm.x2), 16, 1024, tc::kSw128),
+            y1(smem_u32(sm.y1[0]), 16, 1024, tc::kSw128), y2(smem_u32(sm.y2[0]), 16, 1024, tc::kSw128),
+            t1(smem_u32(sm.y1[0]), kYBlk, 1024, tc::kSw128), t2(smem_u32(sm.y2[0]), kYBlk, 1024, tc::kSw128);
+        // tensor-memory column of the 16 Y rows ks of p or e: each half of the columns at its own start
+        auto a_col = [](uint32_t base, int ks) { return base + (ks < 3 ? 0 : kHalf - 24) + ks * 8; };
+        static_assert(kHalf == 48, "three 16-row steps a half");
+        auto scores = [&](uint32_t slot) {
+            if (elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kDQ / 16; ++ks)
+                    tc::mma_bf16(tmem + kColS, x1.at((ks >> 2) * kXBlk + (ks & 3) * 32),
+                                 y1.at(slot * 3 * kYBlk + (ks >> 2) * kYBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                tc::commit(&sm.s_full);
+            }
+        };
+        auto dps = [&](uint32_t slot) {
+            if (elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kDV / 16; ++ks)
+                    tc::mma_bf16(tmem + kColP, x2.at((ks >> 2) * kXBlk + (ks & 3) * 32),
+                                 y2.at(slot * 2 * kYBlk + (ks >> 2) * kYBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+                tc::commit(&sm.dp_full);
+                if (!kKeys)
+                    tc::commit(&sm.y2_empty[slot]);
+            }
+        };
+        Ring<kY1> r1;  // of step i + 1
+        Ring<kY2> r2;
+        uint32_t now1 = 0, now2 = 0;
+        if (steps > 0) {
+            wait(&sm.x_full, 0);
+            wait(&sm.y1_full[0], 0);
+            tc::fence_after_sync();
+            scores(0);
+            wait(&sm.y2_full[0], 0);
+            tc::fence_after_sync();
+            dps(0);
+            r1.step();
+            r2.step();
+        }
+        for (int i = 0; i < steps && !wait.dead; ++i, r1.step(), r2.step()) {
+            wait(&sm.p_full, i & 1);  // p(i) written, or at least S(i) read
+            tc::fence_after_sync();
+            if (kKeys && elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kStep / 16; ++ks)
+                    tc::mma_bf16_ts(tmem + kCol2, tmem + a_col(kColS, ks), t2.at(now2 * 2 * kYBlk + ks * 2048), id_2,
+                                    i > 0 || ks > 0 ? 1u : 0u);
+                tc::commit(&sm.y2_empty[now2]);
+            }
+            if (i + 1 < steps) {
+                wait(&sm.y1_full[r1.slot], r1.round & 1);
+                tc::fence_after_sync();
+                scores(r1.slot);
+            }
+            wait(&sm.e_full, i & 1);
+            tc::fence_after_sync();
+            if (elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kStep / 16; ++ks)
+                    tc::mma_bf16_ts(tmem + kCol1, tmem + a_col(kColP, ks), t1.at(now1 * 3 * kYBlk + ks * 2048), id_1,
+                                    i > 0 || ks > 0 ? 1u : 0u);
+                tc::commit(&sm.y1_empty[now1]);
+                if (i + 1 == steps)
+                    tc::commit(&sm.done);
+            }
+            if (i + 1 < steps) {
+                wait(&sm.y2_full[r2.slot], r2.round & 1);
+                tc::fence_after_sync();
+                dps(r2.slot);
+            }
+            now1 = r1.slot;
+            now2 = r2.slot;
+        }
+    } else {
+        // ---------------- elementwise: row r0 + r, columns half * 48 ..
+        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        const bool live = r < rows;
+        const uint32_t addr = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, half * kHalf);
+        const float sl2 = a.scale * kLog2e;
+        float lse2 = INFINITY, delta = 0.0f;
+        if constexpr (!kKeys) {
+            const int64_t row = (int64_t)(q0 + r0 + r) * a.H + h;
+            if (live) {
+                const uint4 *x = reinterpret_cast<const uint4 *>(a.o + row * kDV + half * 64);
+                const uint4 *y = reinterpret_cast<const uint4 *>(a.dO + row * kDV + half * 64);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 u = x[c], v = y[c];
+                    const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = unpack_bf16x2(uw[k]), g = unpack_bf16x2(vw[k]);
+                        delta += f.x * g.x + f.y * g.y;
+                    }
+                }
+                const float l = a.lse[row];
+                lse2 = l == -INFINITY ? INFINITY : l * kLog2e;  // a row that sees no key: weights 0
+            }
+            sm.dsum[half][r] = delta;
+            row_sync();
+            delta = sm.dsum[0][r] + sm.dsum[1][r];
+            if (live && half == 0) {
+                a.delta[(int64_t)h * a.Tq + q0 + r0 + r] = delta;
+                a.lse2[(int64_t)h * a.Tq + q0 + r0 + r] = lse2;
+            }
+        }
+        Ring<kY1> r1;
+        for (int i = 0; i < steps; ++i, r1.step()) {
+            const int y = y_first + i * kStep + half * kHalf;  // place of the first column
+            // columns lo .. hi - 1 are visible to the row
+            int lo = 0, hi = kHalf;
+            bool edge;
+            if (kKeys) {
+                edge = i + 1 == steps || (a.causal && r0 + kRows - 1 > y_first + i * kStep + off);
+                hi = ly - y;
+                lo = a.causal ? r0 + r - off - y : 0;
+            } else {
+                edge = (i + 1) * kStep > (a.causal ? min(ly, r0 + off + 1) : ly);
+                hi = (a.causal ? min(ly, r0 + r + off + 1) : ly) - y;
+            }
+            float p[kHalf], x[kHalf];
+            wait(&sm.s_full, i & 1);
+            tc::fence_after_sync();
+            load_half(addr + kColS, p);
+            if (kKeys) {
+                wait(&sm.y1_full[r1.slot], r1.round & 1);  // the step's lse and D
+                const float4 *l = reinterpret_cast<const float4 *>(sm.col[r1.slot][0] + half * kHalf);
+#pragma unroll
+                for (int c = 0; c < kHalf / 4; ++c) {
+                    const float4 v = l[c];
+                    p[4 * c] = ex2(fmaf(p[4 * c], sl2, -v.x));
+                    p[4 * c + 1] = ex2(fmaf(p[4 * c + 1], sl2, -v.y));
+                    p[4 * c + 2] = ex2(fmaf(p[4 * c + 2], sl2, -v.z));
+                    p[4 * c + 3] = ex2(fmaf(p[4 * c + 3], sl2, -v.w));
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c)
+                    p[c] = ex2(fmaf(p[c], sl2, -lse2));
+            }
+            if (edge) {
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c)
+                    if (c < lo || c >= hi)
+                        p[c] = 0.0f;
+            }
+            if (kKeys)
+                store_half(addr + kColS, p);
+            tc::fence_before_sync();
+            mbar_arrive(&sm.p_full);
+            wait(&sm.dp_full, i & 1);
+            tc::fence_after_sync();
+            load_half(addr + kColP, x);
+            if (kKeys) {
+                const float4 *d = reinterpret_cast<const float4 *>(sm.col[r1.slot][1] + half * kHalf);
+#pragma unroll
+                for (int c = 0; c < kHalf / 4; ++c) {
+                    const float4 v = d[c];
+                    x[4 * c] = p[4 * c] * (x[4 * c] - v.x);
+                    x[4 * c + 1] = p[4 * c + 1] * (x[4 * c + 1] - v.y);
+                    x[4 * c + 2] = p[4 * c + 2] * (x[4 * c + 2] - v.z);
+                    x[4 * c + 3] = p[4 * c + 3] * (x[4 * c + 3] - v.w);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c)
+                    x[c] = p[c] * (x[c] - delta);
+            }
+            if (edge) {  // a hidden pair's dP may be anything
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c)
+                    if (c < lo || c >= hi)
+                        x[c] = 0.0f;
+            }
+            store_half(addr + kColP, x);
+            tc::fence_before_sync();
+            mbar_arrive(&sm.e_full);
+        }
+        // ---- the sums
+        if (steps > 0) {
+            wait(&sm.done, 0);
+            tc::fence_after_sync();
+        }
+        const uint32_t base = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, 0);
+        const bool none = steps == 0;
+        if (kKeys) {
+            const int64_t key = k0 + r0 + r;
+            __nv_bfloat16 *dst = a.dkv + (key * a.H + h) * kDKV;
+            if (half == 0) {
+                write_out(base + kCol2, kDV, 1.0f, none, live, dst + kDN);
+            } else {
+                write_out(base + kCol1, kDN, a.scale, none, live, dst);
+                float *part = a.part + ((int64_t)h * a.Tk + key) * kDR;
+#pragma unroll 1
+                for (int c = 0; c < kDR; c += 32) {
+                    uint32_t y[32];
+                    if (!none) {
+                        tc::ld_32x32b_x32(base + kCol1 + kDN + c, y);
+                        tc::wait_ld();
+                    }
+                    if (live)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(part + c + k) =
+                                none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                     : make_float4(__uint_as_float(y[k]) * a.scale, __uint_as_float(y[k + 1]) * a.scale,
+                                                   __uint_as_float(y[k + 2]) * a.scale, __uint_as_float(y[k + 3]) * a.scale);
+                }
+            }
+        } else {
+            __nv_bfloat16 *dst = a.dq + ((int64_t)(q0 + r0 + r) * a.H + h) * kDQ;
+            write_out(base + kCol1 + half * 96, 96, a.scale, none, live, dst + half * 96);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 8)
+        tc::tmem_dealloc(tmem, 512);
 }
 
-__global__ void __launch_bounds__(kThreads) mla_dq_kernel(BwdArgs a)
+// dk_rope: its heads' parts in order, four numbers a thread.
+__global__ void __launch_bounds__(256) mla_dkr_kernel(BwdArgs a)
 {
-    if (!axes_ok(a))
+    const bool okq = offsets_ok<256>(a.cu_q, a.N, a.Tq), okk = offsets_ok<256>(a.cu_k, a.N, a.Tk);
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (!okq || !okk || x >= (int64_t)a.cu_k[a.N] * (kDR / 4))
         return;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, h = (int)(unit % a.H);
-    const int64_t row = unit / a.H;
-    if (row >= a.cu_q[a.N])
-        return;
-    const int n = seq_of(a.cu_q, a.N, row);
-    const int lq = a.cu_q[n + 1] - a.cu_q[n], lk = a.cu_k[n + 1] - a.cu_k[n], i = (int)(row - a.cu_q[n]);
-    const int last = a.causal ? min(lk, max(0, i + lk - lq + 1)) : lk;
-    const int64_t r = row * a.H + h;
-    float qf[6], dof[4], dq[6] = {}, delta = 0.0f;
-    for (int c = 0; c < 6; ++c)
-        qf[c] = at(a.q, r * kDQ + c * 32 + lane) * a.scale;
-    for (int c = 0; c < 4; ++c) {
-        dof[c] = at(a.dO, r * kDV + c * 32 + lane);
-        delta += dof[c] * at(a.o, r * kDV + c * 32 + lane);
+    const float4 *p = reinterpret_cast<const float4 *>(a.part) + x;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int h = 0; h < a.H; ++h) {
+        const float4 v = p[(int64_t)h * a.Tk * (kDR / 4)];
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
     }
-    delta = warp_sum(delta);
-    if (lane == 0)
-        a.delta[r] = delta;
-    const float lse = a.lse[r];
-    for (int j = 0; j < last; ++j) {
-        const int64_t t = a.cu_k[n] + j, kvr = (t * a.H + h) * kDKV;
-        float kf[6], s = 0.0f, dp = 0.0f;
-        for (int c = 0; c < 6; ++c) {
-            kf[c] = c < 4 ? at(a.kv, kvr + c * 32 + lane) : at(a.kr, t * kDR + (c - 4) * 32 + lane);
-            s += qf[c] * kf[c];
-        }
-        for (int c = 0; c < 4; ++c)
-            dp += dof[c] * at(a.kv, kvr + kDN + c * 32 + lane);
-        const float ds = a.scale * expf(warp_sum(s) - lse) * (warp_sum(dp) - delta);
-        for (int c = 0; c < 6; ++c)
-            dq[c] += ds * kf[c];
-    }
-    for (int c = 0; c < 6; ++c)
-        a.dq[r * kDQ + c * 32 + lane] = __float2bfloat16(dq[c]);
-}
-
-__global__ void __launch_bounds__(kThreads) mla_dkv_kernel(BwdArgs a)
-{
-    if (!axes_ok(a))
-        return;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, h = (int)(unit % a.H);
-    const int64_t t = unit / a.H;
-    if (t >= a.cu_k[a.N])
-        return;
-    const int n = seq_of(a.cu_k, a.N, t);
-    const int lq = a.cu_q[n + 1] - a.cu_q[n], lk = a.cu_k[n + 1] - a.cu_k[n], j = (int)(t - a.cu_k[n]);
-    const int first = a.causal ? max(0, j - (lk - lq)) : 0;
-    const int64_t kvr = (t * a.H + h) * kDKV;
-    float kf[6], vf[4], dk[6] = {}, dv[4] = {};
-    for (int c = 0; c < 6; ++c)
-        kf[c] = (c < 4 ? at(a.kv, kvr + c * 32 + lane) : at(a.kr, t * kDR + (c - 4) * 32 + lane)) * a.scale;
-    for (int c = 0; c < 4; ++c)
-        vf[c] = at(a.kv, kvr + kDN + c * 32 + lane);
-    for (int i = first; i < lq; ++i) {
-        const int64_t r = (int64_t)(a.cu_q[n] + i) * a.H + h;
-        float qf[6], dof[4], s = 0.0f, dp = 0.0f;
-        for (int c = 0; c < 6; ++c) {
-            qf[c] = at(a.q, r * kDQ + c * 32 + lane);
-            s += qf[c] * kf[c];
-        }
-        for (int c = 0; c < 4; ++c) {
-            dof[c] = at(a.dO, r * kDV + c * 32 + lane);
-            dp += dof[c] * vf[c];
-        }
-        const float p = expf(warp_sum(s) - a.lse[r]);
-        const float ds = a.scale * p * (warp_sum(dp) - a.delta[r]);
-        for (int c = 0; c < 6; ++c)
-            dk[c] += ds * qf[c];
-        for (int c = 0; c < 4; ++c)
-            dv[c] += p * dof[c];
-    }
-    for (int c = 0; c < 4; ++c) {
-        a.dkv[kvr + c * 32 + lane] = __float2bfloat16(dk[c]);
-        a.dkv[kvr + kDN + c * 32 + lane] = __float2bfloat16(dv[c]);
-    }
-    for (int c = 0; c < 2; ++c)
-        a.part[(t * a.H + h) * kDR + c * 32 + lane] = dk[4 + c];
-}
-
-__global__ void __launch_bounds__(kThreads) mla_dkr_kernel(BwdArgs a)
-{
-    if (!axes_ok(a))
-        return;
-    const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t t = x / kDR;
-    if (t >= a.cu_k[a.N])
-        return;
-    float sum = 0.0f;
-    for (int h = 0; h < a.H; ++h)
-        sum += a.part[(t * a.H + h) * kDR + x % kDR];
-    a.dkr[x] = __float2bfloat16(sum);
+    reinterpret_cast<uint2 *>(a.dkr)[x] = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <bool kKeys>
+cudaError_t launch_side(const BwdMaps &maps, const BwdArgs &a, cudaStream_t s)
+{
+    const size_t smem = sizeof(BwdSmem) + 1024;
+    static_assert(sizeof(BwdSmem) + 1024 <= 232448, "shared memory of one CTA");
+    const cudaError_t e =
+        cudaFuncSetAttribute(mla_bwd_kernel<kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t grid = ((int64_t)(kKeys ? a.Tk : a.Tq) / kRows + a.N) * a.H;  // at least the tiles of any N sequences
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    mla_bwd_kernel<kKeys><<<(unsigned)grid, kThreads, smem, s>>>(maps, a);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
 size_t mla_bwd_workspace(int Tq, int Tk, int H)
 {
-    return round256((size_t)Tq * H * 4) + round256((size_t)Tk * H * kDR * 4) + 256;
+    return 2 * round256((size_t)Tq * H * 4) + round256((size_t)Tk * H * kDR * 4) + 256;
 }
 
 cudaError_t launch_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, bool causal,
@@ -164,22 +522,44 @@ cudaError_t launch_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int 
                            const float *lse, const void *dO, void *dq, void *dkv, void *dk_rope, void *workspace,
                            cudaStream_t s)
 {
-    typedef const __nv_bfloat16 *In;
-    typedef __nv_bfloat16 *Out;
-    BwdArgs a{N, Tq, Tk, H, causal, scale, cu_q, cu_k, In(q), In(kv), In(k_rope), In(o), In(dO), lse,
-              Out(dq), Out(dkv), Out(dk_rope), static_cast<float *>(workspace),
-              reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + round256((size_t)Tq * H * 4)),
-              device_status_ptr()};
+    const size_t rows = round256((size_t)Tq * H * 4);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    BwdArgs a{N, Tq, Tk, H, causal, scale, cu_q, cu_k, static_cast<const __nv_bfloat16 *>(o),
+              static_cast<const __nv_bfloat16 *>(dO), lse, static_cast<__nv_bfloat16 *>(dq),
+              static_cast<__nv_bfloat16 *>(dkv), static_cast<__nv_bfloat16 *>(dk_rope), reinterpret_cast<float *>(ws),
+              reinterpret_cast<float *>(ws + rows), reinterpret_cast<float *>(ws + 2 * rows), device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;
-    const int W = kThreads / 32;
-    if (Tq > 0)
-        mla_dq_kernel<<<(unsigned)(((int64_t)Tq * H + W - 1) / W), kThreads, 0, s>>>(a);
-    if (Tk > 0) {
-        mla_dkv_kernel<<<(unsigned)(((int64_t)Tk * H + W - 1) / W), kThreads, 0, s>>>(a);
-        mla_dkr_kernel<<<(unsigned)(((int64_t)Tk * kDR + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    cudaError_t e = cudaSuccess;
+    auto map = [&](CUtensorMap *m, const void *p, int numbers, int heads, int64_t n, int box, int blocks) {
+        if (e == cudaSuccess && n > 0)
+            e = make_rows_map(m, p, numbers, heads, n, box, blocks);
+    };
+    if (Tq > 0) {
+        BwdMaps m{};
+        map(&m.x1, q, kDQ, H, Tq, kRows, 3);
+        map(&m.x2, dO, kDV, H, Tq, kRows, 2);
+        map(&m.y1, kv, kDKV, H, Tk, kStep, 2);
+        map(&m.y1r, k_rope, kDR, 0, Tk, kStep, 1);
+        map(&m.y2, kv, kDKV, H, Tk, kStep, 2);
+        if (e == cudaSuccess)
+            e = launch_side<false>(m, a, s);
     }
-    return cudaGetLastError();
+    if (Tk > 0) {
+        BwdMaps m{};
+        map(&m.x1, kv, kDKV, H, Tk, kRows, 2);
+        map(&m.x1r, k_rope, kDR, 0, Tk, kRows, 1);
+        map(&m.x2, kv, kDKV, H, Tk, kRows, 2);
+        map(&m.y1, q, kDQ, H, Tq, kStep, 3);
+        map(&m.y2, dO, kDV, H, Tq, kStep, 2);
+        if (e == cudaSuccess)
+            e = launch_side<true>(m, a, s);
+        if (e != cudaSuccess)
+            return e;
+        mla_dkr_kernel<<<(unsigned)(((int64_t)Tk * (kDR / 4) + 255) / 256), 256, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 }  // namespace kda
