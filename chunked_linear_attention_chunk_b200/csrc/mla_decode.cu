@@ -1,16 +1,24 @@
 // mla_decode.cu -- absorbed latent attention of a few new tokens over a paged cache.
 //
 //   s_j = scale q . c_j,  o = sum_j softmax_j(s) c_j[0:512]
-// Every query head of a latent group reads the same cached rows (1152 B each in bfloat16), so a
-// row is brought in once for up to 64 (token, head) columns and the kernel is bound by the cache's
-// bytes: at 32 columns it has 2 (576 + 512) 32 / 1152 = 60 flops a byte, a quarter of what the
-// tensor cores could take.
+// Every query head of a latent group reads the same cached rows (1152 B each in bfloat16, 576 B in
+// e4m3), so a row is brought in once for up to 64 (token, head) columns and the kernel is bound by
+// the cache's bytes: at 32 columns it has 2 (576 + 512) 32 / 1152 = 60 flops a byte, a quarter of
+// what the tensor cores could take.
 //
-// Roles are swapped so that the tensor cores' M is the cached rows, not the few heads, and
-// nothing is padded:
+// Roles are swapped so that the tensor cores' M is the cached rows, not the few heads, and nothing
+// is padded:
 //   S^T [64 rows x NC columns] = C Q^T          (M = 64, K = 576; C as the copy laid it down)
 //   O^T [512 x NC] += C[:, 0:512]^T P^T         (M = 128 four times, K = 64; C read MN-major)
 // The same shared-memory tile is the A operand of both; only P^T (64 x NC) is written by threads.
+//
+// e4m3 rows: S^T is taken on the codes as they lie in the cache.  Q is split into two e4m3 terms
+// at a power-of-two scale of its own for each row, q = t (q1 + q2 / 16): q1 keeps four bits and q2
+// the next four, which is all a bfloat16 has (numbers below 2^-15 of their row's largest keep an
+// absolute 2^-23 of it), so the two terms are further columns of the product (N = 2 NC, kind::f8f6f4,
+// half the instructions of bfloat16) and S^T stays as exact as float32 sums are.  Weights span too
+// many magnitudes to be split like that: for O^T the codes are turned into bfloat16 rows (exact) by
+// eight warps, while the tensor cores and the softmax work on S^T of the same tile.
 //
 // One persistent CTA per SM takes an equal share of all 64-row tiles of all (sequence, group)
 // units in order, so a batch of any lengths is balanced without the host knowing them.  A unit
@@ -20,8 +28,9 @@
 //
 // Warps: 0-3 softmax (S^T in the 16-lane M = 64 layout, running maximum per column, O^T in
 // tensor memory rescaled only when a column's maximum grows by more than 2^8, which float32 sums
-// and a bfloat16 weight hold exactly as well); 4 copies (TMA, 16 KB pairs of 64 x 64 blocks through
-// a ring); 5 issues S^T block by block as it arrives; 6 issues O^T and frees the ring; 7 loads Q.
+// and a bfloat16 weight hold exactly as well); 4 copies (TMA: half a tile of bfloat16 rows or a
+// whole one of codes at a time); 5 issues S^T; 6 issues O^T and frees the rows; 7 loads Q; 8-15
+// (e4m3) Q's terms and the bfloat16 rows.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -38,9 +47,8 @@ constexpr int kConv = 8;  // warps that turn codes into bfloat16 rows
 template <bool kE4M3>
 constexpr int kThreads = kE4M3 ? 256 + kConv * 32 : 256;
 constexpr int kTok = 64;                    // cached rows a tile
-constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 64 numbers, 128-byte swizzle
-constexpr uint32_t kPair = 2 * kBlk;        // 128 latent numbers: the M of one O^T product
-constexpr int kPairs = kDL / 128;           // pairs a tile
+constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 128 bytes, 128-byte swizzle
+constexpr int kPairs = kDL / 128;           // 128 latent numbers: the M of one O^T product
 constexpr float kGrow = 8.0f;               // log2 by which a maximum may grow without rescaling
 
 struct DecArgs {
@@ -51,15 +59,16 @@ struct DecArgs {
     const int32_t *block_table, *kv_lens;
     __nv_bfloat16 *o;
     float *lse;
-    float *part_o, *part_lse;  // [CTA][2][NC][512], [CTA][2][NC]
-    int2 *meta;                // [unit][CT]: first share, 2 * shares + (the first starts inside its share)
+    float *part_o, *part_lse;  // [CTA][2][4][NC / 4][128][4] (pair, column / 4, number, column % 4), [CTA][2][NC]
+    int2 *meta;                // [unit][CT]: 2 * first share + (it starts inside that share), last share
     unsigned int *status;
 };
 
-// The cache as [block of 64 numbers][pool row][group][64], so that one copy brings a pair of
-// blocks (or the rope block) of up to 64 rows as the products read them; and q as [block][row][64].
+// bfloat16: the cache as [block of 64 numbers][pool row][group][64], so that one copy brings half a
+// tile (or the rope block) as the products read it; e4m3: [block of 128 codes][pool row][group]
+// [128], and the rope part.  q as [block][row][64].
 struct DecMaps {
-    CUtensorMap pair, rope, q;
+    CUtensorMap latent, rope, q;
     int rows;    // pool rows a copy: min(page_size, 64)
     int q_rows;  // rows of q a copy
 };
@@ -74,7 +83,8 @@ __device__ __forceinline__ int tiles_of(const DecArgs &a, int n)
 // One CTA's share of the tiles, piece by piece; a piece is a run of tiles of one unit.
 struct Pieces {
     int n, g, t, tiles, take;  // current piece: sequence, group, first tile, the unit's tiles, tiles taken
-    int64_t left, pos;         // tiles left behind the current piece; place of the piece's first tile
+    int64_t left;              // tiles left behind the current piece
+    bool inside;               // the piece's unit starts inside the share
     __device__ __forceinline__ void settle(const DecArgs &a)
     {
         while (n < a.N && (tiles = tiles_of(a, n)) == 0) {
@@ -86,36 +96,44 @@ struct Pieces {
     }
     __device__ __forceinline__ void next(const DecArgs &a)
     {
-        pos += take;
         t = 0;
+        inside = true;
         if (++g == a.G) {
             g = 0;
             ++n;
         }
         settle(a);
     }
+    __device__ __forceinline__ bool whole() const { return take == tiles; }
 };
 
 template <int NC, bool kE4M3>
 struct DecSmem {
-    // pairs and rope blocks of bfloat16 rows held, and pairs of blocks of codes in flight
-    static constexpr int kRing = kE4M3 ? (NC == 64 ? 5 : 7) : (NC == 64 ? 8 : 10);
-    static constexpr int kRopes = kE4M3 ? 1 : (NC == 64 ? 2 : 3);
-    static constexpr int kStage = kE4M3 ? (NC == 64 ? 6 : 8) : 1;
-    alignas(1024) unsigned char pair[kRing][kPair];
-    alignas(1024) unsigned char rope[kRopes][kBlk];
-    alignas(1024) unsigned char q[kDC / 64][NC * 128];
+    // bfloat16: half tiles and rope blocks in flight.  e4m3: tiles of codes in flight, pairs of
+    // blocks of bfloat16 rows held.
+    static constexpr int kRing = kE4M3 ? 4 : (NC == 64 ? 4 : 5);
+    static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 3;
+    static constexpr int kStage = kE4M3 ? (NC == 64 ? 2 : 3) : 1;
+    static constexpr uint32_t kSlot = (kE4M3 ? 2 : 4) * kBlk;
+    static constexpr uint32_t kCodes = 4 * kBlk + kBlk / 2;  // a tile of codes: 4 x 128, then 64
+    static constexpr int kSW = kE4M3 ? 2 * NC : NC;          // columns of S^T
+    alignas(1024) unsigned char ring[kRing][kSlot];
+    alignas(1024) unsigned char rope[kRopes][kE4M3 ? 16 : kBlk];
+    // bfloat16: [9 blocks][NC rows][128 B]; e4m3: [4 blocks][2 NC rows][128 B], [2 NC rows][64 B]
+    alignas(1024) unsigned char q[kE4M3 ? 2 * NC * kDC : NC * kDC * 2];
     alignas(1024) unsigned char p[kTok * NC * 2];
-    alignas(1024) unsigned char stage[kStage][kE4M3 ? kBlk : 16];
-    float red[4][NC];  // per warp: column maxima, then column sums
-    float fac[NC];     // per column: rescaling factor, then 1 / sum
-    uint64_t full_pair[kRing], empty_pair[kRing], full_rope[kRopes], empty_rope[kRopes];
+    alignas(1024) unsigned char stage[kStage][kE4M3 ? kCodes : 16];
+    alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
+    float fac[NC], top[NC];  // per column: rescaling factor, then 1 / sum; maximum
+    int row[NC];            // output row of a column, less the sequence's and group's first
+    float q_scale[kE4M3 ? 4 : 1][NC];  // by piece: Q's row scales t
+    uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
     uint64_t full_stage[kStage], empty_stage[kStage];
     uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, q_empty;
     uint32_t tmem_slot;
     int64_t find[40];
-    int64_t share[3];  // begin, end of the CTA's share; tiles a share
-    int first[3];      // n, g, t of its first tile
+    int64_t share[2];  // first tile and tiles of the CTA's share
+    int first[4];      // n, g, t of its first tile; whether that is the unit's first
 };
 
 // Four e4m3 codes as bfloat16 pairs: exact, NaN codes stay NaN.
@@ -125,6 +143,16 @@ __device__ __forceinline__ uint2 decode4(uint32_t w)
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
     const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
     return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
+}
+
+// Two numbers as e4m3 codes of their first (lo 16 bits) and second term.
+__device__ __forceinline__ uint32_t terms2(float2 x)
+{
+    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
+    const __nv_fp8x2_storage_t b =
+        __nv_cvt_float2_to_fp8x2(make_float2((x.x - f.x) * 16.0f, (x.y - f.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+    return (uint32_t)a | ((uint32_t)b << 16);
 }
 
 template <int NC, bool kE4M3>
@@ -137,33 +165,39 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     SM &sm = *reinterpret_cast<SM *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int share = blockIdx.x / a.CT, ct = blockIdx.x % a.CT, Hg = a.H / a.G, cols = a.Sq * Hg;
-    constexpr uint32_t kTmemCols = NC == 64 ? 512 : 256;
+    constexpr uint32_t kTmemCols = 2 * SM::kSW + 4 * NC <= 256 ? 256 : 512;
+    constexpr uint32_t kColO = 2 * SM::kSW;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
     if (tid == 0) {
         for (int i = 0; i < SM::kRing; ++i) {
-            mbar_init(&sm.full_pair[i], kE4M3 ? kConv * 32 : 1);
-            mbar_init(&sm.empty_pair[i], 1);
+            mbar_init(&sm.full[i], kE4M3 ? kConv : 1);
+            mbar_init(&sm.empty[i], 1);
         }
         for (int i = 0; i < SM::kRopes; ++i) {
-            mbar_init(&sm.full_rope[i], kE4M3 ? kConv * 32 : 1);
+            mbar_init(&sm.full_rope[i], 1);
             mbar_init(&sm.empty_rope[i], 1);
         }
         for (int i = 0; i < SM::kStage; ++i) {
             mbar_init(&sm.full_stage[i], 1);
-            mbar_init(&sm.empty_stage[i], kConv);
+            mbar_init(&sm.empty_stage[i], 1 + kConv);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
         }
-        mbar_init(&sm.p_full, 128);
+        mbar_init(&sm.p_full, 4);
         mbar_init(&sm.pv_done, 1);
-        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_full, kE4M3 ? kConv : 1);
         mbar_init(&sm.q_empty, 1);
         fence_mbar_init_cluster();
     }
     if (warp == 4)
         tc::tmem_alloc(&sm.tmem_slot, kTmemCols);
+    if (tid >= 160 && tid < 160 + NC) {
+        const int c = tid - 160, cg = ct * NC + c;
+        sm.row[c] = cg / Hg * a.H + cg % Hg;
+    }
     // this CTA's share: all tiles, then the unit that its first one falls in
     {
         int64_t mine = 0;
@@ -174,21 +208,21 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             bad |= t == 0 && a.kv_lens[n] != 0;
             if (t == 0 && n % a.shares == share)  // nobody's piece: the join writes its (empty) result
                 for (int g = 0; g < a.G; ++g)
-                    a.meta[((int64_t)n * a.G + g) * a.CT + ct] = make_int2(0, 0);
+                    a.meta[((int64_t)n * a.G + g) * a.CT + ct] = make_int2(0, -1);
         }
         if (bad)
             report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        const int64_t all = cta_sum<kT>(mine, sm.find);
-        const int64_t total = all * a.G, per = (total + a.shares - 1) / a.shares;
+        const int64_t total = cta_sum<kT>(mine, sm.find) * a.G;
+        const int64_t per = total < 0x7fffffff - a.shares ? (uint32_t)(total + a.shares - 1) / (uint32_t)a.shares
+                                                          : (total + a.shares - 1) / a.shares;
         const int64_t begin = min(total, share * per), end = min(total, begin + per);
         Item it{0, 0};
         if (begin < end)
             find_item<kT>(a.N, begin, [&](int n) { return tiles_of(a, n) * a.G; }, it, sm.find);
         if (tid == 0) {
-            sm.share[0] = begin;
-            sm.share[1] = end;
-            sm.share[2] = per;
             const int tiles = begin < end ? tiles_of(a, it.seq) : 1;
+            sm.share[0] = begin;
+            sm.share[1] = end - begin;
             sm.first[0] = it.seq;
             sm.first[1] = it.k / tiles;
             sm.first[2] = it.k % tiles;
@@ -198,13 +232,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_slot;
-    const int64_t begin = sm.share[0], end = sm.share[1], per = sm.share[2];
     Pieces w;
     w.n = sm.first[0], w.g = sm.first[1], w.t = sm.first[2];
-    w.pos = begin;
-    w.left = end - begin;
+    w.left = sm.share[1];
     w.take = 0;
-    if (begin < end)
+    w.inside = false;
+    if (w.left > 0)
         w.settle(a);
     Waits wait{a.status, false};
 
@@ -245,56 +278,62 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         }
                     }
                 }
-                constexpr uint32_t kRow = kE4M3 ? 64 : 128;  // bytes of a block's row
-                const uint32_t bytes = (uint32_t)(live * maps.rows) * kRow;
-                // n blocks from `block` on; pages of 64 rows and more take one copy
-                auto copy = [&](unsigned char *dst, int block, int n, uint64_t *bar) {
-                    mbar_arrive_expect_tx(bar, n * bytes);
+                const uint32_t bytes = (uint32_t)(live * maps.rows) * 128u;
+                // four blocks from `block` on; pages of 64 rows and more take one copy
+                auto half = [&](unsigned char *dst, int block, uint64_t *bar) {
                     if (ppt == 1) {
                         if (at[0] >= 0)
-                            tma_load_4d(dst, n == 2 ? &maps.pair : &maps.rope, 0, w.g, at[0], block, bar);
+                            tma_load_4d(dst, &maps.latent, 0, w.g, at[0], block, bar);
                         return;
                     }
-                    for (int i = 0; i < n; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             if (at[b] >= 0)
-                                tma_load_4d(dst + i * kTok * kRow + b * maps.rows * kRow, &maps.rope, 0, w.g, at[b],
-                                            block + i, bar);
+                                tma_load_4d(dst + i * kBlk + b * maps.rows * 128, &maps.latent, 0, w.g, at[b], block + i,
+                                            bar);
+                };
+                auto rope = [&](unsigned char *dst, int row_bytes, uint64_t *bar) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (at[b] >= 0)
+                            tma_load_3d(dst + b * maps.rows * row_bytes, &maps.rope, 0, w.g, at[b], bar);
                 };
                 if constexpr (kE4M3) {
-#pragma unroll
-                    for (int j = 0; j <= kPairs; ++j, rst.step()) {
-                        if (rst.round > 0)
-                            wait(&sm.empty_stage[rst.slot], (rst.round - 1) & 1);
-                        if (!wait.dead && elect())
-                            copy(sm.stage[rst.slot], j == 0 ? 2 * kPairs : 2 * (j - 1), j == 0 ? 1 : 2,
-                                 &sm.full_stage[rst.slot]);
+                    if (rst.round > 0)
+                        wait(&sm.empty_stage[rst.slot], (rst.round - 1) & 1);
+                    if (!wait.dead && elect()) {
+                        mbar_arrive_expect_tx(&sm.full_stage[rst.slot], 4 * bytes + bytes / 2);
+                        rope(sm.stage[rst.slot] + 4 * kBlk, 64, &sm.full_stage[rst.slot]);
+                        half(sm.stage[rst.slot], 0, &sm.full_stage[rst.slot]);
                     }
+                    rst.step();
                 } else {
                     if (rr.round > 0)
                         wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
-                    if (!wait.dead && elect())
-                        copy(sm.rope[rr.slot], 2 * kPairs, 1, &sm.full_rope[rr.slot]);
+                    if (!wait.dead && elect()) {
+                        mbar_arrive_expect_tx(&sm.full_rope[rr.slot], bytes);
+                        rope(sm.rope[rr.slot], 128, &sm.full_rope[rr.slot]);
+                    }
                     rr.step();
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j, rp.step()) {
+                    for (int j = 0; j < 2; ++j, rp.step()) {
                         if (rp.round > 0)
-                            wait(&sm.empty_pair[rp.slot], (rp.round - 1) & 1);
-                        if (!wait.dead && elect())
-                            copy(sm.pair[rp.slot], 2 * j, 2, &sm.full_pair[rp.slot]);
+                            wait(&sm.empty[rp.slot], (rp.round - 1) & 1);
+                        if (!wait.dead && elect()) {
+                            mbar_arrive_expect_tx(&sm.full[rp.slot], 4 * bytes);
+                            half(sm.ring[rp.slot], 4 * j, &sm.full[rp.slot]);
+                        }
                     }
                 }
                 wait.dead = __any_sync(0xffffffffu, wait.dead);
             }
         }
     } else if (warp == 5) {
-        // ---------------- S^T = C Q^T, block by block as the tile arrives (rope first)
-        constexpr uint32_t id = tc::idesc_bf16(64, NC, false, false);
-        const Desc rope(smem_u32(sm.rope[0]), 16, 1024, tc::kSw128), pair(smem_u32(sm.pair[0]), 16, 1024, tc::kSw128),
-            qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128);
+        // ---------------- S^T = C Q^T
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
+        Ring<SM::kStage> rst;
         Ring<2> rs;
         uint32_t nq = 0;
         for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
@@ -302,31 +341,55 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             for (int t = 0; t < w.take && !wait.dead; ++t, rs.step()) {
                 if (rs.round > 0)
                     wait(&sm.s_empty[rs.slot], (rs.round - 1) & 1);
-                const uint32_t d = tmem + rs.slot * NC;
-                wait(&sm.full_rope[rr.slot], rr.round & 1);
-                tc::fence_after_sync();
-                if (elect()) {
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc::mma_bf16(d, rope.at(rr.slot * kBlk + ks * 32), qd.at((kDC / 64 - 1) * NC * 128 + ks * 32), id,
-                                     ks > 0 ? 1u : 0u);
-                    tc::commit(&sm.empty_rope[rr.slot]);
-                }
-                rr.step();
-#pragma unroll
-                for (int j = 0; j < kPairs; ++j, rp.step()) {
-                    wait(&sm.full_pair[rp.slot], rp.round & 1);
+                const uint32_t d = tmem + rs.slot * SM::kSW;
+                if constexpr (kE4M3) {
+                    constexpr uint32_t id = tc::idesc_e4m3(64, SM::kSW);
+                    const Desc cd(smem_u32(sm.stage[0]), 16, 1024, tc::kSw128), qd(smem_u32(sm.q), 16, 1024, tc::kSw128),
+                        cr(smem_u32(sm.stage[0]), 16, 512, tc::kSw64), qr(smem_u32(sm.q), 16, 512, tc::kSw64);
+                    wait(&sm.full_stage[rst.slot], rst.round & 1);
                     tc::fence_after_sync();
                     if (elect()) {
-                        const uint32_t c0 = rp.slot * kPair;
+                        const uint32_t c0 = rst.slot * SM::kCodes;
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc::mma_bf16(d, pair.at(c0 + (ks >> 2) * kBlk + (ks & 3) * 32),
-                                         qd.at((2 * j + (ks >> 2)) * NC * 128 + (ks & 3) * 32), id, 1u);
+                        for (int ks = 0; ks < 16; ++ks)
+                            tc::mma_f8(d, cd.at(c0 + (ks >> 2) * kBlk + (ks & 3) * 32),
+                                       qd.at((ks >> 2) * SM::kSW * 128 + (ks & 3) * 32), id, ks > 0 ? 1u : 0u);
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks)
+                            tc::mma_f8(d, cr.at(c0 + 4 * kBlk + ks * 32), qr.at(4 * SM::kSW * 128 + ks * 32), id, 1u);
+                        tc::commit(&sm.empty_stage[rst.slot]);
+                        tc::commit(&sm.s_full[rs.slot]);
+                    }
+                    rst.step();
+                } else {
+                    constexpr uint32_t id = tc::idesc_bf16(64, NC, false, false);
+                    const Desc rope(smem_u32(sm.rope[0]), 16, 1024, tc::kSw128),
+                        cd(smem_u32(sm.ring[0]), 16, 1024, tc::kSw128), qd(smem_u32(sm.q), 16, 1024, tc::kSw128);
+                    wait(&sm.full_rope[rr.slot], rr.round & 1);
+                    tc::fence_after_sync();
+                    if (elect()) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16(d, rope.at(rr.slot * kBlk + ks * 32),
+                                         qd.at((kDC / 64 - 1) * NC * 128 + ks * 32), id, ks > 0 ? 1u : 0u);
+                        tc::commit(&sm.empty_rope[rr.slot]);
+                    }
+                    rr.step();
+#pragma unroll
+                    for (int j = 0; j < 2; ++j, rp.step()) {
+                        wait(&sm.full[rp.slot], rp.round & 1);
+                        tc::fence_after_sync();
+                        if (elect()) {
+                            const uint32_t c0 = rp.slot * SM::kSlot;
+#pragma unroll
+                            for (int ks = 0; ks < 16; ++ks)
+                                tc::mma_bf16(d, cd.at(c0 + (ks >> 2) * kBlk + (ks & 3) * 32),
+                                             qd.at((4 * j + (ks >> 2)) * NC * 128 + (ks & 3) * 32), id, 1u);
+                            if (j == 1)
+                                tc::commit(&sm.s_full[rs.slot]);
+                        }
                     }
                 }
-                if (elect())
-                    tc::commit(&sm.s_full[rs.slot]);
             }
             if (elect())
                 tc::commit(&sm.q_empty);
@@ -334,7 +397,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     } else if (warp == 6) {
         // ---------------- O^T += C^T P^T, 128 latent numbers at a time
         constexpr uint32_t id = tc::idesc_bf16(128, NC, true, true);
-        const Desc pair(smem_u32(sm.pair[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p));
+        constexpr int kPerSlot = SM::kSlot / (2 * kBlk);
+        const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p));
         Ring<SM::kRing> rp;
         uint32_t nt = 0;
         for (; w.take > 0 && !wait.dead; w.next(a))
@@ -342,92 +406,152 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 wait(&sm.p_full, nt & 1);
                 tc::fence_after_sync();
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j, rp.step())
+                for (int j = 0; j < kPairs / kPerSlot; ++j, rp.step()) {
+                    if (kE4M3) {
+                        wait(&sm.full[rp.slot], rp.round & 1);
+                        tc::fence_after_sync();
+                    }
                     if (elect()) {
-                        const uint32_t c0 = rp.slot * kPair;
+                        const uint32_t c0 = rp.slot * SM::kSlot;
 #pragma unroll
-                        for (int ks = 0; ks < kTok / 16; ++ks)
-                            tc::mma_bf16(tmem + (2 + j) * NC, pair.at(c0 + ks * 2048), pd.at(ks * kPStep<NC>), id,
-                                         t > 0 || ks > 0 ? 1u : 0u);
-                        tc::commit(&sm.empty_pair[rp.slot]);
-                        if (j == kPairs - 1)
+                        for (int k = 0; k < kPerSlot * 4; ++k)
+                            tc::mma_bf16(tmem + kColO + (j * kPerSlot + (k >> 2)) * NC,
+                                         cd.at(c0 + (k >> 2) * 2 * kBlk + (k & 3) * 2048), pd.at((k & 3) * kPStep<NC>), id,
+                                         t > 0 || (k & 3) > 0 ? 1u : 0u);
+                        tc::commit(&sm.empty[rp.slot]);
+                        if (j == kPairs / kPerSlot - 1)
                             tc::commit(&sm.pv_done);
                     }
+                }
             }
     } else if (warp == 7) {
-        // ---------------- Q of each piece: NC columns (token, head) x 576, K-major blocks of 64.
-        // Columns behind the last hold other rows of q or nothing; they stay columns of their own.
+        // ---------------- bfloat16 Q of each piece: NC columns (token, head) x 576, K-major blocks
+        // of 64.  Columns behind the last hold other rows of q or nothing; they stay columns of
+        // their own.
+        if constexpr (!kE4M3) {
+            uint32_t nq = 0;
+            for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
+                if (nq > 0)
+                    wait(&sm.q_empty, (nq - 1) & 1);
+                if (wait.dead)
+                    break;
+                if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
+                    if (elect()) {
+                        mbar_arrive_expect_tx(&sm.q_full, kDC / 64 * NC * 128);
+                        tma_load_3d(sm.q, &maps.q, 0, w.n * cols + ct * NC, 0, &sm.q_full);
+                    }
+                } else {
+                    const int n = (min(cols - ct * NC, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
+                    if (elect())
+                        mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n * maps.q_rows) * kDC * 2);
+                    __syncwarp();
+                    for (int i = lane; i < n * (kDC / 64); i += 32) {
+                        const int c = i / (kDC / 64) * maps.q_rows, blk = i % (kDC / 64);
+                        const int r = w.n * a.Sq * a.H + w.g * Hg + sm.row[c];
+                        tma_load_3d(sm.q + blk * NC * 128 + c * 128, &maps.q, 0, r, blk, &sm.q_full);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (kE4M3 && warp >= 8) {
+        const int cw = warp - 8;
+        Ring<SM::kRing> rp;
+        Ring<SM::kStage> rst;
         uint32_t nq = 0;
         for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
+            // ---------------- Q's two terms: a warp takes a column at a time
             if (nq > 0)
                 wait(&sm.q_empty, (nq - 1) & 1);
             if (wait.dead)
                 break;
-            const int left = cols - ct * NC;
-            if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
-                if (elect()) {
-                    mbar_arrive_expect_tx(&sm.q_full, kDC / 64 * NC * 128);
-                    tma_load_3d(sm.q[0], &maps.q, 0, w.n * cols + ct * NC, 0, &sm.q_full);
-                }
-            } else {
-                const int n = (min(left, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
-                if (elect())
-                    mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n * maps.q_rows) * kDC * 2);
-                __syncwarp();
-                for (int i = lane; i < n * (kDC / 64); i += 32) {
-                    const int c = i / (kDC / 64) * maps.q_rows, blk = i % (kDC / 64), cg = ct * NC + c;
-                    const int r = (w.n * a.Sq + cg / Hg) * a.H + w.g * Hg + cg % Hg;
-                    tma_load_3d(sm.q[blk] + c * 128, &maps.q, 0, r, blk, &sm.q_full);
-                }
-                __syncwarp();
-            }
-        }
-    } else if (kE4M3 && warp >= 8) {
-        // ---------------- codes to bfloat16 rows: 8 rows x 4 vectors of 16 codes a warp, so that
-        // both the swizzled reads and the swizzled writes touch every bank once
-        static_assert(kConv * 8 == kTok, "one pass of the warps covers a block's rows");
-        const int chunk = lane >> 3;
-        Ring<SM::kRing> rp;
-        Ring<SM::kRopes> rr;
-        Ring<SM::kStage> rst;
-        for (; w.take > 0 && !wait.dead; w.next(a)) {
-            const int len = a.kv_lens[w.n];
-            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t) {
-                const int rows = len - t * kTok;
+            const __nv_bfloat16 *q0 = a.q + ((int64_t)w.n * a.Sq * a.H + w.g * Hg) * kDC;
+#pragma unroll 2
+            for (int c = cw; c < NC; c += kConv) {
+                uint4 x[3];
+                uint32_t mx = 0;
 #pragma unroll
-                for (int j = 0; j <= kPairs; ++j, rst.step()) {  // the rope block, then the pairs
-                    unsigned char *dst = j == 0 ? sm.rope[rr.slot] : sm.pair[rp.slot];
-                    if (j == 0 && rr.round > 0)
-                        wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
-                    if (j > 0 && rp.round > 0)
-                        wait(&sm.empty_pair[rp.slot], (rp.round - 1) & 1);
-                    wait(&sm.full_stage[rst.slot], rst.round & 1);
+                for (int i = 0; i < 3; ++i) {
+                    const int v = lane + 32 * i;
+                    x[i] = ct * NC + c < cols && v < kDC / 8
+                               ? reinterpret_cast<const uint4 *>(q0 + (int64_t)sm.row[c] * kDC)[v]
+                               : make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx = max(mx, max(u[k] << 16 & 0x7fffffffu, u[k] & 0x7fff0000u));
+                }
+                // t = 2^e with max|q| < 256 t, and t, 1 / t normal numbers; a row with an infinity or a
+                // NaN gets a NaN for its scale
+                mx = __reduce_max_sync(0xffffffffu, mx);
+                const int e = max((int)(mx >> 23) - 127 - 7, -100);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                if (lane == 0)
+                    sm.q_scale[nq & 3][c] = mx >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                              : __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int v = lane + 32 * i;
+                    if (v >= kDC / 8)
+                        break;
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = unpack_bf16x2(u[k]);
+                        r[k] = terms2(make_float2(f.x * inv, f.y * inv));
+                    }
+                    const uint2 t1 = make_uint2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410));
+                    const uint2 t2 = make_uint2(__byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int r = k * NC + c, vr = v - 64;
+                        unsigned char *dst =
+                            i < 2 ? sm.q + (v >> 4) * SM::kSW * 128 + r * 128 + ((((v & 15) >> 1) ^ (r & 7)) << 4) + (v & 1) * 8
+                                  : sm.q + 4 * SM::kSW * 128 + r * 64 + (((vr >> 1) ^ ((r >> 1) & 3)) << 4) + (vr & 1) * 8;
+                        *reinterpret_cast<uint2 *>(dst) = k ? t2 : t1;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.q_full);
+            // ---------------- codes to bfloat16 rows: 8 rows x 4 vectors of 16 codes at a time, so
+            // that both the swizzled reads and the swizzled writes touch every bank once
+            static_assert(kConv * 8 == kTok, "one pass of the warps covers a block's rows");
+            const int len = a.kv_lens[w.n], row = cw * 8 + (lane & 7);
+            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t, rst.step()) {
+                const bool live = row < len - t * kTok;  // behind the sequence's end: anything may be there
+                wait(&sm.full_stage[rst.slot], rst.round & 1);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j, rp.step()) {
+                    if (rp.round > 0)
+                        wait(&sm.empty[rp.slot], (rp.round - 1) & 1);
                     uint4 c[2];
 #pragma unroll
-                    for (int i = 0; i < (j == 0 ? 1 : 2); ++i) {
-                        const int row = (warp - 8) * 8 + (lane & 7);
-                        c[i] = *reinterpret_cast<const uint4 *>(sm.stage[rst.slot] + i * kBlk / 2 + row * 64 +
-                                                                ((chunk ^ ((row >> 1) & 3)) << 4));
-                        if (row >= rows)  // behind the sequence's end: anything may be there
+                    for (int i = 0; i < 2; ++i) {
+                        const int chunk = i * 4 + (lane >> 3);
+                        c[i] = *reinterpret_cast<const uint4 *>(sm.stage[rst.slot] + j * kBlk + row * 128 +
+                                                                ((chunk ^ (row & 7)) << 4));
+                        if (!live)
                             c[i] = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int i = 0; i < (j == 0 ? 1 : 2); ++i) {
-                        const int row = (warp - 8) * 8 + (lane & 7);
+                    for (int i = 0; i < 2; ++i) {
+                        const int chunk = lane >> 3;
                         const uint2 x = decode4(c[i].x), y = decode4(c[i].y), z = decode4(c[i].z), u = decode4(c[i].w);
-                        unsigned char *p = dst + i * kBlk + row * 128;
+                        unsigned char *p = sm.ring[rp.slot] + i * kBlk + row * 128;
                         *reinterpret_cast<uint4 *>(p + (((2 * chunk) ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
                         *reinterpret_cast<uint4 *>(p + (((2 * chunk + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, u.x, u.y);
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sm.empty_stage[rst.slot]);
                     fence_proxy_async_smem();
-                    mbar_arrive(j == 0 ? &sm.full_rope[rr.slot] : &sm.full_pair[rp.slot]);
-                    if (j == 0)
-                        rr.step();
-                    else
-                        rp.step();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.full[rp.slot]);
+                        if (j == kPairs - 1)
+                            mbar_arrive(&sm.empty_stage[rst.slot]);
+                    }
                 }
             }
         }
@@ -436,17 +560,18 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         constexpr int J = NC / 8;
         const int r0 = warp * 16 + (lane >> 2);
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)warp * 32, 0);
-        uint32_t nt = 0, np = 0;
-        for (; w.take > 0; w.next(a)) {
+        uint32_t nt = 0, nq = 0;
+        Ring<SM::kRing> rp;
+        for (; w.take > 0; w.next(a), ++nq) {
             const int len = a.kv_lens[w.n];
-            float m[2 * J], l[2 * J];
+            float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1];
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 // columns behind the last: weights 0, and no say in when to rescale
                 m[i] = ct * NC + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1) < cols ? -INFINITY : INFINITY;
                 l[i] = 0.0f;
             }
-            for (int t = w.t; t < w.t + w.take; ++t, ++nt, np += kPairs) {
+            for (int t = w.t; t < w.t + w.take; ++t, ++nt) {
                 const uint32_t sb = nt & 1;
                 float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
                 if constexpr (kE4M3) {
@@ -460,7 +585,15 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 wait(&sm.s_full[sb], (nt / 2) & 1);
                 tc::fence_after_sync();
                 float s[J][4];
-                load_s<NC>(lane_base + sb * NC, s);
+                if constexpr (kE4M3) {
+                    if (t == w.t)
+#pragma unroll
+                        for (int i = 0; i < 2 * J; ++i)
+                            qs[i] = sm.q_scale[nq & 3][8 * (i >> 1) + 2 * (lane & 3) + (i & 1)] * a.scale_log2;
+                    load_s2<NC>(lane_base + sb * SM::kSW, s);
+                } else {
+                    load_s<NC>(lane_base + sb * SM::kSW, s);
+                }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
@@ -471,10 +604,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 for (int j = 0; j < J; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float x = s[j][i] * (kE4M3 ? a.scale_log2 * page_scale : a.scale_log2);
+                        float x = s[j][i] * (kE4M3 ? qs[2 * j + (i & 1)] * page_scale : a.scale_log2);
                         if (edge) {
                             const int cg = ct * NC + 8 * j + 2 * (lane & 3) + (i & 1);
-                            const int last = len - a.Sq + min(cg / Hg, a.Sq - 1);
+                            const int last = len - a.Sq + (a.Sq == 1 ? 0 : min(cg / Hg, a.Sq - 1));
                             if (t * kTok + r0 + (i >> 1) * 8 > last)
                                 x = -INFINITY;
                         }
@@ -512,12 +645,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll 1
                         for (int b = 0; b < kPairs * NC / 16; ++b) {
                             uint32_t y[16];
-                            tc::ld_32x32b_x16(lane_base + 2 * NC + b * 16, y);
+                            tc::ld_32x32b_x16(lane_base + kColO + b * 16, y);
                             tc::wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.fac[b * 16 % NC + i]);
-                            tc::st_32x32b_x16(lane_base + 2 * NC + b * 16, y);
+                            tc::st_32x32b_x16(lane_base + kColO + b * 16, y);
                         }
                         tc::wait_st();
                     }
@@ -540,72 +673,94 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                     *reinterpret_cast<uint32_t *>(sm.p + p_off<NC>(r0 + 8, c)) =
                         pack_bf16x2(s[j][2] * page_scale, s[j][3] * page_scale);
                 }
-                // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
-                const int rows = len - t * kTok;
-                if (!kE4M3 && rows < kTok) {
+                if constexpr (!kE4M3) {
+                    // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
+                    const int rows = len - t * kTok;
+                    if (rows < kTok) {
+                        Ring<SM::kRing> rz = rp;
 #pragma unroll
-                    for (int j = 0; j < kPairs; ++j) {
-                        const uint32_t sl = (np + j) % SM::kRing;
-                        wait(&sm.full_pair[sl], ((np + j) / SM::kRing) & 1);
-                        for (int v = tid; v < (kTok - rows) * 16; v += 128)
-                            *reinterpret_cast<uint4 *>(sm.pair[sl] + (v & 8 ? kBlk : 0) + (rows + v / 16) * 128 +
-                                                       (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < 2; ++j, rz.step()) {
+                            wait(&sm.full[rz.slot], rz.round & 1);
+                            for (int v = tid; v < (kTok - rows) * 32; v += 128)
+                                *reinterpret_cast<uint4 *>(sm.ring[rz.slot] + (v >> 3 & 3) * kBlk + (rows + v / 32) * 128 +
+                                                           (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
                     }
+                    rp.step();
+                    rp.step();
                 }
                 fence_proxy_async_smem();
                 tc::fence_before_sync();
-                mbar_arrive(&sm.p_full);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.p_full);
             }
             // ---- the piece's sums, and its result
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
+                const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-                if (lane < 4)
-                    sm.red[warp][8 * (i >> 1) + 2 * lane + (i & 1)] = l[i];
-            }
-            softmax_sync();
-            const bool whole = w.take == w.tiles;
-            const int64_t unit = (int64_t)w.n * a.G + w.g, start = w.pos - w.t;  // place of the unit's first tile
-            const int64_t slot = (int64_t)blockIdx.x * 2 + (start <= begin ? 0 : 1);
-            if (warp == 0 && lane < 4) {
-#pragma unroll
-                for (int i = 0; i < 2 * J; ++i) {
-                    const int c = 8 * (i >> 1) + 2 * lane + (i & 1), cg = ct * NC + c;
-                    const float sum = sm.red[0][c] + sm.red[1][c] + sm.red[2][c] + sm.red[3][c];
-                    const float lse2 = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
-                    sm.fac[c] = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    if (!whole)
-                        a.part_lse[slot * NC + c] = lse2;
-                    else if (a.lse && cg < cols)
-                        a.lse[((int64_t)w.n * a.Sq + cg / Hg) * a.H + w.g * Hg + cg % Hg] = lse2 * kLn2;
+                if (lane < 4) {
+                    sm.red[warp][c] = l[i];
+                    if (warp == 0)
+                        sm.top[c] = m[i];
                 }
             }
-            if (tid == 0 && w.t == 0)
-                a.meta[unit * a.CT + ct] =
-                    make_int2((int)(start / per),
-                              2 * (int)((start + w.tiles - 1) / per - start / per + 1) + (start % per != 0 ? 1 : 0));
+            softmax_sync();
+            const bool whole = w.whole();
+            const int64_t unit = (int64_t)w.n * a.G + w.g, slot = (int64_t)blockIdx.x * 2 + (w.inside ? 1 : 0);
+            const int64_t row0 = (int64_t)w.n * a.Sq * a.H + w.g * Hg;
+            if (tid < NC) {
+                const float sum = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
+                const float lse2 = sum == 0.0f ? -INFINITY : sm.top[tid] + log2f(sum);
+                sm.fac[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (!whole)
+                    a.part_lse[slot * NC + tid] = lse2;
+                else if (a.lse && ct * NC + tid < cols)
+                    a.lse[row0 + sm.row[tid]] = lse2 * kLn2;
+            }
+            if (tid == 0) {
+                int *mt = reinterpret_cast<int *>(a.meta + unit * a.CT + ct);
+                if (w.t == 0)
+                    mt[0] = 2 * share + (w.inside ? 1 : 0);
+                if (w.t + w.take == w.tiles)
+                    mt[1] = share;
+            }
             softmax_sync();
             wait(&sm.pv_done, (nt - 1) & 1);
             tc::fence_after_sync();
-            const int dim = warp * 32 + lane;
+            const int dim = warp * 32 + lane, live = cols - ct * NC;
 #pragma unroll 1
             for (int b = 0; b < kPairs * NC / 16; ++b) {
                 uint32_t y[16];
-                tc::ld_32x32b_x16(lane_base + 2 * NC + b * 16, y);
-                tc::wait_ld();
-                const int d = b * 16 / NC * 128 + dim, c0 = b * 16 % NC;
+                tc::ld_32x32b_x16(lane_base + kColO + b * 16, y);
+                const int pair = b * 16 / NC, c0 = b * 16 % NC;
+                float f[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int c = c0 + i, cg = ct * NC + c;
-                    if (cg >= cols)
-                        break;
-                    const float x = sm.fac[c] == 0.0f ? 0.0f : __uint_as_float(y[i]) * sm.fac[c];
-                    if (whole)
-                        a.o[(((int64_t)w.n * a.Sq + cg / Hg) * a.H + w.g * Hg + cg % Hg) * kDL + d] = __float2bfloat16(x);
-                    else
-                        a.part_o[(slot * NC + c) * kDL + d] = x;
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(sm.fac + c0 + i);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    f[i] = f[i] == 0.0f ? 0.0f : __uint_as_float(y[i]) * f[i];
+                if (!whole) {
+                    float *dst = a.part_o + ((slot * kPairs + pair) * (NC / 4) + c0 / 4) * 512 + dim * 4;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4 *>(dst + i * 128) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                } else {
+                    // a lane and its neighbour trade columns, so that each writes two numbers at once
+                    __nv_bfloat16 *dst = a.o + row0 * kDL + pair * 128 + (dim & ~1);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? f[i] : f[i + 1], 1);
+                        const uint32_t v = lane & 1 ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
+                        const int c = c0 + i + (lane & 1);
+                        if (c < live)
+                            *reinterpret_cast<uint32_t *>(dst + (int64_t)sm.row[c] * kDL) = v;
+                    }
                 }
             }
             softmax_sync();  // sm.fac and sm.red are free again
@@ -620,48 +775,71 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 }
 
 // Joins the partial results of the units that several shares cover, and writes the empty result
-// of the units that none does.  One warp per (unit, column); 16 of the 512 numbers a lane.
+// of the units that none does.  128 threads, one latent number each, take four columns of one
+// unit and one pair; the shares' weights are formed once, by the first threads.
+constexpr int kJoinShares = 64;  // weights held at once
+
 template <int NC>
-__global__ void __launch_bounds__(256) mla_decode_join_kernel(DecArgs a)
+__global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
 {
-    const int lane = threadIdx.x & 31, c = blockIdx.y * 8 + (threadIdx.x >> 5);
+    __shared__ __align__(16) float wgt[kJoinShares][4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, c0 = blockIdx.y * 4, pair = blockIdx.z;
     const int64_t uc = blockIdx.x;  // unit * CT + ct
-    const int ct = (int)(uc % a.CT), Hg = a.H / a.G, cg = ct * NC + c;
-    const int64_t unit = uc / a.CT;
     const int2 mt = a.meta[uc];
-    const int count = mt.y >> 1;
-    if (count == 1 || cg >= a.Sq * Hg)
+    const int first = mt.x >> 1, count = mt.y - first + 1;
+    const int ct = (int)(uc % a.CT), Hg = a.H / a.G, left = a.Sq * Hg - ct * NC - c0;
+    if (count == 1 || left <= 0)
         return;
-    const int64_t r = (unit / a.G * a.Sq + cg / Hg) * a.H + unit % a.G * Hg + cg % Hg;
-    float mx = -INFINITY;
-    auto slot_of = [&](int i) { return ((int64_t)(mt.x + i) * a.CT + ct) * 2 + (i == 0 ? mt.y & 1 : 0); };
-    for (int i = 0; i < count; ++i) {
-        const float x = a.part_lse[slot_of(i) * NC + c];
-        mx = x > mx || x != x ? x : mx;
+    const int64_t unit = uc / a.CT, row0 = unit / a.G * a.Sq * a.H + unit % a.G * Hg;
+    auto slot_of = [&](int i) { return ((int64_t)(first + i) * a.CT + ct) * 2 + (i == 0 ? mt.x & 1 : 0); };
+    // warp c: column c's largest lse and the sum of weights
+    const int lane = tid & 31, c = tid >> 5;
+    float top = -INFINITY;
+    for (int i = lane; i < count; i += 32) {
+        const float x = a.part_lse[slot_of(i) * NC + c0 + c];
+        top = x > top || x != x ? x : top;
     }
-    float acc[16] = {}, sum = 0.0f;
-    for (int i = 0; i < count; ++i) {
-        const int64_t s = slot_of(i) * NC + c;
-        const float x = a.part_lse[s], wgt = x == -INFINITY ? 0.0f : ex2(x - mx);
-        sum += wgt;
-        const float4 *p = reinterpret_cast<const float4 *>(a.part_o + s * kDL) + lane;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = p[k * 32];
-            acc[4 * k] += wgt * v.x;
-            acc[4 * k + 1] += wgt * v.y;
-            acc[4 * k + 2] += wgt * v.z;
-            acc[4 * k + 3] += wgt * v.w;
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, top, d);
+        top = x > top || x != x ? x : top;
+    }
+    float sum = 0.0f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < count; i0 += kJoinShares) {
+        const int n = min(kJoinShares, count - i0);
+        for (int i = lane; i < n; i += 32) {
+            const float x = a.part_lse[slot_of(i0 + i) * NC + c0 + c], v = x == -INFINITY ? 0.0f : ex2(x - top);
+            wgt[i][c] = v;
+            sum += v;
         }
+        __syncthreads();
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(
+                a.part_o)[((slot_of(i0 + i) * kPairs + pair) * (NC / 4) + c0 / 4) * 128 + tid];
+            const float4 f = *reinterpret_cast<const float4 *>(wgt[i]);
+            acc[0] += f.x * v.x;
+            acc[1] += f.y * v.y;
+            acc[2] += f.z * v.z;
+            acc[3] += f.w * v.w;
+        }
+        __syncthreads();
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint2 *dst = reinterpret_cast<uint2 *>(a.o + r * kDL) + lane;
+    sum = warp_sum(sum);
+    if (lane == 0)
+        wgt[0][c] = sum;
+    const int cg = ct * NC + c0 + c;
+    if (pair == 0 && a.lse && lane == 0 && c < left)
+        a.lse[row0 + cg / Hg * a.H + cg % Hg] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        dst[k * 32] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                                 pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-    if (a.lse && lane == 0)
-        a.lse[r] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    for (int k = 0; k < 4; ++k) {
+        const int kg = ct * NC + c0 + k;
+        const float s = wgt[0][k];
+        if (k < left)
+            a.o[(row0 + kg / Hg * a.H + kg % Hg) * kDL + pair * 128 + tid] = __float2bfloat16(s == 0.0f ? 0.0f : acc[k] / s);
+    }
 }
 
 int columns(int Sq, int H, int G) { return Sq * (H / G) <= 32 ? 32 : 64; }
@@ -693,16 +871,29 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    // q: runs of columns that are consecutive rows
-    const int Hg = a.H / a.G;
-    maps.q_rows = a.G == 1 ? NC : Hg % 8 == 0 ? 8 : 1;
-    const int64_t extent[3] = {64, (int64_t)a.N * a.Sq * a.H, kDC / 64}, stride[2] = {kDC * 2, 128};
-    const int box[3] = {64, maps.q_rows, maps.q_rows == NC ? kDC / 64 : 1};
-    if ((e = make_map(&maps.q, a.q, 2, 3, extent, stride, box)) != cudaSuccess)
-        return e;
+    if (!kE4M3) {
+        // q: runs of columns that are consecutive rows
+        const int Hg = a.H / a.G;
+        maps.q_rows = a.G == 1 ? NC : Hg % 8 == 0 ? 8 : 1;
+        const int64_t extent[3] = {64, (int64_t)a.N * a.Sq * a.H, kDC / 64}, stride[2] = {kDC * 2, 128};
+        const int box[3] = {64, maps.q_rows, maps.q_rows == NC ? kDC / 64 : 1};
+        if ((e = make_map(&maps.q, a.q, 2, 3, extent, stride, box)) != cudaSuccess)
+            return e;
+    }
     kernel<<<a.shares * a.CT, kThreads<kE4M3>, smem, s>>>(maps, a);
-    mla_decode_join_kernel<NC><<<dim3(a.N * a.G * a.CT, NC / 8), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    // the join waits on the device for the first launch to end, and is set up meanwhile
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(a.N * a.G * a.CT, NC / 4, kPairs);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC>, a);
 }
 
 }  // namespace
@@ -722,15 +913,18 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
               reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int2 *>(ws), device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;
-    DecMaps maps;
+    DecMaps maps{};
     maps.rows = page_size < kTok ? page_size : kTok;
-    const int64_t es = e4m3 ? 1 : 2;
-    const int64_t extent[4] = {64, G, (int64_t)num_pages * page_size, kDC / 64};
-    const int64_t stride[3] = {kDC * es, G * kDC * es, 64 * es};
-    const int pair_box[4] = {64, 1, maps.rows, 2}, rope_box[4] = {64, 1, maps.rows, 1};
-    cudaError_t e = make_map(&maps.pair, cache, (int)es, 4, extent, stride, pair_box);
-    if (e == cudaSuccess)
-        e = make_map(&maps.rope, cache, (int)es, 4, extent, stride, rope_box);
+    const int es = e4m3 ? 1 : 2, block = 128 / es;  // numbers of a 128-byte row
+    const int64_t extent[4] = {block, G, (int64_t)num_pages * page_size, kDL / block};
+    const int64_t stride[3] = {kDC * es, (int64_t)G * kDC * es, 128};
+    const int box[4] = {block, 1, maps.rows, maps.rows == kTok ? 4 : 1};
+    cudaError_t e = make_map(&maps.latent, cache, es, 4, extent, stride, box);
+    if (e == cudaSuccess) {
+        const int64_t rope[3] = {kDR, G, (int64_t)num_pages * page_size};
+        const int rope_box[3] = {kDR, 1, maps.rows};
+        e = make_map(&maps.rope, static_cast<const unsigned char *>(cache) + kDL * es, es, 3, rope, stride, rope_box);
+    }
     if (e != cudaSuccess)
         return e;
     if (e4m3)

@@ -111,6 +111,28 @@ __device__ __forceinline__ void load_s(uint32_t taddr, float (&s)[NC / 8][4])
         s[i / 4][i % 4] = __uint_as_float(r[i]);
 }
 
+// Two such accumulators side by side, the second worth a sixteenth: their sum.
+template <int NC>
+__device__ __forceinline__ void load_s2(uint32_t taddr, float (&s)[NC / 8][4])
+{
+    float t[NC / 8][4];
+    if constexpr (NC == 64) {
+        load_s<64>(taddr, s);
+        load_s<64>(taddr + 64, t);
+    } else {
+        float both[8][4];
+        load_s<64>(taddr, both);
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+            s[i / 4][i % 4] = both[i / 4][i % 4];
+            t[i / 4][i % 4] = both[4 + i / 4][i % 4];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i)
+        s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 0.0625f, s[i / 4][i % 4]);
+}
+
 // cuTensorMapEncodeTiled, reached through the runtime (the library does not link the driver).
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
 {
