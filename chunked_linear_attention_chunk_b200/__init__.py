@@ -12,6 +12,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -575,19 +576,45 @@ def _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale):
             (dn + dr) ** -0.5 if scale is None else float(scale))
 
 
-def _same_device(*ts):
-    dev = next(t.device for t in ts if t is not None)
-    if any(t is not None and t.device != dev for t in ts):
-        raise ValueError("all tensors must be on one device")
+# The wrappers below are called once a layer and token, so they stay lean: one pass over the
+# tensors, raw pointers, and the device made current only where it is not.
+def _mla_device(*ts):
+    """The device that all tensors (None aside) are on; they must be contiguous CUDA tensors."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            _check_cuda(t)
+            raise ValueError("all tensors must be on one device")
+    if dev.type != "cuda":
+        raise ValueError("libkda takes CUDA tensors only")
     return dev
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _mla_call(name, dev, *args):
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != 0:
+        raise KdaError(st, name)
 
 
 def _out(t, shape, dtype, dev, name):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
     return t
+
+
+def _scratch(workspace, need, dev):
+    return torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
 
 
 def kda_mla_fwd(q, kv, k_rope, cu_q, cu_k=None, scale=None, causal: bool = True, o=None, lse=None):
@@ -597,15 +624,12 @@ def kda_mla_fwd(q, kv, k_rope, cu_q, cu_k=None, scale=None, causal: bool = True,
     all its keys, the one before it all but the last, and so on.  ``scale`` defaults to
     192 ** -0.5.  Returns (o [Tq,H,128] bf16, lse [Tq,H] float32)."""
     cu_k = cu_q if cu_k is None else cu_k
-    _check_cuda(q, kv, k_rope, cu_q, cu_k, o, lse)
-    dev = _same_device(q, kv, k_rope, cu_q, cu_k, o, lse)
+    dev = _mla_device(q, kv, k_rope, cu_q, cu_k, o, lse)
     N, Tq, Tk, H, scale = _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale)
     o = _out(o, (Tq, H, MLA_DIMS[2]), torch.bfloat16, dev, "o")
     lse = _out(lse, (Tq, H), torch.float32, dev, "lse")
-    with torch.cuda.device(dev):
-        st = lib().kda_mla_fwd(N, _ptr(cu_q), _ptr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _ptr(q),
-                               _ptr(kv), _ptr(k_rope), _ptr(o), _ptr(lse), _stream(dev))
-    _raise(st, "kda_mla_fwd")
+    _mla_call("kda_mla_fwd", dev, N, _adr(cu_q), _adr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale,
+              _adr(q), _adr(kv), _adr(k_rope), _adr(o), _adr(lse))
     return o, lse
 
 
@@ -619,22 +643,17 @@ def kda_mla_bwd(q, kv, k_rope, o, lse, dO, cu_q, cu_k=None, scale=None, causal: 
     ``out`` may supply some of them."""
     cu_k = cu_q if cu_k is None else cu_k
     out = dict(out or {})
-    _check_cuda(q, kv, k_rope, o, lse, dO, cu_q, cu_k, workspace, *out.values())
-    dev = _same_device(q, kv, k_rope, o, lse, dO, cu_q, cu_k, workspace, *out.values())
+    dev = _mla_device(q, kv, k_rope, o, lse, dO, cu_q, cu_k, workspace, *out.values())
     N, Tq, Tk, H, scale = _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale)
     for name, t in (("o", o), ("dO", dO)):
         _out(t, (Tq, H, MLA_DIMS[2]), torch.bfloat16, dev, name)
     _out(lse, (Tq, H), torch.float32, dev, "lse")
     g = {name: _out(out.get(name), t.shape, torch.bfloat16, dev, name)
          for name, t in (("dq", q), ("dkv", kv), ("dk_rope", k_rope))}
-    if workspace is None:
-        workspace = torch.empty(kda_mla_bwd_workspace(Tq, Tk, H), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        st = lib().kda_mla_bwd(N, _ptr(cu_q), _ptr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _ptr(q),
-                               _ptr(kv), _ptr(k_rope), _ptr(o), _ptr(lse), _ptr(dO), _ptr(g["dq"]), _ptr(g["dkv"]),
-                               _ptr(g["dk_rope"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream(dev))
-    _raise(st, "kda_mla_bwd")
+    ws = _scratch(workspace, kda_mla_bwd_workspace(Tq, Tk, H), dev)
+    _mla_call("kda_mla_bwd", dev, N, _adr(cu_q), _adr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _adr(q),
+              _adr(kv), _adr(k_rope), _adr(o), _adr(lse), _adr(dO), _adr(g["dq"]), _adr(g["dkv"]), _adr(g["dk_rope"]),
+              _adr(ws), ws.numel() * ws.element_size())
     return g
 
 
@@ -663,14 +682,19 @@ def kda_mla_decode_workspace(N: int, Sq: int, H: int, G: int = 1) -> int:
     return int(lib().kda_mla_decode_workspace(N, Sq, H, G, *MLA_CACHE_DIMS))
 
 
+@functools.lru_cache(maxsize=1024)
+def _decode_workspace(N, Sq, H, G, index):  # depends on the device's SM count
+    with torch.cuda.device(index):
+        return kda_mla_decode_workspace(N, Sq, H, G)
+
+
 def kda_mla_decode(q, cache, block_table, kv_lens, scale=None, cache_scale=None, o=None, lse=None, workspace=None):
     """Absorbed latent attention of new tokens over the paged cache.  q [N,Sq,H,576] bf16 (the
     query in the latent space, then its rotated part); cache [num_pages,page_size,G,576] bf16, or
     float8_e4m3fn with cache_scale float32 [num_pages,G]; block_table int32 [N,max_pages];
     kv_lens int32 [N], the new tokens counted (token i sees the first kv_lens - Sq + 1 + i rows).
     ``scale`` defaults to 192 ** -0.5.  Returns (o [N,Sq,H,512] bf16, lse [N,Sq,H] float32)."""
-    _check_cuda(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
-    dev = _same_device(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
+    dev = _mla_device(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
     code = _mla_cache(cache, cache_scale, block_table, kv_lens)
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
@@ -680,15 +704,11 @@ def kda_mla_decode(q, cache, block_table, kv_lens, scale=None, cache_scale=None,
     P, ps, G, _ = cache.shape
     o = _out(o, (N, Sq, H, MLA_CACHE_DIMS[0]), torch.bfloat16, dev, "o")
     lse = _out(lse, (N, Sq, H), torch.float32, dev, "lse")
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(kda_mla_decode_workspace(N, Sq, H, G), dtype=torch.uint8, device=dev)
-        st = lib().kda_mla_decode(N, Sq, H, G, *MLA_CACHE_DIMS, KDA_BF16,
-                                  sum(MLA_DIMS[:2]) ** -0.5 if scale is None else float(scale), _ptr(q), code,
-                                  _ptr(cache), _ptr(cache_scale), P, ps, _ptr(block_table), block_table.shape[1],
-                                  _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(dev))
-    _raise(st, "kda_mla_decode")
+    ws = _scratch(workspace, _decode_workspace(N, Sq, H, G, dev.index), dev)
+    _mla_call("kda_mla_decode", dev, N, Sq, H, G, *MLA_CACHE_DIMS, KDA_BF16,
+              sum(MLA_DIMS[:2]) ** -0.5 if scale is None else float(scale), _adr(q), code, _adr(cache),
+              _adr(cache_scale), P, ps, _adr(block_table), block_table.shape[1], _adr(kv_lens), _adr(o), _adr(lse),
+              _adr(ws), ws.numel() * ws.element_size())
     return o, lse
 
 
@@ -697,19 +717,16 @@ def kda_mla_cache_append(kv_new, cu_new, kv_lens, block_table, cache, cache_scal
     into the cache behind the kv_lens[n] rows sequence n holds, in place.  A float8_e4m3fn cache
     keeps one power-of-two scale for each page and group in cache_scale [num_pages,G], which grows
     (and the page's earlier rows are rounded anew) where new rows need it."""
-    _check_cuda(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
-    dev = _same_device(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
+    dev = _mla_device(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
     code = _mla_cache(cache, cache_scale, block_table, kv_lens)
     P, ps, G, dc = cache.shape
     if kv_new.dtype != torch.bfloat16 or cu_new.dtype != torch.int32:
         raise TypeError("kv_new must be bfloat16, cu_new int32")
     if kv_new.dim() != 3 or kv_new.shape[1:] != (G, dc) or cu_new.shape != (kv_lens.shape[0] + 1,):
         raise ValueError("shape mismatch: kv_new [T_new,G,576], cu_new [N+1]")
-    with torch.cuda.device(dev):
-        st = lib().kda_mla_cache_append(kv_lens.shape[0], _ptr(cu_new), kv_new.shape[0], G, *MLA_CACHE_DIMS, KDA_BF16,
-                                        _ptr(kv_new), _ptr(kv_lens), _ptr(block_table), block_table.shape[1], code,
-                                        _ptr(cache), _ptr(cache_scale), P, ps, _stream(dev))
-    _raise(st, "kda_mla_cache_append")
+    _mla_call("kda_mla_cache_append", dev, kv_lens.shape[0], _adr(cu_new), kv_new.shape[0], G, *MLA_CACHE_DIMS, KDA_BF16,
+              _adr(kv_new), _adr(kv_lens), _adr(block_table), block_table.shape[1], code, _adr(cache),
+              _adr(cache_scale), P, ps)
 
 
 def kda_device_status(device=None) -> int:
