@@ -19,8 +19,8 @@
 // so that the threads always have two products' time for p(i + 1) and two for e(i), without a
 // second S or dP buffer.
 //
-// Warps: 0-7 elementwise (row = tensor-memory lane; warps 0-3 take columns 0-47, 4-7 48-95);
-// 8 copies (TMA); 9 issues the products.  The launch for dq computes D first and leaves D and lse
+// Warps: 0-11 elementwise (row = tensor-memory lane; four warps for each 32 columns: with two
+// groups of 48 the threads, not the products, set the pace); 12 copies (TMA); 13 issues the products.  The launch for dq computes D first and leaves D and lse
 // in base 2, head by head, for the other.  dk_rope's parts are added over the heads, in order, by
 // a third launch.
 #include "mla_common.cuh"
@@ -32,10 +32,12 @@ namespace {
 
 using namespace mla;
 
-constexpr int kThreads = 320;
+constexpr int kGroups = 3;               // elementwise warpgroups, each a third of the columns
+constexpr int kElem = kGroups * 128;     // their threads
+constexpr int kThreads = kElem + 64;
 constexpr int kRows = 128;               // X rows of a CTA
 constexpr int kStep = 96;                // Y rows a step
-constexpr int kHalf = kStep / 2;         // columns of a warp
+constexpr int kPart = kStep / kGroups;   // columns of a group
 constexpr int kY1 = 3, kY2 = 1;          // stages
 constexpr uint32_t kXBlk = kRows * 128;  // 64 numbers of the rows
 constexpr uint32_t kYBlk = kStep * 128;
@@ -73,52 +75,40 @@ struct BwdSmem {
     int64_t find[40];
 };
 
-__device__ __forceinline__ void row_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void elem_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kElem) : "memory"); }
 
-// kHalf columns of this thread's lane as bfloat16 pairs.
-__device__ __forceinline__ void store_half(uint32_t taddr, const float (&x)[kHalf])
+// kPart columns of this thread's lane as bfloat16 pairs.
+__device__ __forceinline__ void store_part(uint32_t taddr, const float (&x)[kPart])
 {
-    uint32_t w[kHalf / 2];
+    uint32_t w[kPart / 2];
 #pragma unroll
-    for (int i = 0; i < kHalf / 2; ++i)
+    for (int i = 0; i < kPart / 2; ++i)
         w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    tc::st_32x32b_x16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(w));
-    tc::st_32x32b_x8(taddr + 16, *reinterpret_cast<const uint32_t(*)[8]>(w + 16));
+    tc::st_32x32b_x16(taddr, w);
     tc::wait_st();
 }
 
-__device__ __forceinline__ void load_half(uint32_t taddr, float (&x)[kHalf])
+__device__ __forceinline__ void load_part(uint32_t taddr, float (&x)[kPart])
 {
-    uint32_t a[32], b[16];
+    uint32_t a[kPart];
     tc::ld_32x32b_x32(taddr, a);
-    tc::ld_32x32b_x16(taddr + 32, b);
     tc::wait_ld();
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i)
-        x[i] = __uint_as_float(i < 32 ? a[i] : b[i - 32]);
+    for (int i = 0; i < kPart; ++i)
+        x[i] = __uint_as_float(a[i]);
 }
 
-// Columns of this thread's lane, times f, to bfloat16 (zeros where `none`).
-__device__ __forceinline__ void write_out(uint32_t taddr, int columns, float f, bool none, bool live, __nv_bfloat16 *dst)
+// 32 columns of this thread's lane, times f, as bfloat16 into vectors [v0, v0 + 4) of its row of
+// `vecs` 16-byte vectors (swizzled: neighbouring rows start in different banks).
+__device__ __forceinline__ void stage_bf16(unsigned char *rows, int vecs, int r, int v0, uint32_t taddr, float f)
 {
-#pragma unroll 1
-    for (int c = 0; c < columns; c += 32) {
-        uint32_t y[32];
-        if (!none) {
-            tc::ld_32x32b_x32(taddr + c, y);
-            tc::wait_ld();
-        }
-        if (live)
+    float x[32];
+    load_part(taddr, x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = none ? 0u
-                                : pack_bf16x2(__uint_as_float(y[i + 2 * k]) * f, __uint_as_float(y[i + 2 * k + 1]) * f);
-                *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-    }
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(rows + r * vecs * 16 + (((v0 + i) ^ (r & 7)) << 4)) =
+            make_uint4(pack_bf16x2(x[8 * i] * f, x[8 * i + 1] * f), pack_bf16x2(x[8 * i + 2] * f, x[8 * i + 3] * f),
+                       pack_bf16x2(x[8 * i + 4] * f, x[8 * i + 5] * f), pack_bf16x2(x[8 * i + 6] * f, x[8 * i + 7] * f));
 }
 
 template <bool kKeys>  // X rows are keys (dk, dv), else queries (dq)
@@ -129,16 +119,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     BwdSmem &sm = *reinterpret_cast<BwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
-    const bool okq = offsets_ok<kThreads>(a.cu_q, a.N, a.Tq), okk = offsets_ok<kThreads>(a.cu_k, a.N, a.Tk);
-    if (!okq || !okk) {
-        if (tid == 0)
-            report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        return;
-    }
-    const int32_t *cu_x = kKeys ? a.cu_k : a.cu_q;
-    Item it;
-    if (!find_item<kThreads>(
-            a.N, blockIdx.x / a.H, [&](int n) { return (cu_x[n + 1] - cu_x[n] + kRows - 1) / kRows; }, it, sm.find))
+    const Item it = find_item<kThreads>(
+        a.N, blockIdx.x / a.H,
+        [&](int n, bool &bad) {
+            const Span q = span_of(a.cu_q, n, a.Tq, bad), k = span_of(a.cu_k, n, a.Tk, bad);
+            return ((kKeys ? k : q).len() + kRows - 1) / kRows;
+        },
+        sm.find);
+    if (it.bad && tid == 0)
+        report_device_error(a.status, KDA_ERR_INVALID_ARG);
+    if (it.bad || it.seq < 0)
         return;
     const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
     const int lx = kKeys ? lk : lq, ly = kKeys ? lq : lk;
@@ -163,12 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&sm.s_full, 1);
         mbar_init(&sm.dp_full, 1);
-        mbar_init(&sm.p_full, 256);
-        mbar_init(&sm.e_full, 256);
+        mbar_init(&sm.p_full, kElem / 32);
+        mbar_init(&sm.e_full, kElem / 32);
         mbar_init(&sm.done, 1);
         fence_mbar_init_cluster();
     }
-    if (warp == 8)
+    if (warp == kElem / 32)
         tc::tmem_alloc(&sm.tmem_slot, 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -176,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem_slot;
     Waits wait{a.status, false};
 
-    if (warp == 8) {
+    if (warp == kElem / 32) {
         // ---------------- copies
         if (steps > 0 && elect()) {
             mbar_arrive_expect_tx(&sm.x_full, 5 * kXBlk);
@@ -246,16 +236,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live < kStep)
                 zero_tail(sm.y2[r2.slot], 2, live, &sm.y2_full[r2.slot]);
         }
-    } else if (warp == 9) {
+    } else if (warp == kElem / 32 + 1) {
         // ---------------- products
         constexpr uint32_t id_s = tc::idesc_bf16(kRows, kStep, false, false), id_1 = tc::idesc_bf16(kRows, kDQ, false, true),
                            id_2 = tc::idesc_bf16(kRows, kDV, false, true);
         const Desc x1(smem_u32(sm.x1), 16, 1024, tc::kSw128), x2(smem_u32(sm.x2), 16, 1024, tc::kSw128),
             y1(smem_u32(sm.y1[0]), 16, 1024, tc::kSw128), y2(smem_u32(sm.y2[0]), 16, 1024, tc::kSw128),
             t1(smem_u32(sm.y1[0]), kYBlk, 1024, tc::kSw128), t2(smem_u32(sm.y2[0]), kYBlk, 1024, tc::kSw128);
-        // tensor-memory column of the 16 Y rows ks of p or e: each half of the columns at its own start
-        auto a_col = [](uint32_t base, int ks) { return base + (ks < 3 ? 0 : kHalf - 24) + ks * 8; };
-        static_assert(kHalf == 48, "three 16-row steps a half");
+        // tensor-memory column of the 16 Y rows ks of p or e: each group's at its own start
+        auto a_col = [](uint32_t base, int ks) { return base + (ks >> 1) * kPart + (ks & 1) * 8; };
+        static_assert(kPart == 32, "two 16-row steps a group");
         auto scores = [&](uint32_t slot) {
             if (elect()) {
 #pragma unroll
@@ -325,17 +315,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             now2 = r2.slot;
         }
     } else {
-        // ---------------- elementwise: row r0 + r, columns half * 48 ..
-        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
+        // ---------------- elementwise: row r0 + r, columns group * 32 ..
+        const int r = (warp & 3) * 32 + lane, group = warp >> 2;
         const bool live = r < rows;
-        const uint32_t addr = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, half * kHalf);
+        const uint32_t addr = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, group * kPart);
         const float sl2 = a.scale * kLog2e;
         float lse2 = INFINITY, delta = 0.0f;
         if constexpr (!kKeys) {
             const int64_t row = (int64_t)(q0 + r0 + r) * a.H + h;
-            if (live) {
-                const uint4 *x = reinterpret_cast<const uint4 *>(a.o + row * kDV + half * 64);
-                const uint4 *y = reinterpret_cast<const uint4 *>(a.dO + row * kDV + half * 64);
+            if (live && group < 2) {  // half a row each
+                const uint4 *x = reinterpret_cast<const uint4 *>(a.o + row * kDV + group * 64);
+                const uint4 *y = reinterpret_cast<const uint4 *>(a.dO + row * kDV + group * 64);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint4 u = x[c], v = y[c];
@@ -346,22 +336,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         delta += f.x * g.x + f.y * g.y;
                     }
                 }
-                const float l = a.lse[row];
-                lse2 = l == -INFINITY ? INFINITY : l * kLog2e;  // a row that sees no key: weights 0
             }
-            sm.dsum[half][r] = delta;
-            row_sync();
+            if (group < 2)
+                sm.dsum[group][r] = delta;
+            const float l = live ? a.lse[row] : -INFINITY;
+            lse2 = l == -INFINITY ? INFINITY : l * kLog2e;  // a row that sees no key: weights 0
+            elem_sync();
             delta = sm.dsum[0][r] + sm.dsum[1][r];
-            if (live && half == 0) {
+            if (live && group == 0) {
                 a.delta[(int64_t)h * a.Tq + q0 + r0 + r] = delta;
                 a.lse2[(int64_t)h * a.Tq + q0 + r0 + r] = lse2;
             }
         }
         Ring<kY1> r1;
         for (int i = 0; i < steps; ++i, r1.step()) {
-            const int y = y_first + i * kStep + half * kHalf;  // place of the first column
+            const int y = y_first + i * kStep + group * kPart;  // place of the first column
             // columns lo .. hi - 1 are visible to the row
-            int lo = 0, hi = kHalf;
+            int lo = 0, hi = kPart;
             bool edge;
             if (kKeys) {
                 edge = i + 1 == steps || (a.causal && r0 + kRows - 1 > y_first + i * kStep + off);
@@ -371,15 +362,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 edge = (i + 1) * kStep > (a.causal ? min(ly, r0 + off + 1) : ly);
                 hi = (a.causal ? min(ly, r0 + r + off + 1) : ly) - y;
             }
-            float p[kHalf], x[kHalf];
+            float p[kPart], x[kPart];
             wait(&sm.s_full, i & 1);
             tc::fence_after_sync();
-            load_half(addr + kColS, p);
+            load_part(addr + kColS, p);
             if (kKeys) {
                 wait(&sm.y1_full[r1.slot], r1.round & 1);  // the step's lse and D
-                const float4 *l = reinterpret_cast<const float4 *>(sm.col[r1.slot][0] + half * kHalf);
+                const float4 *l = reinterpret_cast<const float4 *>(sm.col[r1.slot][0] + group * kPart);
 #pragma unroll
-                for (int c = 0; c < kHalf / 4; ++c) {
+                for (int c = 0; c < kPart / 4; ++c) {
                     const float4 v = l[c];
                     p[4 * c] = ex2(fmaf(p[4 * c], sl2, -v.x));
                     p[4 * c + 1] = ex2(fmaf(p[4 * c + 1], sl2, -v.y));
@@ -388,26 +379,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kHalf; ++c)
+                for (int c = 0; c < kPart; ++c)
                     p[c] = ex2(fmaf(p[c], sl2, -lse2));
             }
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < kHalf; ++c)
+                for (int c = 0; c < kPart; ++c)
                     if (c < lo || c >= hi)
                         p[c] = 0.0f;
             }
             if (kKeys)
-                store_half(addr + kColS, p);
+                store_part(addr + kColS, p);
             tc::fence_before_sync();
-            mbar_arrive(&sm.p_full);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.p_full);
             wait(&sm.dp_full, i & 1);
             tc::fence_after_sync();
-            load_half(addr + kColP, x);
+            load_part(addr + kColP, x);
             if (kKeys) {
-                const float4 *d = reinterpret_cast<const float4 *>(sm.col[r1.slot][1] + half * kHalf);
+                const float4 *d = reinterpret_cast<const float4 *>(sm.col[r1.slot][1] + group * kPart);
 #pragma unroll
-                for (int c = 0; c < kHalf / 4; ++c) {
+                for (int c = 0; c < kPart / 4; ++c) {
                     const float4 v = d[c];
                     x[4 * c] = p[4 * c] * (x[4 * c] - v.x);
                     x[4 * c + 1] = p[4 * c + 1] * (x[4 * c + 1] - v.y);
@@ -416,68 +409,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kHalf; ++c)
+                for (int c = 0; c < kPart; ++c)
                     x[c] = p[c] * (x[c] - delta);
             }
             if (edge) {  // a hidden pair's dP may be anything
 #pragma unroll
-                for (int c = 0; c < kHalf; ++c)
+                for (int c = 0; c < kPart; ++c)
                     if (c < lo || c >= hi)
                         x[c] = 0.0f;
             }
-            store_half(addr + kColP, x);
+            store_part(addr + kColP, x);
             tc::fence_before_sync();
-            mbar_arrive(&sm.e_full);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.e_full);
         }
-        // ---- the sums
+        // ---- the sums, through shared memory (nothing reads the tiles any more), so that the
+        // writes are whole rows
         if (steps > 0) {
             wait(&sm.done, 0);
             tc::fence_after_sync();
         }
         const uint32_t base = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, 0);
-        const bool none = steps == 0;
-        if (kKeys) {
-            const int64_t key = k0 + r0 + r;
-            __nv_bfloat16 *dst = a.dkv + (key * a.H + h) * kDKV;
-            if (half == 0) {
-                write_out(base + kCol2, kDV, 1.0f, none, live, dst + kDN);
-            } else {
-                write_out(base + kCol1, kDN, a.scale, none, live, dst);
-                float *part = a.part + ((int64_t)h * a.Tk + key) * kDR;
+        constexpr int kVecs = (kKeys ? kDKV : kDQ) / 8;  // 16-byte vectors of a row of dkv or dq
+        unsigned char *rowbuf = sm.x1;                   // x1 and x2: 80 KB
+        float *part = reinterpret_cast<float *>(sm.y1[0]);
+        static_assert(kRows * kDKV * 2 <= 5 * kXBlk && kRows * kDR * 4 <= kY1 * 3 * kYBlk, "room for the sums");
+        if (steps > 0) {
+            if (kKeys) {
+                // dk (4 x 32 columns), dv (4 x 32), the rope part of dk (2 x 32), a group every third
 #pragma unroll 1
-                for (int c = 0; c < kDR; c += 32) {
-                    uint32_t y[32];
-                    if (!none) {
-                        tc::ld_32x32b_x32(base + kCol1 + kDN + c, y);
-                        tc::wait_ld();
-                    }
-                    if (live)
+                for (int c = group; c < 8; c += kGroups)
+                    stage_bf16(rowbuf, kVecs, r, c * 4, base + (c < 4 ? kCol1 + c * 32 : kCol2 + (c - 4) * 32),
+                               c < 4 ? a.scale : 1.0f);
+                if (group > 0) {
+                    float x[32];
+                    load_part(base + kCol1 + kDN + (group - 1) * 32, x);
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(part + c + k) =
-                                none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                     : make_float4(__uint_as_float(y[k]) * a.scale, __uint_as_float(y[k + 1]) * a.scale,
-                                                   __uint_as_float(y[k + 2]) * a.scale, __uint_as_float(y[k + 3]) * a.scale);
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4 *>(part + r * kDR + ((((group - 1) * 8 + i) ^ (r & 7)) << 2)) =
+                            make_float4(x[4 * i] * a.scale, x[4 * i + 1] * a.scale, x[4 * i + 2] * a.scale,
+                                        x[4 * i + 3] * a.scale);
                 }
+            } else {
+#pragma unroll 1
+                for (int c = group; c < 6; c += kGroups)
+                    stage_bf16(rowbuf, kVecs, r, c * 4, base + kCol1 + c * 32, a.scale);
             }
-        } else {
-            __nv_bfloat16 *dst = a.dq + ((int64_t)(q0 + r0 + r) * a.H + h) * kDQ;
-            write_out(base + kCol1 + half * 96, 96, a.scale, none, live, dst + half * 96);
+        }
+        elem_sync();
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        __nv_bfloat16 *dst = kKeys ? a.dkv + ((int64_t)(k0 + r0) * a.H + h) * kDKV : a.dq + ((int64_t)(q0 + r0) * a.H + h) * kDQ;
+        const int64_t pitch = (int64_t)a.H * (kKeys ? kDKV : kDQ);
+        for (int v = tid; v < rows * kVecs; v += kElem) {
+            const int vr = v / kVecs, c = v % kVecs;
+            *reinterpret_cast<uint4 *>(dst + vr * pitch + c * 8) =
+                steps > 0 ? *reinterpret_cast<const uint4 *>(rowbuf + vr * kVecs * 16 + ((c ^ (vr & 7)) << 4)) : zero;
+        }
+        if (kKeys) {
+            float4 *out = reinterpret_cast<float4 *>(a.part + ((int64_t)h * a.Tk + k0 + r0) * kDR);
+            for (int v = tid; v < rows * (kDR / 4); v += kElem) {
+                const int vr = v / (kDR / 4), c = v % (kDR / 4);
+                out[v] = steps > 0 ? *reinterpret_cast<const float4 *>(part + vr * kDR + ((c ^ (vr & 7)) << 2))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 8)
+    if (warp == kElem / 32)
         tc::tmem_dealloc(tmem, 512);
 }
 
 // dk_rope: its heads' parts in order, four numbers a thread.
 __global__ void __launch_bounds__(256) mla_dkr_kernel(BwdArgs a)
 {
-    const bool okq = offsets_ok<256>(a.cu_q, a.N, a.Tq), okk = offsets_ok<256>(a.cu_k, a.N, a.Tk);
+    bool bad = false;
+    for (int n = threadIdx.x; n < a.N; n += 256) {
+        span_of(a.cu_q, n, a.Tq, bad);
+        span_of(a.cu_k, n, a.Tk, bad);
+    }
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (!okq || !okk || x >= (int64_t)a.cu_k[a.N] * (kDR / 4))
+    if (__syncthreads_or(bad) || x >= (int64_t)a.cu_k[a.N] * (kDR / 4))
         return;
     const float4 *p = reinterpret_cast<const float4 *>(a.part) + x;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -76,22 +76,18 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
     __shared__ int64_t sh[40];
     __shared__ float s_max[kThreads / 32];
     const int tid = threadIdx.x, ps = a.page_size;
-    if (!offsets_ok<kThreads>(a.cu, a.N, a.T_new)) {
-        if (tid == 0)
-            report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        return;
-    }
     // sequence n touches the pages of its places [len, len + new rows)
-    auto touched = [&](int n) {
-        const int m = a.cu[n + 1] - a.cu[n], len = a.kv_lens[n];
-        if (m == 0)
-            return 0;
-        if (len < 0)
-            return 1;  // refused below
-        return (len % ps + m - 1) / ps + 1;
-    };
-    Item it;
-    if (!find_item<kThreads>(a.N, blockIdx.x, touched, it, sh))
+    const Item it = find_item<kThreads>(
+        a.N, blockIdx.x,
+        [&](int n, bool &bad) {
+            const int m = span_of(a.cu, n, a.T_new, bad).len(), len = a.kv_lens[n];
+            // a refused length stands for one page, whose CTA reports it
+            return m <= 0 ? 0 : len < 0 ? 1 : (len % ps + m - 1) / ps + 1;
+        },
+        sh);
+    if (it.bad && tid == 0)
+        report_device_error(a.status, KDA_ERR_INVALID_ARG);
+    if (it.bad || it.seq < 0)
         return;
     const int n = it.seq, g = blockIdx.y, len = a.kv_lens[n], m = a.cu[n + 1] - a.cu[n];
     const int64_t p_idx = len < 0 ? -1 : (int64_t)len / ps + it.k;

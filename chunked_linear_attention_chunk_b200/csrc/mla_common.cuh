@@ -16,19 +16,6 @@ constexpr int kDC = kDL + kDR;                 // a cached row
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The packed offsets of one axis are usable: cu[0] = 0, non-decreasing, cu[N] <= T.  All threads
-// of the CTA call it (it ends in a barrier).
-template <int kThreads>
-__device__ __forceinline__ bool offsets_ok(const int32_t *__restrict__ cu, int N, int T)
-{
-    int bad = 0;
-    for (int i = threadIdx.x; i <= N; i += kThreads) {
-        const int x = cu[i];
-        bad |= x < 0 || x > T || (i == 0 ? x != 0 : x < cu[i - 1]);
-    }
-    return __syncthreads_or(bad) == 0;
-}
-
 // A sum over the CTA; all threads call it.  `sh` is 40 int64 of shared memory.
 template <int kThreads>
 __device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *sh)
@@ -47,20 +34,26 @@ __device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *sh)
 }
 
 // Work item x of the list that has count(0) items for sequence 0, then count(1) for sequence 1,
-// and so on: its sequence and its place among that sequence's items.  False past the end.  All
-// threads of the CTA call it; `sh` is 40 int64 of shared memory.
+// and so on: its sequence and its place among that sequence's items, or seq = -1 past the end.
+// `count` sees every sequence once and sets `bad` for what is not to be used; the CTA learns of
+// it whichever of its threads saw it.  All threads of the CTA call; `sh` is 40 int64 of shared
+// memory.
 struct Item {
     int seq, k;
+    bool bad;
 };
 template <int kThreads, class Count>
-__device__ __forceinline__ bool find_item(int N, int64_t x, Count count, Item &it, int64_t *sh)
+__device__ __forceinline__ Item find_item(int N, int64_t x, Count count, int64_t *sh)
 {
     static_assert(kThreads % 32 == 0 && kThreads <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    bool bad = false;
     int64_t base = 0;
+    if (tid == 0)
+        sh[33] = -1;
     for (int s0 = 0; s0 < N; s0 += kThreads) {
         const int s = s0 + tid;
-        const int64_t c = s < N ? count(s) : 0;
+        const int64_t c = s < N ? count(s, bad) : 0;
         int64_t inc = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -80,15 +73,27 @@ __device__ __forceinline__ bool find_item(int N, int64_t x, Count count, Item &i
             sh[33] = s;
             sh[34] = rel;
         }
-        __syncthreads();
         base += total;
-        if (x < base) {
-            it.seq = (int)sh[33];
-            it.k = (int)sh[34];
-            return true;
-        }
+        if (s0 + kThreads < N)
+            __syncthreads();
     }
-    return false;
+    Item it;
+    it.bad = __syncthreads_or(bad) != 0;
+    it.seq = (int)sh[33];
+    it.k = (int)sh[34];
+    return it;
+}
+
+// Sequence n's rows [lo, hi) of a packed axis of T; bad unless 0 = cu[0] <= cu[1] <= .. <= T.
+struct Span {
+    int lo, hi;
+    __device__ __forceinline__ int len() const { return hi - lo; }
+};
+__device__ __forceinline__ Span span_of(const int32_t *__restrict__ cu, int n, int T, bool &bad)
+{
+    Span s{cu[n], cu[n + 1]};
+    bad |= s.lo < 0 || s.hi < s.lo || s.hi > T || (n == 0 && s.lo != 0);
+    return s;
 }
 
 // 2^x by the hardware's approximation (2 ulp; results below the normal range flush to 0).

@@ -216,9 +216,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         const int64_t per = total < 0x7fffffff - a.shares ? (uint32_t)(total + a.shares - 1) / (uint32_t)a.shares
                                                           : (total + a.shares - 1) / a.shares;
         const int64_t begin = min(total, share * per), end = min(total, begin + per);
-        Item it{0, 0};
-        if (begin < end)
-            find_item<kT>(a.N, begin, [&](int n) { return tiles_of(a, n) * a.G; }, it, sm.find);
+        const Item it = find_item<kT>(a.N, begin, [&](int n, bool &) { return tiles_of(a, n) * a.G; }, sm.find);
         if (tid == 0) {
             const int tiles = begin < end ? tiles_of(a, it.seq) : 1;
             sm.share[0] = begin;

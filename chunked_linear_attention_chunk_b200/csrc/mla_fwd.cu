@@ -71,16 +71,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     FwdSmem &sm = *reinterpret_cast<FwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
-    const bool okq = offsets_ok<kThreads>(a.cu_q, a.N, a.Tq), okk = offsets_ok<kThreads>(a.cu_k, a.N, a.Tk);
-    if (!okq || !okk) {
-        if (tid == 0)
-            report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        return;
-    }
-    Item it;
-    if (!find_item<kThreads>(
-            a.N, blockIdx.x / a.H,
-            [&](int n) { return (a.cu_q[n + 1] - a.cu_q[n] + kTiles * kRows - 1) / (kTiles * kRows); }, it, sm.find))
+    const Item it = find_item<kThreads>(
+        a.N, blockIdx.x / a.H,
+        [&](int n, bool &bad) {
+            span_of(a.cu_k, n, a.Tk, bad);
+            return (span_of(a.cu_q, n, a.Tq, bad).len() + kTiles * kRows - 1) / (kTiles * kRows);
+        },
+        sm.find);
+    if (it.bad && tid == 0)
+        report_device_error(a.status, KDA_ERR_INVALID_ARG);
+    if (it.bad || it.seq < 0)
         return;
     const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
     // with a causal mask the last queries see the most keys: they go first
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], kRows);
+            mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
         }
         fence_mbar_init_cluster();
@@ -274,15 +274,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::st_32x32b_x16(s_addr + 32, *reinterpret_cast<const uint32_t(*)[16]>(p + 32));
             tc::wait_st();
             tc::fence_before_sync();
-            mbar_arrive(&sm.p_full[t]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.p_full[t]);
         }
-        // ---- the row's result
+        // ---- the rows' results, through the place of the tile's Q (read for the last time before
+        // the last O), so that the writes are whole rows
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t r = (int64_t)(q0 + row) * a.H + h;
         if (n > 0) {
             wait(&sm.pv_done[t], (n - 1) & 1);
             tc::fence_after_sync();
+        } else if (n_steps > 0) {
+            wait(&sm.q_full, 0);  // the copy of a Q that nothing reads
         }
+        const int tr = tid & (kRows - 1);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             uint32_t y[32];
@@ -290,17 +296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::ld_32x32b_x32(o_addr + c * 32, y);
                 tc::wait_ld();
             }
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = l == 0.0f ? 0u
-                                 : pack_bf16x2(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
-            if (row < lq) {
-                uint4 *dst = reinterpret_cast<uint4 *>(a.o + r * kDV + c * 32);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int k = 0; k < 4; ++k)
+                    w[k] = l == 0.0f ? 0u
+                                     : pack_bf16x2(__uint_as_float(y[8 * i + 2 * k]) * inv,
+                                                   __uint_as_float(y[8 * i + 2 * k + 1]) * inv);
+                *reinterpret_cast<uint4 *>(sm.q[t] + tr * 256 + (((c * 4 + i) ^ (tr & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+        for (int v = tr; v < kRows * 16; v += kRows) {
+            const int vr = v >> 4, c = v & 15, i = i0 + t * kRows + vr;
+            if (i < lq)
+                *reinterpret_cast<uint4 *>(a.o + ((int64_t)(q0 + i) * a.H + h) * kDV + c * 8) =
+                    *reinterpret_cast<const uint4 *>(sm.q[t] + vr * 256 + ((c ^ (vr & 7)) << 4));
         }
         if (a.lse && row < lq)
             a.lse[r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
