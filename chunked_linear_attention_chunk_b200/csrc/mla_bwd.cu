@@ -9,20 +9,26 @@
 // for the 832 of the formulas.
 //
 // Both launches hold a 128-row tile (X: queries for dq, keys for dk and dv) and step through the
-// other side (Y) 96 rows at a time:
+// other side (Y) 64 rows at a time:
 //   S = X1 Y1^T (K = 192),  dP = X2 Y2^T (K = 128),  acc1 += e Y1 (N = 192),
 //   keys only: acc2 += p Y2 (N = 128)
 // with X1, Y1 the q and [k, k_rope] rows and X2, Y2 the dO and v rows.  A Y tile serves as K-major
-// operand of the first two products and MN-major operand of the last two; p and e go back to
-// tensor memory as their A operands, over the S and dP they came from.  The products are issued
-//   acc2(i), S(i + 1), acc1(i), dP(i + 1)
-// so that the threads always have two products' time for p(i + 1) and two for e(i), without a
-// second S or dP buffer.
+// operand of the first two products and MN-major operand of the last two.
 //
-// Warps: 0-11 elementwise (row = tensor-memory lane; four warps for each 32 columns: with two
-// groups of 48 the threads, not the products, set the pace); 12 copies (TMA); 13 issues the products.  The launch for dq computes D first and leaves D and lse
-// in base 2, head by head, for the other.  dk_rope's parts are added over the heads, in order, by
-// a third launch.
+// A 128 x 64 x 16 product takes 52 cycles with both operands in shared memory and 32 with X in
+// tensor memory, so X lives there as far as it fits beside the sums: all of it for dq (160 + 192
+// columns), dO's partner v for dk and dv (64 + 320; k stays in shared memory).  That leaves one S
+// and one dP of 64 columns, which the threads read at once; p and e go to the sums through shared
+// memory, so that S and dP never wait for the sums.
+//
+// Three warps issue the products, one S, one dP, one the sums: a warp that finds its barriers ready
+// still spends some 150 cycles on each, in which it feeds nothing to the tensor cores, and a 128 x
+// 64 x 16 product takes about as long to issue as to run.  Two sets of eight warps take steps in
+// turn, a thread half of a row.  The launch for dq computes D first and leaves D and lse in base 2,
+// head by head, for the other.  dk_rope's parts are added over the heads, in order, by a third
+// launch.
+//
+// Warps: 0-15 elementwise; 16 copies (TMA) of X and Y1; 17 S; 18 the sums; 19 dP and copies of Y2.
 #include "mla_common.cuh"
 #include "mla_tc.cuh"
 
@@ -32,17 +38,22 @@ namespace {
 
 using namespace mla;
 
-constexpr int kGroups = 3;               // elementwise warpgroups, each a third of the columns
-constexpr int kElem = kGroups * 128;     // their threads
-constexpr int kThreads = kElem + 64;
+constexpr int kElemWarps = 16;
+constexpr int kElem = kElemWarps * 32;   // elementwise threads: two sets, two threads a row
+constexpr int kThreads = kElem + 128;    // 20 warps: one more on a scheduler would cost 16 registers a thread
 constexpr int kRows = 128;               // X rows of a CTA
-constexpr int kStep = 96;                // Y rows a step
-constexpr int kPart = kStep / kGroups;   // columns of a group
-constexpr int kY1 = 3, kY2 = 1;          // stages
+constexpr int kStep = 64;                // Y rows a step
 constexpr uint32_t kXBlk = kRows * 128;  // 64 numbers of the rows
 constexpr uint32_t kYBlk = kStep * 128;
-constexpr uint32_t kColS = 0, kColP = kStep, kCol2 = 2 * kStep, kCol1 = kCol2 + 128;  // tensor memory columns
-static_assert(kCol1 + kDQ <= 512, "tensor memory");
+
+// Tensor-memory columns.
+template <bool kKeys>
+struct Cols {
+    static constexpr uint32_t X1 = 0, X2 = kKeys ? 0 : 96;  // X1: queries only
+    static constexpr uint32_t S = kKeys ? 64 : 160, P = S + kStep;
+    static constexpr uint32_t Acc2 = P + kStep, Acc1 = kKeys ? Acc2 + 128 : Acc2;  // Acc2: keys only
+    static_assert(Acc1 + kDQ <= 512, "tensor memory");
+};
 
 struct BwdArgs {
     int N, Tq, Tk, H;
@@ -62,40 +73,74 @@ struct BwdMaps {
     CUtensorMap x1, x1r, x2, y1, y1r, y2;
 };
 
+template <bool kKeys>
 struct BwdSmem {
-    alignas(1024) unsigned char x1[3 * kXBlk];
-    alignas(1024) unsigned char x2[2 * kXBlk];
+    // stages; with three of Y1 the keys' S waits for copies (its stage is held until acc1)
+    static constexpr int kY1 = kKeys ? 4 : 5, kY2 = kKeys ? 2 : 4;
+    alignas(1024) unsigned char x1[kKeys ? 3 * kXBlk : 16];
+    // queries: the last two stages hold x1 on its way to tensor memory
     alignas(1024) unsigned char y1[kY1][3 * kYBlk];
     alignas(1024) unsigned char y2[kY2][2 * kYBlk];
-    float col[kY1][2][kStep];  // keys: lse in base 2 and D of a step's queries
-    float dsum[2][kRows];      // queries: halves of D
-    uint64_t x_full, y1_full[kY1], y1_empty[kY1], y2_full[kY2], y2_empty[kY2], tail;
-    uint64_t s_full, p_full, dp_full, e_full, done;
+    // e, p [128 rows][64 numbers]; before the first step x2 on its way to tensor memory
+    alignas(1024) unsigned char e[kXBlk], p[kXBlk];
+    alignas(16) float col[kKeys ? kY1 : 1][2][kStep];  // keys: lse in base 2 and D of a step's queries
+    float delta[kRows];                    // queries: D
+    uint64_t x_landed, x_full, y1_full[kY1], y1_empty[kY1], y2_full[kY2], y2_empty[kY2], tail[2];
+    uint64_t s_full[2], dp_full[2], p_full[2], e_full[2], acc1_done[2], acc2_done[2];  // by step parity
+    uint64_t s_read, dp_read, done;
     uint32_t tmem_slot;
     int64_t find[40];
 };
 
-__device__ __forceinline__ void elem_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kElem) : "memory"); }
-
-// kPart columns of this thread's lane as bfloat16 pairs.
-__device__ __forceinline__ void store_part(uint32_t taddr, const float (&x)[kPart])
+// A warp clears the rows from `live` on of `blocks` blocks and passes the stage on: rows behind a
+// sequence's end may hold anything, and 0 * NaN is NaN.
+__device__ __forceinline__ void zero_tail(unsigned char *p, int blocks, int live, uint64_t *full)
 {
-    uint32_t w[kPart / 2];
-#pragma unroll
-    for (int i = 0; i < kPart / 2; ++i)
-        w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    tc::st_32x32b_x16(taddr, w);
-    tc::wait_st();
+    for (int i = threadIdx.x & 31; i < (kStep - live) * 8 * blocks; i += 32)
+        *reinterpret_cast<uint4 *>(p + i % blocks * kYBlk + (live + i / (8 * blocks)) * 128 + i / blocks % 8 * 16) =
+            make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect())
+        mbar_arrive(full);
 }
 
-__device__ __forceinline__ void load_part(uint32_t taddr, float (&x)[kPart])
+__device__ __forceinline__ void elem_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kElem) : "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void load_32(uint32_t taddr, float (&x)[32])
 {
-    uint32_t a[kPart];
+    uint32_t a[32];
     tc::ld_32x32b_x32(taddr, a);
     tc::wait_ld();
 #pragma unroll
-    for (int i = 0; i < kPart; ++i)
+    for (int i = 0; i < 32; ++i)
         x[i] = __uint_as_float(a[i]);
+}
+
+// 32 numbers of row r as bfloat16 into vectors [v0, v0 + 4) of its 128-byte row (swizzled).
+__device__ __forceinline__ void store_32(unsigned char *rows, int r, int v0, const float (&x)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(rows + r * 128 + (((v0 + i) ^ (r & 7)) << 4)) =
+            make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                       pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+}
+
+// Row r of a block of 64 numbers (swizzled) to 32 columns of this thread's lane.
+__device__ __forceinline__ void keep_64(uint32_t taddr, const unsigned char *rows, int r)
+{
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(rows + r * 128 + ((i ^ (r & 7)) << 4));
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+    tc::st_32x32b_x32(taddr, w);
 }
 
 // 32 columns of this thread's lane, times f, as bfloat16 into vectors [v0, v0 + 4) of its row of
@@ -103,7 +148,7 @@ __device__ __forceinline__ void load_part(uint32_t taddr, float (&x)[kPart])
 __device__ __forceinline__ void stage_bf16(unsigned char *rows, int vecs, int r, int v0, uint32_t taddr, float f)
 {
     float x[32];
-    load_part(taddr, x);
+    load_32(taddr, x);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4 *>(rows + r * vecs * 16 + (((v0 + i) ^ (r & 7)) << 4)) =
@@ -116,9 +161,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     mla_bwd_kernel(const __grid_constant__ BwdMaps maps, BwdArgs a)
 {
     extern __shared__ unsigned char raw[];
-    BwdSmem &sm = *reinterpret_cast<BwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    using SM = BwdSmem<kKeys>;
+    using C = Cols<kKeys>;
+    SM &sm = *reinterpret_cast<SM *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
+    if (tid == 0) {
+        mbar_init(&sm.x_landed, 1);
+        mbar_init(&sm.x_full, kKeys ? 8 : kElemWarps);
+        mbar_init(&sm.tail[0], 1);
+        mbar_init(&sm.tail[1], 1);
+        for (int i = 0; i < SM::kY1; ++i) {
+            mbar_init(&sm.y1_full[i], kKeys ? 33 : 1);
+            mbar_init(&sm.y1_empty[i], 1);
+        }
+        for (int i = 0; i < SM::kY2; ++i) {
+            mbar_init(&sm.y2_full[i], 1);
+            mbar_init(&sm.y2_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.dp_full[i], 1);
+            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.e_full[i], 8);
+            mbar_init(&sm.acc1_done[i], 1);
+            mbar_init(&sm.acc2_done[i], 1);
+        }
+        mbar_init(&sm.s_read, 8);
+        mbar_init(&sm.dp_read, 8);
+        mbar_init(&sm.done, 1);
+        fence_mbar_init_cluster();
+    }
     const Item it = find_item<kThreads>(
         a.N, blockIdx.x / a.H,
         [&](int n, bool &bad) {
@@ -140,25 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int y_end = !kKeys && a.causal ? min(ly, r0 + rows + off) : ly;
     const int steps = y_first < y_end ? (y_end - y_first + kStep - 1) / kStep : 0;
 
-    if (tid == 0) {
-        mbar_init(&sm.x_full, 1);
-        mbar_init(&sm.tail, 1);
-        for (int i = 0; i < kY1; ++i) {
-            mbar_init(&sm.y1_full[i], kKeys ? 33 : 1);
-            mbar_init(&sm.y1_empty[i], 1);
-        }
-        for (int i = 0; i < kY2; ++i) {
-            mbar_init(&sm.y2_full[i], 1);
-            mbar_init(&sm.y2_empty[i], 1);
-        }
-        mbar_init(&sm.s_full, 1);
-        mbar_init(&sm.dp_full, 1);
-        mbar_init(&sm.p_full, kElem / 32);
-        mbar_init(&sm.e_full, kElem / 32);
-        mbar_init(&sm.done, 1);
-        fence_mbar_init_cluster();
-    }
-    if (warp == kElem / 32)
+    if (warp == kElemWarps)
         tc::tmem_alloc(&sm.tmem_slot, 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -166,32 +221,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem_slot;
     Waits wait{a.status, false};
 
-    if (warp == kElem / 32) {
-        // ---------------- copies
+    if (warp == kElemWarps) {
+        // ---------------- copies of X and Y1
         if (steps > 0 && elect()) {
-            mbar_arrive_expect_tx(&sm.x_full, 5 * kXBlk);
             const int x = (kKeys ? k0 : q0) + r0;
-            tma_load_4d(sm.x1, &maps.x1, 0, x, h, 0, &sm.x_full);
+            mbar_arrive_expect_tx(&sm.x_landed, 5 * kXBlk);
+            unsigned char *x1 = kKeys ? sm.x1 : sm.y1[SM::kY1 - 2];
+            tma_load_4d(x1, &maps.x1, 0, x, h, 0, &sm.x_landed);
             if (kKeys)
-                tma_load_2d(sm.x1 + 2 * kXBlk, &maps.x1r, 0, x, &sm.x_full);
-            tma_load_4d(sm.x2, &maps.x2, 0, x, h, kKeys ? 2 : 0, &sm.x_full);
+                tma_load_2d(x1 + 2 * kXBlk, &maps.x1r, 0, x, &sm.x_landed);
+            tma_load_4d(sm.e, &maps.x2, 0, x, h, kKeys ? 2 : 0, &sm.x_landed);
         }
         __syncwarp();
-        Ring<kY1> r1;
-        Ring<kY2> r2;
-        uint32_t tails = 0;
-        // rows behind the sequence's end may hold anything (0 * NaN): zeros
-        auto zero_tail = [&](unsigned char *p, int blocks, int live, uint64_t *full) {
-            wait(&sm.tail, tails++ & 1);
-            for (int i = lane; i < (kStep - live) * 8 * blocks; i += 32)
-                *reinterpret_cast<uint4 *>(p + i % blocks * kYBlk + (live + i / (8 * blocks)) * 128 +
-                                           i / blocks % 8 * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect())
-                mbar_arrive(full);
-        };
-        for (int i = 0; i < steps && !wait.dead; ++i, r1.step(), r2.step()) {
+        Ring<SM::kY1> r1;
+        for (int i = 0; i < steps && !wait.dead; ++i, r1.step()) {
             const int first = y_first + i * kStep, live = ly - first, y = (kKeys ? q0 : k0) + first;
             float cl[kStep / 32], cd[kStep / 32];
             if (kKeys)
@@ -203,9 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             if (r1.round > 0)
                 wait(&sm.y1_empty[r1.slot], (r1.round - 1) & 1);
+            else if (!kKeys && r1.slot == SM::kY1 - 2)
+                wait(&sm.x_full, 0);
             if (wait.dead)
                 break;
-            uint64_t *bar = live < kStep ? &sm.tail : &sm.y1_full[r1.slot];
+            uint64_t *bar = live < kStep ? &sm.tail[0] : &sm.y1_full[r1.slot];
             if (elect()) {
                 mbar_arrive_expect_tx(bar, 3 * kYBlk);
                 tma_load_4d(sm.y1[r1.slot], &maps.y1, 0, y, h, 0, bar);
@@ -221,208 +266,255 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mbar_arrive(&sm.y1_full[r1.slot]);
             }
-            if (live < kStep)
+            if (live < kStep) {
+                wait(&sm.tail[0], 0);
                 zero_tail(sm.y1[r1.slot], 3, live, &sm.y1_full[r1.slot]);
-            if (r2.round > 0)
-                wait(&sm.y2_empty[r2.slot], (r2.round - 1) & 1);
-            if (wait.dead)
-                break;
-            bar = live < kStep ? &sm.tail : &sm.y2_full[r2.slot];
+            }
+        }
+    } else if (warp == kElemWarps + 1) {
+        // ---------------- S, as soon as the threads have read the one before
+        constexpr uint32_t id = tc::idesc_bf16(kRows, kStep, false, false);
+        const Desc x1(smem_u32(sm.x1), 16, 1024, tc::kSw128), y1(smem_u32(sm.y1[0]), 16, 1024, tc::kSw128);
+        Ring<SM::kY1> r1;
+        if (steps > 0)
+            wait(kKeys ? &sm.x_landed : &sm.x_full, 0);
+        for (int i = 0; i < steps && !wait.dead; ++i, r1.step()) {
+            wait(&sm.y1_full[r1.slot], r1.round & 1);
+            if (i > 0)
+                wait(&sm.s_read, (i - 1) & 1);
+            tc::fence_after_sync();
+            if (elect()) {
+                const uint32_t y0 = r1.slot * 3 * kYBlk;
+#pragma unroll
+                for (int ks = 0; ks < kDQ / 16; ++ks) {
+                    const uint64_t b = y1.at(y0 + (ks >> 2) * kYBlk + (ks & 3) * 32);
+                    if (kKeys)
+                        tc::mma_bf16(tmem + C::S, x1.at((ks >> 2) * kXBlk + (ks & 3) * 32), b, id, ks > 0 ? 1u : 0u);
+                    else
+                        tc::mma_bf16_ts(tmem + C::S, tmem + C::X1 + ks * 8, b, id, ks > 0 ? 1u : 0u);
+                }
+                tc::commit(&sm.s_full[i & 1]);
+            }
+        }
+    } else if (warp == kElemWarps + 3) {
+        // ---------------- dP, likewise, and the copies of Y2
+        constexpr uint32_t id = tc::idesc_bf16(kRows, kStep, false, false);
+        const Desc y2(smem_u32(sm.y2[0]), 16, 1024, tc::kSw128);
+        auto fetch = [&](int i, int slot) {
+            const int first = y_first + i * kStep, live = ly - first;
+            uint64_t *bar = live < kStep ? &sm.tail[1] : &sm.y2_full[slot];
             if (elect()) {
                 mbar_arrive_expect_tx(bar, 2 * kYBlk);
-                tma_load_4d(sm.y2[r2.slot], &maps.y2, 0, y, h, kKeys ? 0 : 2, bar);
+                tma_load_4d(sm.y2[slot], &maps.y2, 0, (kKeys ? q0 : k0) + first, h, kKeys ? 0 : 2, bar);
             }
             __syncwarp();
-            if (live < kStep)
-                zero_tail(sm.y2[r2.slot], 2, live, &sm.y2_full[r2.slot]);
-        }
-    } else if (warp == kElem / 32 + 1) {
-        // ---------------- products
-        constexpr uint32_t id_s = tc::idesc_bf16(kRows, kStep, false, false), id_1 = tc::idesc_bf16(kRows, kDQ, false, true),
-                           id_2 = tc::idesc_bf16(kRows, kDV, false, true);
-        const Desc x1(smem_u32(sm.x1), 16, 1024, tc::kSw128), x2(smem_u32(sm.x2), 16, 1024, tc::kSw128),
-            y1(smem_u32(sm.y1[0]), 16, 1024, tc::kSw128), y2(smem_u32(sm.y2[0]), 16, 1024, tc::kSw128),
-            t1(smem_u32(sm.y1[0]), kYBlk, 1024, tc::kSw128), t2(smem_u32(sm.y2[0]), kYBlk, 1024, tc::kSw128);
-        // tensor-memory column of the 16 Y rows ks of p or e: each group's at its own start
-        auto a_col = [](uint32_t base, int ks) { return base + (ks >> 1) * kPart + (ks & 1) * 8; };
-        static_assert(kPart == 32, "two 16-row steps a group");
-        auto scores = [&](uint32_t slot) {
-            if (elect()) {
-#pragma unroll
-                for (int ks = 0; ks < kDQ / 16; ++ks)
-                    tc::mma_bf16(tmem + kColS, x1.at((ks >> 2) * kXBlk + (ks & 3) * 32),
-                                 y1.at(slot * 3 * kYBlk + (ks >> 2) * kYBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                tc::commit(&sm.s_full);
+            if (live < kStep) {
+                wait(&sm.tail[1], 0);
+                zero_tail(sm.y2[slot], 2, live, &sm.y2_full[slot]);
             }
         };
-        auto dps = [&](uint32_t slot) {
+        for (int i = 0; i < SM::kY2 && i < steps; ++i)
+            fetch(i, i);
+        Ring<SM::kY2> r2, rf;
+        if (steps > 0)
+            wait(&sm.x_full, 0);
+        for (int i = 0; i < steps && !wait.dead; ++i, r2.step()) {
+            wait(&sm.y2_full[r2.slot], r2.round & 1);
+            if (i > 0)
+                wait(&sm.dp_read, (i - 1) & 1);
+            tc::fence_after_sync();
             if (elect()) {
+                const uint32_t y0 = r2.slot * 2 * kYBlk;
 #pragma unroll
                 for (int ks = 0; ks < kDV / 16; ++ks)
-                    tc::mma_bf16(tmem + kColP, x2.at((ks >> 2) * kXBlk + (ks & 3) * 32),
-                                 y2.at(slot * 2 * kYBlk + (ks >> 2) * kYBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                tc::commit(&sm.dp_full);
-                if (!kKeys)
-                    tc::commit(&sm.y2_empty[slot]);
+                    tc::mma_bf16_ts(tmem + C::P, tmem + C::X2 + ks * 8, y2.at(y0 + (ks >> 2) * kYBlk + (ks & 3) * 32), id,
+                                    ks > 0 ? 1u : 0u);
+                tc::commit(&sm.dp_full[i & 1]);
             }
-        };
-        Ring<kY1> r1;  // of step i + 1
-        Ring<kY2> r2;
-        uint32_t now1 = 0, now2 = 0;
-        if (steps > 0) {
-            wait(&sm.x_full, 0);
-            wait(&sm.y1_full[0], 0);
-            tc::fence_after_sync();
-            scores(0);
-            wait(&sm.y2_full[0], 0);
-            tc::fence_after_sync();
-            dps(0);
-            r1.step();
-            r2.step();
+            // dP(i - 1) has been read; once acc2(i - 1) is over its Y2 makes room
+            if (i > 0) {
+                if (i - 1 + SM::kY2 < steps) {
+                    if (kKeys)
+                        wait(&sm.y2_empty[rf.slot], rf.round & 1);
+                    if (!wait.dead)
+                        fetch(i - 1 + SM::kY2, rf.slot);
+                }
+                rf.step();
+            }
         }
+    } else if (warp == kElemWarps + 2) {
+        // ---------------- the sums
+        constexpr uint32_t id_1 = tc::idesc_bf16(kRows, kDQ, false, true), id_2 = tc::idesc_bf16(kRows, kDV, false, true);
+        const Desc t1(smem_u32(sm.y1[0]), kYBlk, 1024, tc::kSw128), t2(smem_u32(sm.y2[0]), kYBlk, 1024, tc::kSw128),
+            ed(smem_u32(sm.e), 16, 1024, tc::kSw128), pd(smem_u32(sm.p), 16, 1024, tc::kSw128);
+        Ring<SM::kY1> r1;
+        Ring<SM::kY2> r2;
         for (int i = 0; i < steps && !wait.dead; ++i, r1.step(), r2.step()) {
-            wait(&sm.p_full, i & 1);  // p(i) written, or at least S(i) read
-            tc::fence_after_sync();
-            if (kKeys && elect()) {
-#pragma unroll
-                for (int ks = 0; ks < kStep / 16; ++ks)
-                    tc::mma_bf16_ts(tmem + kCol2, tmem + a_col(kColS, ks), t2.at(now2 * 2 * kYBlk + ks * 2048), id_2,
-                                    i > 0 || ks > 0 ? 1u : 0u);
-                tc::commit(&sm.y2_empty[now2]);
-            }
-            if (i + 1 < steps) {
-                wait(&sm.y1_full[r1.slot], r1.round & 1);
+            const uint32_t buf = i & 1, par = (i >> 1) & 1;
+            if (kKeys) {
+                wait(&sm.y2_full[r2.slot], r2.round & 1);
+                wait(&sm.p_full[buf], par);
                 tc::fence_after_sync();
-                scores(r1.slot);
+                if (elect()) {
+#pragma unroll
+                    for (int ks = 0; ks < kStep / 16; ++ks)
+                        tc::mma_bf16(tmem + C::Acc2, pd.at(ks * 32), t2.at(r2.slot * 2 * kYBlk + ks * 2048), id_2,
+                                     i > 0 || ks > 0 ? 1u : 0u);
+                    tc::commit(&sm.acc2_done[buf]);
+                    tc::commit(&sm.y2_empty[r2.slot]);
+                }
             }
-            wait(&sm.e_full, i & 1);
+            wait(&sm.e_full[buf], par);
             tc::fence_after_sync();
             if (elect()) {
 #pragma unroll
                 for (int ks = 0; ks < kStep / 16; ++ks)
-                    tc::mma_bf16_ts(tmem + kCol1, tmem + a_col(kColP, ks), t1.at(now1 * 3 * kYBlk + ks * 2048), id_1,
-                                    i > 0 || ks > 0 ? 1u : 0u);
-                tc::commit(&sm.y1_empty[now1]);
+                    tc::mma_bf16(tmem + C::Acc1, ed.at(ks * 32), t1.at(r1.slot * 3 * kYBlk + ks * 2048), id_1,
+                                 i > 0 || ks > 0 ? 1u : 0u);
+                tc::commit(&sm.acc1_done[buf]);
+                tc::commit(&sm.y1_empty[r1.slot]);
                 if (i + 1 == steps)
                     tc::commit(&sm.done);
             }
-            if (i + 1 < steps) {
-                wait(&sm.y2_full[r2.slot], r2.round & 1);
-                tc::fence_after_sync();
-                dps(r2.slot);
-            }
-            now1 = r1.slot;
-            now2 = r2.slot;
         }
     } else {
-        // ---------------- elementwise: row r0 + r, columns group * 32 ..
-        const int r = (warp & 3) * 32 + lane, group = warp >> 2;
+        // ---------------- elementwise: half a row a thread, every other step
+        const int r = (warp & 3) * 32 + lane, quarter = warp >> 2, half = quarter & 1, set = quarter >> 1;
         const bool live = r < rows;
-        const uint32_t addr = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, group * kPart);
+        const uint32_t base = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, 0);
         const float sl2 = a.scale * kLog2e;
         float lse2 = INFINITY, delta = 0.0f;
-        if constexpr (!kKeys) {
-            const int64_t row = (int64_t)(q0 + r0 + r) * a.H + h;
-            if (live && group < 2) {  // half a row each
-                const uint4 *x = reinterpret_cast<const uint4 *>(a.o + row * kDV + group * 64);
-                const uint4 *y = reinterpret_cast<const uint4 *>(a.dO + row * kDV + group * 64);
+        auto arrive = [&](uint64_t *bar) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+        };
+        // X to tensor memory (a row a lane), 64 numbers a warp at a time
+        if (steps > 0 && (!kKeys || quarter < 2)) {
+            wait(&sm.x_landed, 0);
+            if (!kKeys && quarter < 3)
+                keep_64(base + C::X1 + quarter * 32, sm.y1[SM::kY1 - 2] + quarter * kXBlk, r);
+            else if (kKeys)
+                keep_64(base + C::X2 + quarter * 32, sm.e + quarter * kXBlk, r);
+            else
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint4 u = x[c], v = y[c];
+                for (int b = 0; b < 2; ++b)
+                    keep_64(base + C::X2 + b * 32, sm.e + b * kXBlk, r);
+            tc::wait_st();
+            tc::fence_before_sync();
+            arrive(&sm.x_full);
+        }
+        if constexpr (!kKeys) {
+            // D, 16 lanes a row
+#pragma unroll
+            for (int k = 0; k < kRows / kElemWarps / 2; ++k) {
+                const int dr = warp * (kRows / kElemWarps) + k * 2 + (lane >> 4);
+                float d = 0.0f;
+                if (dr < rows) {
+                    const int64_t at = ((int64_t)(q0 + r0 + dr) * a.H + h) * kDV + (lane & 15) * 8;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(a.o + at), v = *reinterpret_cast<const uint4 *>(a.dO + at);
                     const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = unpack_bf16x2(uw[k]), g = unpack_bf16x2(vw[k]);
-                        delta += f.x * g.x + f.y * g.y;
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 f = unpack_bf16x2(uw[c]), g = unpack_bf16x2(vw[c]);
+                        d += f.x * g.x + f.y * g.y;
                     }
                 }
+#pragma unroll
+                for (int c = 8; c > 0; c >>= 1)
+                    d += __shfl_xor_sync(0xffffffffu, d, c);
+                if ((lane & 15) == 0)
+                    sm.delta[dr] = d;
             }
-            if (group < 2)
-                sm.dsum[group][r] = delta;
-            const float l = live ? a.lse[row] : -INFINITY;
+            const float l = live ? a.lse[(int64_t)(q0 + r0 + r) * a.H + h] : -INFINITY;
             lse2 = l == -INFINITY ? INFINITY : l * kLog2e;  // a row that sees no key: weights 0
             elem_sync();
-            delta = sm.dsum[0][r] + sm.dsum[1][r];
-            if (live && group == 0) {
+            delta = sm.delta[r];
+            if (live && quarter == 0) {
                 a.delta[(int64_t)h * a.Tq + q0 + r0 + r] = delta;
                 a.lse2[(int64_t)h * a.Tq + q0 + r0 + r] = lse2;
             }
         }
-        Ring<kY1> r1;
-        for (int i = 0; i < steps; ++i, r1.step()) {
-            const int y = y_first + i * kStep + group * kPart;  // place of the first column
+        for (int i = set; i < steps; i += 2) {
+            const int y = y_first + i * kStep;  // place of the step's first column
+            const uint32_t par = (i >> 1) & 1;
+            const int slot = i % SM::kY1, round = i / SM::kY1;
             // columns lo .. hi - 1 are visible to the row
-            int lo = 0, hi = kPart;
+            int lo = 0, hi;
             bool edge;
             if (kKeys) {
-                edge = i + 1 == steps || (a.causal && r0 + kRows - 1 > y_first + i * kStep + off);
+                edge = y + kStep > ly || (a.causal && r0 + kRows - 1 > y + off);
                 hi = ly - y;
                 lo = a.causal ? r0 + r - off - y : 0;
             } else {
-                edge = (i + 1) * kStep > (a.causal ? min(ly, r0 + off + 1) : ly);
+                edge = y + kStep > (a.causal ? min(ly, r0 + off + 1) : ly);
                 hi = (a.causal ? min(ly, r0 + r + off + 1) : ly) - y;
             }
-            float p[kPart], x[kPart];
-            wait(&sm.s_full, i & 1);
+            const uint32_t seen = edge ? bit_span(lo - half * 32, hi - half * 32) : 0xffffffffu;
+            float p[32], x[32];
+            wait(&sm.s_full[set], par);
             tc::fence_after_sync();
-            load_part(addr + kColS, p);
+            load_32(base + C::S + half * 32, p);
+            tc::fence_before_sync();
+            arrive(&sm.s_read);
             if (kKeys) {
-                wait(&sm.y1_full[r1.slot], r1.round & 1);  // the step's lse and D
-                const float4 *l = reinterpret_cast<const float4 *>(sm.col[r1.slot][0] + group * kPart);
+                wait(&sm.y1_full[slot], round & 1);  // the step's lse and D
+                const float4 *l = reinterpret_cast<const float4 *>(sm.col[slot][0] + half * 32);
 #pragma unroll
-                for (int c = 0; c < kPart / 4; ++c) {
-                    const float4 v = l[c];
-                    p[4 * c] = ex2(fmaf(p[4 * c], sl2, -v.x));
-                    p[4 * c + 1] = ex2(fmaf(p[4 * c + 1], sl2, -v.y));
-                    p[4 * c + 2] = ex2(fmaf(p[4 * c + 2], sl2, -v.z));
-                    p[4 * c + 3] = ex2(fmaf(p[4 * c + 3], sl2, -v.w));
+                for (int k = 0; k < 8; ++k) {
+                    const float4 v = l[k];
+                    p[4 * k] = ex2(fmaf(p[4 * k], sl2, -v.x));
+                    p[4 * k + 1] = ex2(fmaf(p[4 * k + 1], sl2, -v.y));
+                    p[4 * k + 2] = ex2(fmaf(p[4 * k + 2], sl2, -v.z));
+                    p[4 * k + 3] = ex2(fmaf(p[4 * k + 3], sl2, -v.w));
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kPart; ++c)
-                    p[c] = ex2(fmaf(p[c], sl2, -lse2));
+                for (int k = 0; k < 32; ++k)
+                    p[k] = ex2(fmaf(p[k], sl2, -lse2));
             }
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < kPart; ++c)
-                    if (c < lo || c >= hi)
-                        p[c] = 0.0f;
+                for (int k = 0; k < 32; ++k)
+                    p[k] = seen >> k & 1 ? p[k] : 0.0f;
             }
-            if (kKeys)
-                store_part(addr + kColS, p);
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.p_full);
-            wait(&sm.dp_full, i & 1);
-            tc::fence_after_sync();
-            load_part(addr + kColP, x);
             if (kKeys) {
-                const float4 *d = reinterpret_cast<const float4 *>(sm.col[r1.slot][1] + group * kPart);
+                if (i > 0)
+                    wait(&sm.acc2_done[set ^ 1], ((i - 1) >> 1) & 1);
+                store_32(sm.p, r, half * 4, p);
+                fence_proxy_async_smem();
+                arrive(&sm.p_full[set]);
+            }
+            wait(&sm.dp_full[set], par);
+            tc::fence_after_sync();
+            load_32(base + C::P + half * 32, x);
+            tc::fence_before_sync();
+            arrive(&sm.dp_read);
+            if (kKeys) {
+                const float4 *d = reinterpret_cast<const float4 *>(sm.col[slot][1] + half * 32);
 #pragma unroll
-                for (int c = 0; c < kPart / 4; ++c) {
-                    const float4 v = d[c];
-                    x[4 * c] = p[4 * c] * (x[4 * c] - v.x);
-                    x[4 * c + 1] = p[4 * c + 1] * (x[4 * c + 1] - v.y);
-                    x[4 * c + 2] = p[4 * c + 2] * (x[4 * c + 2] - v.z);
-                    x[4 * c + 3] = p[4 * c + 3] * (x[4 * c + 3] - v.w);
+                for (int k = 0; k < 8; ++k) {
+                    const float4 v = d[k];
+                    x[4 * k] = p[4 * k] * (x[4 * k] - v.x);
+                    x[4 * k + 1] = p[4 * k + 1] * (x[4 * k + 1] - v.y);
+                    x[4 * k + 2] = p[4 * k + 2] * (x[4 * k + 2] - v.z);
+                    x[4 * k + 3] = p[4 * k + 3] * (x[4 * k + 3] - v.w);
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kPart; ++c)
-                    x[c] = p[c] * (x[c] - delta);
+                for (int k = 0; k < 32; ++k)
+                    x[k] = p[k] * (x[k] - delta);
             }
             if (edge) {  // a hidden pair's dP may be anything
 #pragma unroll
-                for (int c = 0; c < kPart; ++c)
-                    if (c < lo || c >= hi)
-                        x[c] = 0.0f;
+                for (int k = 0; k < 32; ++k)
+                    x[k] = seen >> k & 1 ? x[k] : 0.0f;
             }
-            store_part(addr + kColP, x);
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.e_full);
+            if (i > 0)
+                wait(&sm.acc1_done[set ^ 1], ((i - 1) >> 1) & 1);
+            store_32(sm.e, r, half * 4, x);
+            fence_proxy_async_smem();
+            arrive(&sm.e_full[set]);
         }
         // ---- the sums, through shared memory (nothing reads the tiles any more), so that the
         // writes are whole rows
@@ -430,31 +522,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(&sm.done, 0);
             tc::fence_after_sync();
         }
-        const uint32_t base = tc::taddr(tmem, (uint32_t)(warp & 3) * 32, 0);
         constexpr int kVecs = (kKeys ? kDKV : kDQ) / 8;  // 16-byte vectors of a row of dkv or dq
-        unsigned char *rowbuf = sm.x1;                   // x1 and x2: 80 KB
-        float *part = reinterpret_cast<float *>(sm.y1[0]);
-        static_assert(kRows * kDKV * 2 <= 5 * kXBlk && kRows * kDR * 4 <= kY1 * 3 * kYBlk, "room for the sums");
+        unsigned char *rowbuf = sm.y1[0];
+        float *part = reinterpret_cast<float *>(sm.e);
+        static_assert(sizeof(sm.y1) >= kRows * kVecs * 16 && 2 * kXBlk >= kRows * kDR * 4, "room for the sums");
         if (steps > 0) {
             if (kKeys) {
-                // dk (4 x 32 columns), dv (4 x 32), the rope part of dk (2 x 32), a group every third
+                // dk (4 x 32 columns), dv (4 x 32), the rope part of dk (2 x 32), shared out to the groups
 #pragma unroll 1
-                for (int c = group; c < 8; c += kGroups)
-                    stage_bf16(rowbuf, kVecs, r, c * 4, base + (c < 4 ? kCol1 + c * 32 : kCol2 + (c - 4) * 32),
-                               c < 4 ? a.scale : 1.0f);
-                if (group > 0) {
+                for (int c = quarter; c < 10; c += 4) {
+                    if (c < 8) {
+                        stage_bf16(rowbuf, kVecs, r, c * 4, base + (c < 4 ? C::Acc1 + c * 32 : C::Acc2 + (c - 4) * 32),
+                                   c < 4 ? a.scale : 1.0f);
+                        continue;
+                    }
                     float x[32];
-                    load_part(base + kCol1 + kDN + (group - 1) * 32, x);
+                    load_32(base + C::Acc1 + kDN + (c - 8) * 32, x);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4 *>(part + r * kDR + ((((group - 1) * 8 + i) ^ (r & 7)) << 2)) =
+                        *reinterpret_cast<float4 *>(part + r * kDR + ((((c - 8) * 8 + i) ^ (r & 7)) << 2)) =
                             make_float4(x[4 * i] * a.scale, x[4 * i + 1] * a.scale, x[4 * i + 2] * a.scale,
                                         x[4 * i + 3] * a.scale);
                 }
             } else {
 #pragma unroll 1
-                for (int c = group; c < 6; c += kGroups)
-                    stage_bf16(rowbuf, kVecs, r, c * 4, base + kCol1 + c * 32, a.scale);
+                for (int c = quarter; c < 6; c += 4)
+                    stage_bf16(rowbuf, kVecs, r, c * 4, base + C::Acc1 + c * 32, a.scale);
             }
         }
         elem_sync();
@@ -478,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kElem / 32)
+    if (warp == kElemWarps)
         tc::tmem_dealloc(tmem, 512);
 }
 
@@ -511,8 +604,8 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 template <bool kKeys>
 cudaError_t launch_side(const BwdMaps &maps, const BwdArgs &a, cudaStream_t s)
 {
-    const size_t smem = sizeof(BwdSmem) + 1024;
-    static_assert(sizeof(BwdSmem) + 1024 <= 232448, "shared memory of one CTA");
+    const size_t smem = sizeof(BwdSmem<kKeys>) + 1024;
+    static_assert(sizeof(BwdSmem<kKeys>) + 1024 <= 232448, "shared memory of one CTA");
     const cudaError_t e =
         cudaFuncSetAttribute(mla_bwd_kernel<kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)

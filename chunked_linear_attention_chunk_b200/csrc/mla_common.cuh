@@ -35,8 +35,9 @@ __device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *sh)
 
 // Work item x of the list that has count(0) items for sequence 0, then count(1) for sequence 1,
 // and so on: its sequence and its place among that sequence's items, or seq = -1 past the end.
-// `count` sees every sequence once and sets `bad` for what is not to be used; the CTA learns of
-// it whichever of its threads saw it.  All threads of the CTA call; `sh` is 40 int64 of shared
+// `count` sees every sequence and sets `bad` for what is not to be used; the whole CTA learns of
+// it.  Up to 256 sequences every warp goes through the list by itself (a few hundred cycles, no
+// barrier); beyond that the CTA's threads share it.  All threads call; `sh` is 40 int64 of shared
 // memory.
 struct Item {
     int seq, k;
@@ -47,19 +48,35 @@ __device__ __forceinline__ Item find_item(int N, int64_t x, Count count, int64_t
 {
     static_assert(kThreads % 32 == 0 && kThreads <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto scan = [&](int64_t c) {  // inclusive sum over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
+            c += lane >= d ? y : 0;
+        }
+        return c;
+    };
     bool bad = false;
     int64_t base = 0;
+    Item it{-1, 0, false};
+    if (N <= 256) {
+        for (int s0 = 0; s0 < N; s0 += 32) {
+            const int64_t c = s0 + lane < N ? count(s0 + lane, bad) : 0, inc = scan(c), rel = x - base - (inc - c);
+            const uint32_t hit = __ballot_sync(0xffffffffu, rel >= 0 && rel < c);
+            if (hit) {
+                it.seq = s0 + __ffs(hit) - 1;
+                it.k = (int)__shfl_sync(0xffffffffu, rel, __ffs(hit) - 1);
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        it.bad = __any_sync(0xffffffffu, bad);
+        return it;
+    }
     if (tid == 0)
         sh[33] = -1;
     for (int s0 = 0; s0 < N; s0 += kThreads) {
         const int s = s0 + tid;
-        const int64_t c = s < N ? count(s, bad) : 0;
-        int64_t inc = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-            inc += lane >= d ? y : 0;
-        }
+        const int64_t c = s < N ? count(s, bad) : 0, inc = scan(c);
         if (lane == 31)
             sh[warp] = inc;
         __syncthreads();
@@ -74,10 +91,8 @@ __device__ __forceinline__ Item find_item(int N, int64_t x, Count count, int64_t
             sh[34] = rel;
         }
         base += total;
-        if (s0 + kThreads < N)
-            __syncthreads();
+        __syncthreads();
     }
-    Item it;
     it.bad = __syncthreads_or(bad) != 0;
     it.seq = (int)sh[33];
     it.k = (int)sh[34];
@@ -102,6 +117,14 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Bits [lo, hi) of a word (bounds may lie outside 0 .. 32).
+__device__ __forceinline__ uint32_t bit_span(int lo, int hi)
+{
+    const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1;
+    const uint32_t skip = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1;
+    return below & ~skip;
 }
 
 }  // namespace mla

@@ -71,6 +71,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     FwdSmem &sm = *reinterpret_cast<FwdSmem *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x % a.H;
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.v_tail, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+        }
+        fence_mbar_init_cluster();
+    }
     const Item it = find_item<kThreads>(
         a.N, blockIdx.x / a.H,
         [&](int n, bool &bad) {
@@ -93,20 +107,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_steps = max(n_steps, steps[t]);
     }
 
-    if (tid == 0) {
-        mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.v_tail, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.k_full[i], 1);
-            mbar_init(&sm.k_empty[i], 1);
-            mbar_init(&sm.v_full[i], 1);
-            mbar_init(&sm.v_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.pv_done[i], 1);
-        }
-        fence_mbar_init_cluster();
-    }
     if (warp == 8)
         tc::tmem_alloc(&sm.tmem_slot, 512);
     tc::fence_before_sync();
@@ -223,11 +223,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::wait_ld();
             if ((j + 1) * kKeys - 1 > last_0) {
 #pragma unroll
-                for (int c = 0; c < 3; ++c)
+                for (int c = 0; c < 3; ++c) {
+                    const uint32_t seen = bit_span(0, last + 1 - j * kKeys - c * 32);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (j * kKeys + c * 32 + i > last)
-                            x[c][i] = __float_as_uint(-INFINITY);
+                        x[c][i] = seen >> i & 1 ? x[c][i] : __float_as_uint(-INFINITY);
+                }
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
