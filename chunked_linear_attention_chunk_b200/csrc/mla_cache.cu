@@ -4,9 +4,9 @@
 // Bound by bytes: a new row is read once (1152 B) and written once (1152 or 576 B); a page that
 // held earlier rows and whose scale grows is read and written once more.  One CTA takes one
 // (page that receives rows, group): the page is where the scale lives, so one CTA sees all that
-// decides it and no two CTAs write the same page.  Its new rows stay in registers between the
-// maximum and the rounding when they fit (kKeep vectors a thread), else they are read again
-// (from L2).
+// decides it and no two CTAs write the same page.  A thread keeps one 16-byte column of eight rows
+// (64 rows over 576 threads) in registers between the maximum and the rounding; longer pages read
+// the rest again, from L2.  Two CTAs an SM keep 147 KB in flight.
 #include <cuda_fp8.h>
 
 #include "mla_common.cuh"
@@ -17,9 +17,10 @@ namespace {
 
 using namespace mla;
 
-constexpr int kThreads = 256;
 constexpr int kVecs = kDC / 8;  // 16-byte vectors of a bfloat16 row
-constexpr int kKeep = 18;       // 64 rows of a group over 256 threads
+constexpr int kPass = 8;        // rows the CTA takes at once
+constexpr int kThreads = kPass * kVecs;
+constexpr int kKeep = 8;        // passes held in registers: 64 rows
 
 struct AppendArgs {
     int N, T_new, G, max_pages, num_pages, page_size;
@@ -30,7 +31,7 @@ struct AppendArgs {
     unsigned int *status;
 };
 
-__device__ __forceinline__ float amax8(uint4 v)
+__device__ __forceinline__ uint32_t amax8(uint4 v)
 {
     // |x| of two bfloat16 a word, compared as integers: NaN is above infinity, which is above all
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -38,7 +39,7 @@ __device__ __forceinline__ float amax8(uint4 v)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-    return __uint_as_float(m);
+    return m;
 }
 
 // Two floats to two e4m3 codes, to nearest even (saturating; the caller's scale leaves |x| <= 448).
@@ -59,10 +60,10 @@ __device__ __forceinline__ uint2 quantise8(uint4 v, float inv)
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// The smallest power of two s >= 2^-100 with amax <= 448 s; NaN for an infinite or NaN amax.
-__device__ __forceinline__ float scale_for(float amax)
+// The smallest power of two s >= 2^-100 with amax <= 448 s, for the bits of amax; NaN for an
+// infinite or NaN one.
+__device__ __forceinline__ float scale_for(uint32_t b)
 {
-    const uint32_t b = __float_as_uint(amax);
     if (b >= 0x7f800000u)
         return __uint_as_float(0x7fc00000u);
     // amax = 1.f 2^(E - 127); 448 = 1.75 2^8
@@ -71,10 +72,10 @@ __device__ __forceinline__ float scale_for(float amax)
 }
 
 template <bool kE4M3>
-__global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 2) mla_append_kernel(AppendArgs a)
 {
     __shared__ int64_t sh[40];
-    __shared__ float s_max[kThreads / 32];
+    __shared__ uint32_t s_max[kThreads / 32];
     const int tid = threadIdx.x, ps = a.page_size;
     // sequence n touches the pages of its places [len, len + new rows)
     const Item it = find_item<kThreads>(
@@ -100,39 +101,40 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
     const int slot0 = it.k == 0 ? len % ps : 0;                         // first slot written
     const int64_t first = it.k == 0 ? 0 : (int64_t)it.k * ps - len % ps;  // its row among the sequence's
     const int rows = (int)min((int64_t)(ps - slot0), m - first);
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.x + ((a.cu[n] + first) * a.G + g) * kDC);
-    const int64_t src_row = (int64_t)a.G * kVecs;  // 16-byte vectors from a row to the next
-    const int64_t dst0 = (((int64_t)page * ps + slot0) * a.G + g) * kDC;
-    const int nvec = rows * kVecs;
+    const int r0 = tid / kVecs, vec = tid % kVecs;  // this thread's first row and its vector
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.x + ((a.cu[n] + first + r0) * a.G + g) * kDC) + vec;
+    const int64_t step = (int64_t)kPass * a.G * kVecs;  // vectors from a pass to the next
+    const int64_t row0 = ((int64_t)page * ps + slot0 + r0) * a.G + g;
     if constexpr (!kE4M3) {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + dst0);
-        for (int v = tid; v < nvec; v += kThreads)
-            dst[v / kVecs * src_row + v % kVecs] = src[v / kVecs * src_row + v % kVecs];
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + row0 * kDC) + vec;
+#pragma unroll 4
+        for (int i = 0; i * kPass + r0 < rows; ++i)
+            dst[i * step] = src[i * step];
         return;
     }
     uint4 keep[kKeep];
-    float mx = 0.0f;
+    uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        const int v = tid + i * kThreads;
-        if (v < nvec) {
-            keep[i] = src[v / kVecs * src_row + v % kVecs];
-            mx = __uint_as_float(max(__float_as_uint(mx), __float_as_uint(amax8(keep[i]))));
-        }
-    }
-    for (int v = tid + kKeep * kThreads; v < nvec; v += kThreads)
-        mx = __uint_as_float(max(__float_as_uint(mx), __float_as_uint(amax8(src[v / kVecs * src_row + v % kVecs]))));
-    uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+    for (int i = 0; i < kKeep; ++i)
+        if (i * kPass + r0 < rows)
+            keep[i] = src[i * step];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (i * kPass + r0 < rows)
+            mx = max(mx, amax8(keep[i]));
+    for (int i = kKeep; i * kPass + r0 < rows; ++i)
+        mx = max(mx, amax8(src[i * step]));
+    mx = __reduce_max_sync(0xffffffffu, mx);
     if ((tid & 31) == 0)
-        s_max[tid >> 5] = __uint_as_float(mb);
+        s_max[tid >> 5] = mx;
     float *sp = a.cache_scale + (int64_t)page * a.G + g;
     const float old = slot0 > 0 ? *sp : 0.0f;  // read by all before one thread writes it (barrier between)
     __syncthreads();
-    mb = 0;
+    mx = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
-        mb = max(mb, __float_as_uint(s_max[w]));
-    const float need = scale_for(__uint_as_float(mb));
+        mx = max(mx, s_max[w]);
+    const float need = scale_for(mx);
     // a NaN scale (new or held) stays NaN
     const float now = slot0 > 0 ? (need != need || old != old ? __uint_as_float(0x7fc00000u) : fmaxf(need, old)) : need;
     if (tid == 0)
@@ -140,34 +142,30 @@ __global__ void __launch_bounds__(kThreads) mla_append_kernel(AppendArgs a)
     unsigned char *codes = static_cast<unsigned char *>(a.cache);
     if (slot0 > 0 && !(now == old)) {  // earlier rows of the page, at the larger scale
         const float f = old / now;
-        const int64_t base = ((int64_t)page * ps * a.G + g) * kDC;
-        for (int v = tid; v < slot0 * kVecs; v += kThreads) {
-            uint2 *p = reinterpret_cast<uint2 *>(codes + base + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8);
+        unsigned char *held = codes + (((int64_t)page * ps + r0) * a.G + g) * kDC + vec * 8;
+        for (int i = 0; i * kPass + r0 < slot0; ++i) {
+            uint2 *p = reinterpret_cast<uint2 *>(held + i * step * 8);
             const uint2 u = *p;
             const uint32_t w[2] = {u.x, u.y};
             uint32_t r[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3);
-                const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> 16), __NV_E4M3);
+            for (int k = 0; k < 2; ++k) {
+                const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k] & 0xffffu), __NV_E4M3);
+                const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k] >> 16), __NV_E4M3);
                 const float2 f0 = __half22float2(__half2(h0)), f1 = __half22float2(__half2(h1));
-                r[i] = e4m3x2(f0.x * f, f0.y * f) | (e4m3x2(f1.x * f, f1.y * f) << 16);
+                r[k] = e4m3x2(f0.x * f, f0.y * f) | (e4m3x2(f1.x * f, f1.y * f) << 16);
             }
             *p = make_uint2(r[0], r[1]);
         }
     }
-    // 1 / now as a power of two's exact reciprocal (now >= 2^-100)
-    const float inv = 1.0f / now;
-    unsigned char *dst = codes + dst0;
+    const float inv = 1.0f / now;  // exact: a power of two from 2^-100 to 2^120
+    unsigned char *dst = codes + row0 * kDC + vec * 8;
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        const int v = tid + i * kThreads;
-        if (v < nvec)
-            *reinterpret_cast<uint2 *>(dst + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8) = quantise8(keep[i], inv);
-    }
-    for (int v = tid + kKeep * kThreads; v < nvec; v += kThreads)
-        *reinterpret_cast<uint2 *>(dst + (int64_t)(v / kVecs) * a.G * kDC + v % kVecs * 8) =
-            quantise8(src[v / kVecs * src_row + v % kVecs], inv);
+    for (int i = 0; i < kKeep; ++i)
+        if (i * kPass + r0 < rows)
+            *reinterpret_cast<uint2 *>(dst + i * step * 8) = quantise8(keep[i], inv);
+    for (int i = kKeep; i * kPass + r0 < rows; ++i)
+        *reinterpret_cast<uint2 *>(dst + i * step * 8) = quantise8(src[i * step], inv);
 }
 
 }  // namespace
