@@ -561,19 +561,22 @@ def kda_decode_step(q, k, v, a, beta, S, g_min: float = -5.0, o=None):
 
 MLA_DIMS = (128, 64, 128)     # dn, dr, dv of the expanded latent attention
 MLA_CACHE_DIMS = (512, 64)    # dl, dr of a cached row
+_MLA_SCALE = sum(MLA_DIMS[:2]) ** -0.5
+_MLA_ROW = sum(MLA_CACHE_DIMS)
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
 def _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale):
     dn, dr, dv = MLA_DIMS
-    if any(t.dtype != torch.bfloat16 for t in (q, kv, k_rope)):
+    if q.dtype != _BF16 or kv.dtype != _BF16 or k_rope.dtype != _BF16:
         raise TypeError("q, kv, k_rope must be bfloat16")
-    if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32:
+    if cu_q.dtype != _I32 or cu_k.dtype != _I32:
         raise TypeError("cu_q and cu_k must be int32")
-    if q.dim() != 3 or kv.dim() != 3 or q.shape[-1] != dn + dr or kv.shape[1:] != (q.shape[1], dn + dv) or \
-            k_rope.shape != (kv.shape[0], dr) or cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.numel() < 2:
+    qs, ks, ns = q.shape, kv.shape, cu_q.shape
+    if len(qs) != 3 or len(ks) != 3 or qs[2] != dn + dr or ks[1] != qs[1] or ks[2] != dn + dv or \
+            k_rope.shape != (ks[0], dr) or len(ns) != 1 or cu_k.shape != ns or ns[0] < 2:
         raise ValueError("shape mismatch: q [Tq,H,192], kv [Tk,H,256], k_rope [Tk,64], cu_q and cu_k [N+1]")
-    return (cu_q.numel() - 1, q.shape[0], kv.shape[0], q.shape[1],
-            (dn + dr) ** -0.5 if scale is None else float(scale))
+    return ns[0] - 1, qs[0], ks[0], qs[1], _MLA_SCALE if scale is None else float(scale)
 
 
 # The wrappers below are called once a layer and token, so they stay lean: one pass over the
@@ -582,7 +585,7 @@ def _mla_device(*ts):
     """The device that all tensors (None aside) are on; they must be contiguous CUDA tensors."""
     dev = ts[0].device
     for t in ts:
-        if t is not None and (t.device != dev or not t.is_contiguous()):
+        if t is not None and not (t.is_contiguous() and t.device == dev):
             _check_cuda(t)
             raise ValueError("all tensors must be on one device")
     if dev.type != "cuda":
@@ -595,12 +598,13 @@ def _adr(t):
 
 
 def _mla_call(name, dev, *args):
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    fn, index = getattr(_lib or lib(), name), dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
     if st != 0:
         raise KdaError(st, name)
 
@@ -628,8 +632,8 @@ def kda_mla_fwd(q, kv, k_rope, cu_q, cu_k=None, scale=None, causal: bool = True,
     N, Tq, Tk, H, scale = _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale)
     o = _out(o, (Tq, H, MLA_DIMS[2]), torch.bfloat16, dev, "o")
     lse = _out(lse, (Tq, H), torch.float32, dev, "lse")
-    _mla_call("kda_mla_fwd", dev, N, _adr(cu_q), _adr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale,
-              _adr(q), _adr(kv), _adr(k_rope), _adr(o), _adr(lse))
+    _mla_call("kda_mla_fwd", dev, N, cu_q.data_ptr(), cu_k.data_ptr(), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale,
+              q.data_ptr(), kv.data_ptr(), k_rope.data_ptr(), o.data_ptr(), lse.data_ptr())
     return o, lse
 
 
@@ -653,29 +657,30 @@ def kda_mla_bwd(q, kv, k_rope, o, lse, dO, cu_q, cu_k=None, scale=None, causal: 
     ws = _scratch(workspace, kda_mla_bwd_workspace(Tq, Tk, H), dev)
     _mla_call("kda_mla_bwd", dev, N, _adr(cu_q), _adr(cu_k), Tq, Tk, H, *MLA_DIMS, KDA_BF16, int(causal), scale, _adr(q),
               _adr(kv), _adr(k_rope), _adr(o), _adr(lse), _adr(dO), _adr(g["dq"]), _adr(g["dkv"]), _adr(g["dk_rope"]),
-              _adr(ws), ws.numel() * ws.element_size())
+              _adr(ws), ws.nbytes)
     return g
 
 
 def _mla_cache(cache, cache_scale, block_table, kv_lens):
-    if cache.dim() != 4 or cache.shape[-1] != sum(MLA_CACHE_DIMS):
+    shape, dtype = cache.shape, cache.dtype
+    if len(shape) != 4 or shape[3] != _MLA_ROW:
         raise ValueError("cache must be [num_pages, page_size, G, 576]")
-    if cache.dtype == torch.bfloat16:
+    if dtype == _BF16:
         code = KDA_BF16
-    elif cache.dtype == torch.float8_e4m3fn:
+    elif dtype == _E4M3:
         code = KDA_E4M3
     else:
         raise TypeError("cache must be bfloat16 or float8_e4m3fn")
     if (code == KDA_E4M3) != (cache_scale is not None):
         raise ValueError("cache_scale goes with a float8_e4m3fn cache, and only with one")
-    if cache_scale is not None and (cache_scale.dtype != torch.float32 or
-                                    cache_scale.shape != (cache.shape[0], cache.shape[2])):
+    if cache_scale is not None and (cache_scale.dtype != _F32 or cache_scale.shape != (shape[0], shape[2])):
         raise ValueError("cache_scale must be float32 [num_pages, G]")
-    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32:
+    if block_table.dtype != _I32 or kv_lens.dtype != _I32:
         raise TypeError("block_table and kv_lens must be int32")
-    if block_table.dim() != 2 or kv_lens.shape != block_table.shape[:1]:
+    ts = block_table.shape
+    if len(ts) != 2 or kv_lens.shape != ts[:1]:
         raise ValueError("shape mismatch: block_table [N, max_pages], kv_lens [N]")
-    return code
+    return code, shape, ts
 
 
 def kda_mla_decode_workspace(N: int, Sq: int, H: int, G: int = 1) -> int:
@@ -695,20 +700,20 @@ def kda_mla_decode(q, cache, block_table, kv_lens, scale=None, cache_scale=None,
     kv_lens int32 [N], the new tokens counted (token i sees the first kv_lens - Sq + 1 + i rows).
     ``scale`` defaults to 192 ** -0.5.  Returns (o [N,Sq,H,512] bf16, lse [N,Sq,H] float32)."""
     dev = _mla_device(q, cache, block_table, kv_lens, cache_scale, o, lse, workspace)
-    code = _mla_cache(cache, cache_scale, block_table, kv_lens)
-    if q.dtype != torch.bfloat16:
+    code, (P, ps, G, _), (_, pages) = _mla_cache(cache, cache_scale, block_table, kv_lens)
+    if q.dtype != _BF16:
         raise TypeError("q must be bfloat16")
-    if q.dim() != 4 or q.shape[0] != block_table.shape[0] or q.shape[-1] != sum(MLA_CACHE_DIMS):
+    qs = q.shape
+    if len(qs) != 4 or qs[0] != block_table.shape[0] or qs[3] != _MLA_ROW:
         raise ValueError("q must be [N, Sq, H, 576]")
-    N, Sq, H, _ = q.shape
-    P, ps, G, _ = cache.shape
+    N, Sq, H, _ = qs
     o = _out(o, (N, Sq, H, MLA_CACHE_DIMS[0]), torch.bfloat16, dev, "o")
     lse = _out(lse, (N, Sq, H), torch.float32, dev, "lse")
     ws = _scratch(workspace, _decode_workspace(N, Sq, H, G, dev.index), dev)
     _mla_call("kda_mla_decode", dev, N, Sq, H, G, *MLA_CACHE_DIMS, KDA_BF16,
-              sum(MLA_DIMS[:2]) ** -0.5 if scale is None else float(scale), _adr(q), code, _adr(cache),
-              _adr(cache_scale), P, ps, _adr(block_table), block_table.shape[1], _adr(kv_lens), _adr(o), _adr(lse),
-              _adr(ws), ws.numel() * ws.element_size())
+              _MLA_SCALE if scale is None else float(scale), q.data_ptr(), code, cache.data_ptr(), _adr(cache_scale), P,
+              ps, block_table.data_ptr(), pages, kv_lens.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+              ws.nbytes)
     return o, lse
 
 
@@ -718,15 +723,14 @@ def kda_mla_cache_append(kv_new, cu_new, kv_lens, block_table, cache, cache_scal
     keeps one power-of-two scale for each page and group in cache_scale [num_pages,G], which grows
     (and the page's earlier rows are rounded anew) where new rows need it."""
     dev = _mla_device(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
-    code = _mla_cache(cache, cache_scale, block_table, kv_lens)
-    P, ps, G, dc = cache.shape
-    if kv_new.dtype != torch.bfloat16 or cu_new.dtype != torch.int32:
+    code, (P, ps, G, dc), (N, pages) = _mla_cache(cache, cache_scale, block_table, kv_lens)
+    if kv_new.dtype != _BF16 or cu_new.dtype != _I32:
         raise TypeError("kv_new must be bfloat16, cu_new int32")
-    if kv_new.dim() != 3 or kv_new.shape[1:] != (G, dc) or cu_new.shape != (kv_lens.shape[0] + 1,):
+    xs = kv_new.shape
+    if len(xs) != 3 or xs[1] != G or xs[2] != dc or cu_new.shape != (N + 1,):
         raise ValueError("shape mismatch: kv_new [T_new,G,576], cu_new [N+1]")
-    _mla_call("kda_mla_cache_append", dev, kv_lens.shape[0], _adr(cu_new), kv_new.shape[0], G, *MLA_CACHE_DIMS, KDA_BF16,
-              _adr(kv_new), _adr(kv_lens), _adr(block_table), block_table.shape[1], code, _adr(cache),
-              _adr(cache_scale), P, ps)
+    _mla_call("kda_mla_cache_append", dev, N, cu_new.data_ptr(), xs[0], G, *MLA_CACHE_DIMS, KDA_BF16, kv_new.data_ptr(),
+              kv_lens.data_ptr(), block_table.data_ptr(), pages, code, cache.data_ptr(), _adr(cache_scale), P, ps)
 
 
 def kda_device_status(device=None) -> int:

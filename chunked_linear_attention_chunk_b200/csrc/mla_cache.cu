@@ -60,6 +60,15 @@ __device__ __forceinline__ uint2 quantise8(uint4 v, float inv)
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// Four codes times f, rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f)
+{
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
+    return e4m3x2(x.x * f, x.y * f) | (e4m3x2(y.x * f, y.y * f) << 16);
+}
+
 // The smallest power of two s >= 2^-100 with amax <= 448 s, for the bits of amax; NaN for an
 // infinite or NaN one.
 __device__ __forceinline__ float scale_for(uint32_t b)
@@ -143,19 +152,16 @@ __global__ void __launch_bounds__(kThreads, 2) mla_append_kernel(AppendArgs a)
     if (slot0 > 0 && !(now == old)) {  // earlier rows of the page, at the larger scale
         const float f = old / now;
         unsigned char *held = codes + (((int64_t)page * ps + r0) * a.G + g) * kDC + vec * 8;
-        for (int i = 0; i * kPass + r0 < slot0; ++i) {
-            uint2 *p = reinterpret_cast<uint2 *>(held + i * step * 8);
-            const uint2 u = *p;
-            const uint32_t w[2] = {u.x, u.y};
-            uint32_t r[2];
+        for (int i0 = 0; i0 * kPass + r0 < slot0; i0 += kKeep) {
+            uint2 u[kKeep];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k] & 0xffffu), __NV_E4M3);
-                const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k] >> 16), __NV_E4M3);
-                const float2 f0 = __half22float2(__half2(h0)), f1 = __half22float2(__half2(h1));
-                r[k] = e4m3x2(f0.x * f, f0.y * f) | (e4m3x2(f1.x * f, f1.y * f) << 16);
-            }
-            *p = make_uint2(r[0], r[1]);
+            for (int i = 0; i < kKeep; ++i)
+                if ((i0 + i) * kPass + r0 < slot0)
+                    u[i] = *reinterpret_cast<const uint2 *>(held + (i0 + i) * step * 8);
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i)
+                if ((i0 + i) * kPass + r0 < slot0)
+                    *reinterpret_cast<uint2 *>(held + (i0 + i) * step * 8) = make_uint2(rescale4(u[i].x, f), rescale4(u[i].y, f));
         }
     }
     const float inv = 1.0f / now;  // exact: a power of two from 2^-100 to 2^120

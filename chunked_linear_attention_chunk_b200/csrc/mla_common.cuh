@@ -36,9 +36,9 @@ __device__ __forceinline__ int64_t cta_sum(int64_t x, int64_t *sh)
 // Work item x of the list that has count(0) items for sequence 0, then count(1) for sequence 1,
 // and so on: its sequence and its place among that sequence's items, or seq = -1 past the end.
 // `count` sees every sequence and sets `bad` for what is not to be used; the whole CTA learns of
-// it.  Up to 256 sequences every warp goes through the list by itself (a few hundred cycles, no
-// barrier); beyond that the CTA's threads share it.  All threads call; `sh` is 40 int64 of shared
-// memory.
+// it.  Up to 64 sequences one warp goes through the list, beyond that all threads share it (every
+// warp by itself would cost the CTA more than the barriers do).  Any 32 counts of usable offsets
+// add up to less than 2^31.  All threads call; `sh` is 40 int64 of shared memory.
 struct Item {
     int seq, k;
     bool bad;
@@ -48,51 +48,54 @@ __device__ __forceinline__ Item find_item(int N, int64_t x, Count count, int64_t
 {
     static_assert(kThreads % 32 == 0 && kThreads <= 1024, "whole warps");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto scan = [&](int64_t c) {  // inclusive sum over the lanes
+    auto scan = [&](int c) {  // inclusive sum over the lanes
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
+            const int y = __shfl_up_sync(0xffffffffu, c, d);
             c += lane >= d ? y : 0;
         }
         return c;
     };
     bool bad = false;
     int64_t base = 0;
-    Item it{-1, 0, false};
-    if (N <= 256) {
-        for (int s0 = 0; s0 < N; s0 += 32) {
-            const int64_t c = s0 + lane < N ? count(s0 + lane, bad) : 0, inc = scan(c), rel = x - base - (inc - c);
-            const uint32_t hit = __ballot_sync(0xffffffffu, rel >= 0 && rel < c);
-            if (hit) {
-                it.seq = s0 + __ffs(hit) - 1;
-                it.k = (int)__shfl_sync(0xffffffffu, rel, __ffs(hit) - 1);
-            }
-            base += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        it.bad = __any_sync(0xffffffffu, bad);
-        return it;
-    }
     if (tid == 0)
         sh[33] = -1;
-    for (int s0 = 0; s0 < N; s0 += kThreads) {
-        const int s = s0 + tid;
-        const int64_t c = s < N ? count(s, bad) : 0, inc = scan(c);
-        if (lane == 31)
-            sh[warp] = inc;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            before += w < warp ? sh[w] : 0;
-            total += sh[w];
+    __syncwarp();
+    if (N <= 64) {
+        if (warp == 0) {
+            for (int s0 = 0; s0 < N; s0 += 32) {
+                const int c = s0 + lane < N ? count(s0 + lane, bad) : 0, inc = scan(c);
+                const int64_t rel = x - base - (inc - c);
+                if (rel >= 0 && rel < c) {
+                    sh[33] = s0 + lane;
+                    sh[34] = rel;
+                }
+                base += __shfl_sync(0xffffffffu, inc, 31);
+                __syncwarp();
+            }
         }
-        const int64_t rel = x - base - before - (inc - c);
-        if (rel >= 0 && rel < c) {
-            sh[33] = s;
-            sh[34] = rel;
+    } else {
+        for (int s0 = 0; s0 < N; s0 += kThreads) {
+            const int s = s0 + tid, c = s < N ? count(s, bad) : 0, inc = scan(c);
+            if (lane == 31)
+                sh[warp] = inc;
+            __syncthreads();
+            int64_t before = 0, total = 0;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                before += w < warp ? sh[w] : 0;
+                total += sh[w];
+            }
+            const int64_t rel = x - base - before - (inc - c);
+            if (rel >= 0 && rel < c) {
+                sh[33] = s;
+                sh[34] = rel;
+            }
+            base += total;
+            if (s0 + kThreads < N)
+                __syncthreads();
         }
-        base += total;
-        __syncthreads();
     }
+    Item it;
     it.bad = __syncthreads_or(bad) != 0;
     it.seq = (int)sh[33];
     it.k = (int)sh[34];
