@@ -112,16 +112,17 @@ struct DecSmem {
     // bfloat16: half tiles and rope blocks in flight.  e4m3: tiles of codes in flight, pairs of
     // blocks of bfloat16 rows held.
     static constexpr int kRing = kE4M3 ? 4 : (NC == 64 ? 4 : 5);
-    static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 3;
+    static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 2;
     static constexpr int kStage = kE4M3 ? (NC == 64 ? 2 : 3) : 1;
     static constexpr uint32_t kSlot = (kE4M3 ? 2 : 4) * kBlk;
     static constexpr uint32_t kCodes = 4 * kBlk + kBlk / 2;  // a tile of codes: 4 x 128, then 64
     static constexpr int kSW = kE4M3 ? 2 * NC : NC;          // columns of S^T
+    static constexpr int kPB = NC == 64 ? 1 : 2;             // buffers of P^T (one where a second has no room)
     alignas(1024) unsigned char ring[kRing][kSlot];
     alignas(1024) unsigned char rope[kRopes][kE4M3 ? 16 : kBlk];
     // bfloat16: [9 blocks][NC rows][128 B]; e4m3: [4 blocks][2 NC rows][128 B], [2 NC rows][64 B]
     alignas(1024) unsigned char q[kE4M3 ? 2 * NC * kDC : NC * kDC * 2];
-    alignas(1024) unsigned char p[kTok * NC * 2];
+    alignas(1024) unsigned char p[kPB][kTok * NC * 2];
     alignas(1024) unsigned char stage[kStage][kE4M3 ? kCodes : 16];
     alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
     float fac[NC], top[NC];  // per column: rescaling factor, then 1 / sum; maximum
@@ -129,7 +130,7 @@ struct DecSmem {
     float q_scale[kE4M3 ? 4 : 1][NC];  // by piece: Q's row scales t
     uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
     uint64_t full_stage[kStage], empty_stage[kStage];
-    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, q_empty;
+    uint64_t s_full[2], s_empty[2], p_full[kPB], pv_done[kPB], q_full, q_empty;
     uint32_t tmem_slot;
     int64_t find[40];
     int64_t share[2];  // first tile and tiles of the CTA's share
@@ -186,8 +187,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
         }
-        mbar_init(&sm.p_full, 4);
-        mbar_init(&sm.pv_done, 1);
+        for (int i = 0; i < SM::kPB; ++i) {
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+        }
         mbar_init(&sm.q_full, kE4M3 ? kConv : 1);
         mbar_init(&sm.q_empty, 1);
         fence_mbar_init_cluster();
@@ -396,12 +399,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         // ---------------- O^T += C^T P^T, 128 latent numbers at a time
         constexpr uint32_t id = tc::idesc_bf16(128, NC, true, true);
         constexpr int kPerSlot = SM::kSlot / (2 * kBlk);
-        const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p));
+        const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p[0]));
         Ring<SM::kRing> rp;
-        uint32_t nt = 0;
+        Ring<SM::kPB> rb;
         for (; w.take > 0 && !wait.dead; w.next(a))
-            for (int t = 0; t < w.take && !wait.dead; ++t, ++nt) {
-                wait(&sm.p_full, nt & 1);
+            for (int t = 0; t < w.take && !wait.dead; ++t, rb.step()) {
+                wait(&sm.p_full[rb.slot], rb.round & 1);
                 tc::fence_after_sync();
 #pragma unroll
                 for (int j = 0; j < kPairs / kPerSlot; ++j, rp.step()) {
@@ -414,11 +417,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
                         for (int k = 0; k < kPerSlot * 4; ++k)
                             tc::mma_bf16(tmem + kColO + (j * kPerSlot + (k >> 2)) * NC,
-                                         cd.at(c0 + (k >> 2) * 2 * kBlk + (k & 3) * 2048), pd.at((k & 3) * kPStep<NC>), id,
+                                         cd.at(c0 + (k >> 2) * 2 * kBlk + (k & 3) * 2048), pd.at(rb.slot * kTok * NC * 2 + (k & 3) * kPStep<NC>), id,
                                          t > 0 || (k & 3) > 0 ? 1u : 0u);
                         tc::commit(&sm.empty[rp.slot]);
                         if (j == kPairs / kPerSlot - 1)
-                            tc::commit(&sm.pv_done);
+                            tc::commit(&sm.pv_done[rb.slot]);
                     }
                 }
             }
@@ -560,8 +563,22 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)warp * 32, 0);
         uint32_t nt = 0, nq = 0;
         Ring<SM::kRing> rp;
+        // P^T and O^T of tile n: which buffer and round
+        auto pv_wait = [&](uint32_t n) { wait(&sm.pv_done[n % SM::kPB], n / SM::kPB & 1); };
         for (; w.take > 0; w.next(a), ++nq) {
             const int len = a.kv_lens[w.n];
+            // e4m3: the scale of this warp's 16 rows of a tile (they lie in one page), which takes two
+            // loads: the page is asked for two tiles ahead, its scale one
+            auto page_of = [&](int t) {
+                const int p0 = t * kTok + warp * 16;
+                return kE4M3 && p0 < len ? a.block_table[(int64_t)w.n * a.max_pages + p0 / a.page_size] : -1;
+            };
+            auto scale_of = [&](int page) {
+                return kE4M3 && page >= 0 && page < a.num_pages ? a.cache_scale[(int64_t)page * a.G + w.g] : 1.0f;
+            };
+            int page_next = page_of(w.t);
+            float scale_next = scale_of(page_next);
+            page_next = page_of(w.t + 1);
             float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1];
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
@@ -571,15 +588,9 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             }
             for (int t = w.t; t < w.t + w.take; ++t, ++nt) {
                 const uint32_t sb = nt & 1;
-                float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
-                if constexpr (kE4M3) {
-                    const int p0 = t * kTok + warp * 16;
-                    if (p0 < len) {
-                        const int page = a.block_table[(int64_t)w.n * a.max_pages + p0 / a.page_size];
-                        if (page >= 0 && page < a.num_pages)
-                            page_scale = a.cache_scale[(int64_t)page * a.G + w.g];
-                    }
-                }
+                const float page_scale = scale_next;
+                scale_next = scale_of(page_next);
+                page_next = page_of(t + 2);
                 wait(&sm.s_full[sb], (nt / 2) & 1);
                 tc::fence_after_sync();
                 float s[J][4];
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                     }
                     softmax_sync();
                     if (t > w.t) {
-                        wait(&sm.pv_done, (nt - 1) & 1);  // O^T of the tiles so far is complete
+                        pv_wait(nt - 1);  // O^T of the tiles so far is complete
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int b = 0; b < kPairs * NC / 16; ++b) {
@@ -661,14 +672,15 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         s[j][i] = ex2(s[j][i] - (mm == -INFINITY ? 0.0f : mm));
                         l[2 * j + (i & 1)] += s[j][i];
                     }
-                if (nt > 0)
-                    wait(&sm.pv_done, (nt - 1) & 1);  // P^T has been read
+                if (nt >= SM::kPB)
+                    pv_wait(nt - SM::kPB);  // this buffer of P^T has been read
+                unsigned char *pt = sm.p[nt % SM::kPB];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const int c = 8 * j + 2 * (lane & 3);
-                    *reinterpret_cast<uint32_t *>(sm.p + p_off<NC>(r0, c)) =
+                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0, c)) =
                         pack_bf16x2(s[j][0] * page_scale, s[j][1] * page_scale);
-                    *reinterpret_cast<uint32_t *>(sm.p + p_off<NC>(r0 + 8, c)) =
+                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0 + 8, c)) =
                         pack_bf16x2(s[j][2] * page_scale, s[j][3] * page_scale);
                 }
                 if constexpr (!kE4M3) {
@@ -691,7 +703,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sm.p_full);
+                    mbar_arrive(&sm.p_full[nt % SM::kPB]);
             }
             // ---- the piece's sums, and its result
 #pragma unroll
@@ -727,7 +739,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                     mt[1] = share;
             }
             softmax_sync();
-            wait(&sm.pv_done, (nt - 1) & 1);
+            pv_wait(nt - 1);
             tc::fence_after_sync();
             const int dim = warp * 32 + lane, live = cols - ct * NC;
 #pragma unroll 1
