@@ -17,8 +17,11 @@
 // the next four, which is all a bfloat16 has (numbers below 2^-15 of their row's largest keep an
 // absolute 2^-23 of it), so the two terms are further columns of the product (N = 2 NC, kind::f8f6f4,
 // half the instructions of bfloat16) and S^T stays as exact as float32 sums are.  Weights span too
-// many magnitudes to be split like that: for O^T the codes are turned into bfloat16 rows (exact) by
-// eight warps, while the tensor cores and the softmax work on S^T of the same tile.
+// many magnitudes to be split like that: for O^T the codes are turned into f16 rows (exact, one
+// instruction a pair, where bfloat16 takes four) by eight warps, while the tensor cores and the
+// softmax work on S^T of the same tile.  A weight times its page's scale is brought into f16's
+// range by a running maximum of its own for each column, over score + log2(scale): it is 2^7 to
+// 2^15 at the maximum, keeps 11 bits down to 2^-21 of it, and 2^-32 of it at worst.
 //
 // One persistent CTA per SM takes an equal share of all 64-row tiles of all (sequence, group)
 // units in order, so a batch of any lengths is balanced without the host knowing them.  A unit
@@ -30,7 +33,7 @@
 // tensor memory rescaled only when a column's maximum grows by more than 2^8, which float32 sums
 // and a bfloat16 weight hold exactly as well); 4 copies (TMA: half a tile of bfloat16 rows or a
 // whole one of codes at a time); 5 issues S^T; 6 issues O^T and frees the rows; 7 loads Q; 8-15
-// (e4m3) Q's terms and the bfloat16 rows.
+// (e4m3) Q's terms and the f16 rows.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -43,13 +46,14 @@ namespace {
 
 using namespace mla;
 
-constexpr int kConv = 8;  // warps that turn codes into bfloat16 rows
+constexpr int kConv = 8;  // warps that turn codes into f16 rows
 template <bool kE4M3>
 constexpr int kThreads = kE4M3 ? 256 + kConv * 32 : 256;
 constexpr int kTok = 64;                    // cached rows a tile
 constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kPairs = kDL / 128;           // 128 latent numbers: the M of one O^T product
 constexpr float kGrow = 8.0f;               // log2 by which a maximum may grow without rescaling
+constexpr float kLift = 7.0f;               // e4m3: log2 of a weight at its maximum
 
 struct DecArgs {
     int N, Sq, H, G, num_pages, page_size, max_pages, CT, shares;
@@ -61,14 +65,18 @@ struct DecArgs {
     float *lse;
     float *part_o, *part_lse;  // [CTA][2][4][NC / 4][128][4] (pair, column / 4, number, column % 4), [CTA][2][NC]
     int2 *meta;                // [unit][CT]: 2 * first share + (it starts inside that share), last share
+    // e4m3: q's terms [2][rows of q][576] and row scales
+    unsigned char *q_terms;
+    float *q_scale;
     unsigned int *status;
 };
 
 // bfloat16: the cache as [block of 64 numbers][pool row][group][64], so that one copy brings half a
 // tile (or the rope block) as the products read it; e4m3: [block of 128 codes][pool row][group]
-// [128], and the rope part.  q as [block][row][64].
+// [128], and the rope part.  q as [block][row][64], or its terms as [block][term][row][128] and
+// [term][row][64].
 struct DecMaps {
-    CUtensorMap latent, rope, q;
+    CUtensorMap latent, rope, q, q_rope;
     int rows;    // pool rows a copy: min(page_size, 64)
     int q_rows;  // rows of q a copy
 };
@@ -110,7 +118,7 @@ struct Pieces {
 template <int NC, bool kE4M3>
 struct DecSmem {
     // bfloat16: half tiles and rope blocks in flight.  e4m3: tiles of codes in flight, pairs of
-    // blocks of bfloat16 rows held.
+    // blocks of f16 rows held.
     static constexpr int kRing = kE4M3 ? 4 : (NC == 64 ? 4 : 5);
     static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 2;
     static constexpr int kStage = kE4M3 ? (NC == 64 ? 2 : 3) : 1;
@@ -125,9 +133,9 @@ struct DecSmem {
     alignas(1024) unsigned char p[kPB][kTok * NC * 2];
     alignas(1024) unsigned char stage[kStage][kE4M3 ? kCodes : 16];
     alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
-    float fac[NC], top[NC];  // per column: rescaling factor, then 1 / sum; maximum
+    float red_o[kE4M3 ? 4 : 1][NC];  // e4m3: maxima with the pages' scales
+    float fac[NC], top[NC], top_o[NC];  // per column: rescaling factor, then 1 / sum; the maxima
     int row[NC];            // output row of a column, less the sequence's and group's first
-    float q_scale[kE4M3 ? 4 : 1][NC];  // by piece: Q's row scales t
     uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
     uint64_t full_stage[kStage], empty_stage[kStage];
     uint64_t s_full[2], s_empty[2], p_full[kPB], pv_done[kPB], q_full, q_empty;
@@ -137,13 +145,12 @@ struct DecSmem {
     int first[4];      // n, g, t of its first tile; whether that is the unit's first
 };
 
-// Four e4m3 codes as bfloat16 pairs: exact, NaN codes stay NaN.
+// Four e4m3 codes as f16 pairs: exact, NaN codes stay NaN.
 __device__ __forceinline__ uint2 decode4(uint32_t w)
 {
     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
-    return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
+    return make_uint2((uint32_t)a.x | ((uint32_t)a.y << 16), (uint32_t)b.x | ((uint32_t)b.y << 16));
 }
 
 // Two numbers as e4m3 codes of their first (lo 16 bits) and second term.
@@ -154,6 +161,50 @@ __device__ __forceinline__ uint32_t terms2(float2 x)
     const __nv_fp8x2_storage_t b =
         __nv_cvt_float2_to_fp8x2(make_float2((x.x - f.x) * 16.0f, (x.y - f.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
     return (uint32_t)a | ((uint32_t)b << 16);
+}
+
+// q's two terms, a warp a row: t = 2^e with max|q| < 256 t, and t and 1 / t normal numbers; a row
+// with an infinity or a NaN gets a NaN for its scale.
+__global__ void __launch_bounds__(256) mla_split_q_kernel(DecArgs a, int64_t rows)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows)
+        return;
+    uint4 x[3];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int v = lane + 32 * i;
+        x[i] = v < kDC / 8 ? reinterpret_cast<const uint4 *>(a.q + r * kDC)[v] : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mx = max(mx, max(u[k] << 16 & 0x7fffffffu, u[k] & 0x7fff0000u));
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    const int e = max((int)(mx >> 23) - 127 - 7, -100);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (lane == 0)
+        a.q_scale[r] = __uint_as_float(mx >= 0x7f800000u ? 0x7fc00000u : (uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int v = lane + 32 * i;
+        if (v >= kDC / 8)
+            break;
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack_bf16x2(u[k]);
+            t[k] = terms2(make_float2(f.x * inv, f.y * inv));
+        }
+        *reinterpret_cast<uint2 *>(a.q_terms + r * kDC + v * 8) =
+            make_uint2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[2], t[3], 0x5410));
+        *reinterpret_cast<uint2 *>(a.q_terms + (rows + r) * kDC + v * 8) =
+            make_uint2(__byte_perm(t[0], t[1], 0x7632), __byte_perm(t[2], t[3], 0x7632));
+    }
 }
 
 template <int NC, bool kE4M3>
@@ -191,7 +242,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
         }
-        mbar_init(&sm.q_full, kE4M3 ? kConv : 1);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
         fence_mbar_init_cluster();
     }
@@ -242,7 +293,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         w.settle(a);
     Waits wait{a.status, false};
 
+    // e4m3: 512 threads start with 128 registers each; the softmax warps need more, the others less
+    // (208 + 64 + 2 x 96 for a thread of each warpgroup: below the 512 of the launch)
     if (warp == 4) {
+        if (kE4M3)
+            regs_dec<64>();
         // ---------------- copies
         const int ppt = kTok / maps.rows;  // copies a block
         int batch_n = -1, batch_0 = 0, ids = 0;
@@ -331,6 +386,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             }
         }
     } else if (warp == 5) {
+        if (kE4M3)
+            regs_dec<64>();
         // ---------------- S^T = C Q^T
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
@@ -396,8 +453,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 tc::commit(&sm.q_empty);
         }
     } else if (warp == 6) {
+        if (kE4M3)
+            regs_dec<64>();
         // ---------------- O^T += C^T P^T, 128 latent numbers at a time
-        constexpr uint32_t id = tc::idesc_bf16(128, NC, true, true);
+        constexpr uint32_t id = kE4M3 ? tc::idesc_f16(128, NC, true, true) : tc::idesc_bf16(128, NC, true, true);
         constexpr int kPerSlot = SM::kSlot / (2 * kBlk);
         const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p[0]));
         Ring<SM::kRing> rp;
@@ -426,99 +485,77 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 }
             }
     } else if (warp == 7) {
-        // ---------------- bfloat16 Q of each piece: NC columns (token, head) x 576, K-major blocks
-        // of 64.  Columns behind the last hold other rows of q or nothing; they stay columns of
-        // their own.
-        if constexpr (!kE4M3) {
-            uint32_t nq = 0;
-            for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
-                if (nq > 0)
-                    wait(&sm.q_empty, (nq - 1) & 1);
-                if (wait.dead)
-                    break;
-                if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
-                    if (elect()) {
-                        mbar_arrive_expect_tx(&sm.q_full, kDC / 64 * NC * 128);
-                        tma_load_3d(sm.q, &maps.q, 0, w.n * cols + ct * NC, 0, &sm.q_full);
-                    }
-                } else {
-                    const int n = (min(cols - ct * NC, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
-                    if (elect())
-                        mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n * maps.q_rows) * kDC * 2);
-                    __syncwarp();
-                    for (int i = lane; i < n * (kDC / 64); i += 32) {
-                        const int c = i / (kDC / 64) * maps.q_rows, blk = i % (kDC / 64);
-                        const int r = w.n * a.Sq * a.H + w.g * Hg + sm.row[c];
-                        tma_load_3d(sm.q + blk * NC * 128 + c * 128, &maps.q, 0, r, blk, &sm.q_full);
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-    } else if (kE4M3 && warp >= 8) {
-        const int cw = warp - 8;
-        Ring<SM::kRing> rp;
-        Ring<SM::kStage> rst;
+        if (kE4M3)
+            regs_dec<64>();
+        // ---------------- Q of each piece: NC columns (token, head) x 576, K-major; e4m3: its terms, the
+        // second behind the first.  Columns behind the last hold other rows of q or nothing; they
+        // stay columns of their own.
+        if constexpr (kE4M3)
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that writes the terms
+        constexpr uint32_t kBytes = kE4M3 ? 2 * kDC : kDC * 2;  // of a column
         uint32_t nq = 0;
         for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
-            // ---------------- Q's two terms: a warp takes a column at a time
             if (nq > 0)
                 wait(&sm.q_empty, (nq - 1) & 1);
             if (wait.dead)
                 break;
-            const __nv_bfloat16 *q0 = a.q + ((int64_t)w.n * a.Sq * a.H + w.g * Hg) * kDC;
-#pragma unroll 2
-            for (int c = cw; c < NC; c += kConv) {
-                uint4 x[3];
-                uint32_t mx = 0;
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int v = lane + 32 * i;
-                    x[i] = ct * NC + c < cols && v < kDC / 8
-                               ? reinterpret_cast<const uint4 *>(q0 + (int64_t)sm.row[c] * kDC)[v]
-                               : make_uint4(0, 0, 0, 0);
-                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx = max(mx, max(u[k] << 16 & 0x7fffffffu, u[k] & 0x7fff0000u));
-                }
-                // t = 2^e with max|q| < 256 t, and t, 1 / t normal numbers; a row with an infinity or a
-                // NaN gets a NaN for its scale
-                mx = __reduce_max_sync(0xffffffffu, mx);
-                const int e = max((int)(mx >> 23) - 127 - 7, -100);
-                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                if (lane == 0)
-                    sm.q_scale[nq & 3][c] = mx >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                              : __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int v = lane + 32 * i;
-                    if (v >= kDC / 8)
-                        break;
-                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    uint32_t r[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = unpack_bf16x2(u[k]);
-                        r[k] = terms2(make_float2(f.x * inv, f.y * inv));
-                    }
-                    const uint2 t1 = make_uint2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410));
-                    const uint2 t2 = make_uint2(__byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int r = k * NC + c, vr = v - 64;
-                        unsigned char *dst =
-                            i < 2 ? sm.q + (v >> 4) * SM::kSW * 128 + r * 128 + ((((v & 15) >> 1) ^ (r & 7)) << 4) + (v & 1) * 8
-                                  : sm.q + 4 * SM::kSW * 128 + r * 64 + (((vr >> 1) ^ ((r >> 1) & 3)) << 4) + (vr & 1) * 8;
-                        *reinterpret_cast<uint2 *>(dst) = k ? t2 : t1;
+            if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
+                if (elect()) {
+                    const int r = w.n * cols + ct * NC;
+                    mbar_arrive_expect_tx(&sm.q_full, NC * kBytes);
+                    if constexpr (kE4M3) {
+                        tma_load_4d(sm.q, &maps.q, 0, r, 0, 0, &sm.q_full);
+                        tma_load_3d(sm.q + 4 * SM::kSW * 128, &maps.q_rope, 0, r, 0, &sm.q_full);
+                    } else {
+                        tma_load_3d(sm.q, &maps.q, 0, r, 0, &sm.q_full);
                     }
                 }
+            } else {
+                const int n = (min(cols - ct * NC, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
+                const int row0 = w.n * a.Sq * a.H + w.g * Hg;
+                // a copy's destination is a multiple of 128 bytes: single rope rows of codes (64 bytes)
+                // are moved by the lanes instead
+                const bool by_hand = kE4M3 && maps.q_rows == 1;
+                if (by_hand) {
+                    for (int i = lane; i < 2 * n; i += 32) {
+                        const int c = i >> 1, k = i & 1, r = k * NC + c;
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            a.q_terms + ((int64_t)k * a.N * a.Sq * a.H + row0 + sm.row[c]) * kDC + kDL);
+                        unsigned char *dst = sm.q + 4 * SM::kSW * 128 + r * 64;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<uint4 *>(dst + ((v ^ ((r >> 1) & 3)) << 4)) = src[v];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const int copies = kE4M3 ? (by_hand ? 8 : 10) : kDC / 64;
+                if (elect())
+                    mbar_arrive_expect_tx(&sm.q_full,
+                                          (uint32_t)(n * maps.q_rows) * (by_hand ? kBytes - 2 * kDR : kBytes));
+                __syncwarp();
+                for (int i = lane; i < n * copies; i += 32) {
+                    const int c = i / copies * maps.q_rows, blk = i % copies;
+                    const int r = row0 + sm.row[c];
+                    if (!kE4M3)
+                        tma_load_3d(sm.q + blk * NC * 128 + c * 128, &maps.q, 0, r, blk, &sm.q_full);
+                    else if (blk < 8)
+                        tma_load_4d(sm.q + (blk >> 1) * SM::kSW * 128 + ((blk & 1) * NC + c) * 128, &maps.q, 0, r, blk & 1,
+                                    blk >> 1, &sm.q_full);
+                    else
+                        tma_load_3d(sm.q + 4 * SM::kSW * 128 + ((blk & 1) * NC + c) * 64, &maps.q_rope, 0, r, blk & 1,
+                                    &sm.q_full);
+                }
+                __syncwarp();
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.q_full);
-            // ---------------- codes to bfloat16 rows: 8 rows x 4 vectors of 16 codes at a time, so
+        }
+    } else if (kE4M3 && warp >= 8) {
+        regs_dec<96>();
+        const int cw = warp - 8;
+        Ring<SM::kRing> rp;
+        Ring<SM::kStage> rst;
+        for (; w.take > 0 && !wait.dead; w.next(a)) {
+            // ---------------- codes to f16 rows: 8 rows x 4 vectors of 16 codes at a time, so
             // that both the swizzled reads and the swizzled writes touch every bank once
             static_assert(kConv * 8 == kTok, "one pass of the warps covers a block's rows");
             const int len = a.kv_lens[w.n], row = cw * 8 + (lane & 7);
@@ -558,6 +595,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
     } else {
         // ---------------- softmax: rows 16 warp + lane / 4 (+ 8), columns 8 j + 2 (lane % 4) (+ 1)
+        if (kE4M3)
+            regs_inc<208>();
+        if (kE4M3)  // q's row scales
+            asm volatile("griddepcontrol.wait;" ::: "memory");
         constexpr int J = NC / 8;
         const int r0 = warp * 16 + (lane >> 2);
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)warp * 32, 0);
@@ -579,30 +620,33 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             int page_next = page_of(w.t);
             float scale_next = scale_of(page_next);
             page_next = page_of(w.t + 1);
-            float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1];
+            float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1], mo[kE4M3 ? 2 * J : 1], base[kE4M3 ? 2 * J : 1];
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 // columns behind the last: weights 0, and no say in when to rescale
                 m[i] = ct * NC + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1) < cols ? -INFINITY : INFINITY;
                 l[i] = 0.0f;
+                if (kE4M3) {
+                    const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                    mo[i] = m[i];
+                    base[i] = 0.0f;
+                    qs[i] = ct * NC + c < cols
+                                ? a.q_scale[(int64_t)w.n * a.Sq * a.H + w.g * Hg + sm.row[c]] * a.scale_log2 : 0.0f;
+                }
             }
             for (int t = w.t; t < w.t + w.take; ++t, ++nt) {
                 const uint32_t sb = nt & 1;
                 const float page_scale = scale_next;
                 scale_next = scale_of(page_next);
                 page_next = page_of(t + 2);
+                const float lg = kE4M3 ? log2f(page_scale) : 0.0f;
                 wait(&sm.s_full[sb], (nt / 2) & 1);
                 tc::fence_after_sync();
                 float s[J][4];
-                if constexpr (kE4M3) {
-                    if (t == w.t)
-#pragma unroll
-                        for (int i = 0; i < 2 * J; ++i)
-                            qs[i] = sm.q_scale[nq & 3][8 * (i >> 1) + 2 * (lane & 3) + (i & 1)] * a.scale_log2;
+                if constexpr (kE4M3)
                     load_s2<NC>(lane_base + sb * SM::kSW, s);
-                } else {
+                else
                     load_s<NC>(lane_base + sb * SM::kSW, s);
-                }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
@@ -612,16 +656,21 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
                 for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = s[j][i] * (kE4M3 ? qs[2 * j + (i & 1)] * page_scale : a.scale_log2);
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = 2 * j + i;
+                        const float f = kE4M3 ? qs[k] * page_scale : a.scale_log2;
+                        s[j][i] *= f;
+                        s[j][2 + i] *= f;
                         if (edge) {
-                            const int cg = ct * NC + 8 * j + 2 * (lane & 3) + (i & 1);
+                            const int cg = ct * NC + 8 * j + 2 * (lane & 3) + i;
                             const int last = len - a.Sq + (a.Sq == 1 ? 0 : min(cg / Hg, a.Sq - 1));
-                            if (t * kTok + r0 + (i >> 1) * 8 > last)
-                                x = -INFINITY;
+                            if (t * kTok + r0 > last)
+                                s[j][i] = -INFINITY;
+                            if (t * kTok + r0 + 8 > last)
+                                s[j][2 + i] = -INFINITY;
                         }
-                        s[j][i] = x;
-                        grow |= x > m[2 * j + (i & 1)] + kGrow;
+                        const float most = (kE4M3 ? fminf(m[k], mo[k] - lg) : m[k]) + kGrow;
+                        grow |= s[j][i] > most || s[j][2 + i] > most;
                     }
                 if (softmax_or(grow)) {
                     // new column maxima over the tile's 64 rows
@@ -632,8 +681,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if (lane < 4)
+                        if (lane < 4) {
                             sm.red[warp][8 * (i >> 1) + 2 * lane + (i & 1)] = x;
+                            if (kE4M3)
+                                sm.red_o[warp][8 * (i >> 1) + 2 * lane + (i & 1)] = x + lg;
+                        }
                     }
                     softmax_sync();
 #pragma unroll
@@ -644,6 +696,14 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         f[i] = m[i] == mn ? 1.0f : ex2(m[i] - mn);
                         m[i] = mn;
                         l[i] *= f[i];
+                        if (kE4M3) {
+                            const float on = fmaxf(
+                                fmaxf(fmaxf(sm.red_o[0][c], sm.red_o[1][c]), fmaxf(sm.red_o[2][c], sm.red_o[3][c])), mo[i]);
+                            f[i] = mo[i] == on ? 1.0f : ex2(mo[i] - on);
+                            mo[i] = on;
+                            // a weight's share of O^T is p scale base: in units of 2^(mo - m - kLift)
+                            base[i] = ex2((mn == -INFINITY ? 0.0f : mn) - (on == -INFINITY ? 0.0f : on) + kLift);
+                        }
                         if (warp == 0 && lane < 4)
                             sm.fac[c] = f[i];
                     }
@@ -678,10 +738,19 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     const int c = 8 * j + 2 * (lane & 3);
-                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0, c)) =
-                        pack_bf16x2(s[j][0] * page_scale, s[j][1] * page_scale);
-                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0 + 8, c)) =
-                        pack_bf16x2(s[j][2] * page_scale, s[j][3] * page_scale);
+                    uint32_t w0, w1;  // rows r0 and r0 + 8
+                    if constexpr (kE4M3) {
+                        const float g[2] = {page_scale * base[2 * j], page_scale * base[2 * j + 1]};
+                        const __half2 h0 = __floats2half2_rn(s[j][0] * g[0], s[j][1] * g[1]);
+                        const __half2 h1 = __floats2half2_rn(s[j][2] * g[0], s[j][3] * g[1]);
+                        w0 = *reinterpret_cast<const uint32_t *>(&h0);
+                        w1 = *reinterpret_cast<const uint32_t *>(&h1);
+                    } else {
+                        w0 = pack_bf16x2(s[j][0], s[j][1]);
+                        w1 = pack_bf16x2(s[j][2], s[j][3]);
+                    }
+                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0, c)) = w0;
+                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0 + 8, c)) = w1;
                 }
                 if constexpr (!kE4M3) {
                     // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
@@ -714,8 +783,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                     l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
                 if (lane < 4) {
                     sm.red[warp][c] = l[i];
-                    if (warp == 0)
+                    if (warp == 0) {
                         sm.top[c] = m[i];
+                        if (kE4M3)
+                            sm.top_o[c] = mo[i];
+                    }
                 }
             }
             softmax_sync();
@@ -725,7 +797,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             if (tid < NC) {
                 const float sum = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
                 const float lse2 = sum == 0.0f ? -INFINITY : sm.top[tid] + log2f(sum);
-                sm.fac[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float unit = kE4M3 ? ex2((sm.top_o[tid] == -INFINITY ? 0.0f : sm.top_o[tid]) - sm.top[tid] - kLift) : 1.0f;
+                sm.fac[tid] = sum == 0.0f ? 0.0f : unit / sum;
                 if (!whole)
                     a.part_lse[slot * NC + tid] = lse2;
                 else if (a.lse && ct * NC + tid < cols)
@@ -856,7 +929,7 @@ int columns(int Sq, int H, int G) { return Sq * (H / G) <= 32 ? 32 : 64; }
 
 struct DecPlan {
     int nc, ct, shares;
-    size_t part_lse, part_o, total;
+    size_t part_lse, part_o, q_scale, q_terms, total;
 };
 
 DecPlan plan(int N, int Sq, int H, int G)
@@ -868,7 +941,10 @@ DecPlan plan(int N, int Sq, int H, int G)
     const size_t slots = (size_t)p.shares * p.ct * 2;
     p.part_lse = ((size_t)N * G * p.ct * sizeof(int2) + 255) / 256 * 256;
     p.part_o = p.part_lse + (slots * p.nc * 4 + 255) / 256 * 256;
-    p.total = p.part_o + slots * p.nc * kDL * 4;
+    const size_t rows = (size_t)N * Sq * H;
+    p.q_scale = p.part_o + slots * p.nc * kDL * 4;
+    p.q_terms = p.q_scale + (rows * 4 + 255) / 256 * 256;
+    p.total = p.q_terms + 2 * rows * kDC;
     return p;
 }
 
@@ -881,27 +957,44 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    if (!kE4M3) {
-        // q: runs of columns that are consecutive rows
-        const int Hg = a.H / a.G;
-        maps.q_rows = a.G == 1 ? NC : Hg % 8 == 0 ? 8 : 1;
-        const int64_t extent[3] = {64, (int64_t)a.N * a.Sq * a.H, kDC / 64}, stride[2] = {kDC * 2, 128};
-        const int box[3] = {64, maps.q_rows, maps.q_rows == NC ? kDC / 64 : 1};
-        if ((e = make_map(&maps.q, a.q, 2, 3, extent, stride, box)) != cudaSuccess)
-            return e;
-    }
-    kernel<<<a.shares * a.CT, kThreads<kE4M3>, smem, s>>>(maps, a);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    // the join waits on the device for the first launch to end, and is set up meanwhile
+    // q: runs of columns that are consecutive rows
+    const int Hg = a.H / a.G;
+    const int64_t rows = (int64_t)a.N * a.Sq * a.H;
+    maps.q_rows = a.G == 1 ? NC : Hg % 8 == 0 ? 8 : 1;
+    const bool all = maps.q_rows == NC;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(a.N * a.G * a.CT, NC / 4, kPairs);
-    cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = &attr;
+    if constexpr (kE4M3) {
+        const int64_t extent[4] = {128, rows, 2, 4}, stride[3] = {kDC, rows * kDC, 128};
+        const int box[4] = {128, maps.q_rows, all ? 2 : 1, all ? 4 : 1};
+        const int64_t rope[3] = {kDR, rows, 2};
+        const int rope_box[3] = {kDR, maps.q_rows, all ? 2 : 1};
+        if ((e = make_map(&maps.q, a.q_terms, 1, 4, extent, stride, box)) != cudaSuccess ||
+            (e = make_map(&maps.q_rope, a.q_terms + kDL, 1, 3, rope, stride, rope_box)) != cudaSuccess)
+            return e;
+        mla_split_q_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, rows);
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+        cfg.numAttrs = 1;  // set up while the terms are written
+    } else {
+        const int64_t extent[3] = {64, rows, kDC / 64}, stride[2] = {kDC * 2, 128};
+        const int box[3] = {64, maps.q_rows, all ? kDC / 64 : 1};
+        if ((e = make_map(&maps.q, a.q, 2, 3, extent, stride, box)) != cudaSuccess)
+            return e;
+    }
+    cfg.gridDim = dim3(a.shares * a.CT);
+    cfg.blockDim = dim3(kThreads<kE4M3>);
+    cfg.dynamicSmemBytes = smem;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, maps, a)) != cudaSuccess)
+        return e;
+    // the join waits on the device for the launch before it to end, and is set up meanwhile
+    cfg.gridDim = dim3(a.N * a.G * a.CT, NC / 4, kPairs);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC>, a);
 }
@@ -920,7 +1013,8 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
     DecArgs a{N, Sq, H, G, num_pages, page_size, max_pages, p.ct, p.shares, scale * kLog2e,
               static_cast<const __nv_bfloat16 *>(q), cache_scale, block_table, kv_lens,
               static_cast<__nv_bfloat16 *>(o), lse, reinterpret_cast<float *>(ws + p.part_o),
-              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int2 *>(ws), device_status_ptr()};
+              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int2 *>(ws), ws + p.q_terms, reinterpret_cast<float *>(ws + p.q_scale),
+              device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;
     DecMaps maps{};
