@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_slot;
-    Waits wait{a.status, false};
+    Waits wait{false};
 
     if (warp == kElemWarps) {
         // ---------------- copies of X and Y1
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    wait.report(a.status);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

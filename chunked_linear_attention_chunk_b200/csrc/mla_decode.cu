@@ -135,9 +135,10 @@ struct DecSmem {
     alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
     float red_o[kE4M3 ? 4 : 1][NC];  // e4m3: maxima with the pages' scales
     float fac[NC], top[NC], top_o[NC];  // per column: rescaling factor, then 1 / sum; the maxima
+    float scale[kE4M3 ? 8 : 1][4];  // by tile: its boxes' page scales
     int row[NC];            // output row of a column, less the sequence's and group's first
     uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
-    uint64_t full_stage[kStage], empty_stage[kStage];
+    uint64_t full_stage[kStage], empty_stage[kStage], full_scale[8];
     uint64_t s_full[2], s_empty[2], p_full[kPB], pv_done[kPB], q_full, q_empty;
     uint32_t tmem_slot;
     int64_t find[40];
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
     if (tid == 0) {
         for (int i = 0; i < SM::kRing; ++i) {
-            mbar_init(&sm.full[i], kE4M3 ? kConv : 1);
+            mbar_init(&sm.full[i], kE4M3 ? 2 : 1);
             mbar_init(&sm.empty[i], 1);
         }
         for (int i = 0; i < SM::kRopes; ++i) {
@@ -234,6 +235,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             mbar_init(&sm.full_stage[i], 1);
             mbar_init(&sm.empty_stage[i], 1 + kConv);
         }
+        for (int i = 0; i < 8; ++i)
+            mbar_init(&sm.full_scale[i], 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_empty[i], 4);
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     w.inside = false;
     if (w.left > 0)
         w.settle(a);
-    Waits wait{a.status, false};
+    Waits wait{false};
 
     // e4m3: 512 threads start with 128 registers each; the softmax warps need more, the others less
     // (208 + 64 + 2 x 96 for a thread of each warpgroup: below the 512 of the launch)
@@ -301,6 +304,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         // ---------------- copies
         const int ppt = kTok / maps.rows;  // copies a block
         int batch_n = -1, batch_0 = 0, ids = 0;
+        uint32_t nt = 0;
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
         Ring<SM::kStage> rst;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             int e = w.t * kTok / a.page_size, off = w.t * kTok % a.page_size;  // page entry, slot in it
             for (int t = w.t; t < w.t + w.take && !wait.dead; ++t) {
                 // the pool rows of the tile's copies, from the table 32 entries at a time
-                int at[4], live = 0;
+                int at[4], live = 0, my_page = -1;  // my_page: of box `lane`
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     at[b] = -1;
@@ -324,6 +328,8 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         if (page >= 0 && page < a.num_pages) {
                             at[b] = page * a.page_size + off;
                             ++live;
+                            if (lane == b)
+                                my_page = page;
                         } else if (lane == 0) {
                             report_device_error(a.status, KDA_ERR_INVALID_ARG);
                         }
@@ -363,6 +369,18 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         rope(sm.stage[rst.slot] + 4 * kBlk, 64, &sm.full_stage[rst.slot]);
                         half(sm.stage[rst.slot], 0, &sm.full_stage[rst.slot]);
                     }
+                    // the page scales come on their own; the softmax is never eight tiles behind (S^T of a
+                    // tile waits for it to read the one two before, and three tiles are in flight)
+                    if (!wait.dead && lane < 4) {
+                        float *dst = &sm.scale[nt & 7][lane];
+                        if (my_page >= 0)
+                            cp_async_4(dst, a.cache_scale + (int64_t)my_page * a.G + w.g);
+                        else
+                            *dst = 1.0f;
+                        cp_async_arrive(&sm.full_scale[nt & 7]);
+                    }
+                    __syncwarp();
+                    ++nt;
                     rst.step();
                 } else {
                     if (rr.round > 0)
@@ -551,45 +569,41 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
     } else if (kE4M3 && warp >= 8) {
         regs_dec<96>();
-        const int cw = warp - 8;
-        Ring<SM::kRing> rp;
+        // ---------------- codes to f16 rows: two warps a pair of blocks (32 rows each), 8 rows x 4
+        // vectors of 16 codes at a time, so that both the swizzled reads and the swizzled writes touch
+        // every bank once
+        static_assert(!kE4M3 || (kConv == 2 * kPairs && SM::kRing == kPairs), "a pair keeps its warps and its place");
+        const int j = (warp - 8) >> 1, row0 = ((warp - 8) & 1) * 32 + (lane & 7), chunk = lane >> 3;
         Ring<SM::kStage> rst;
+        uint32_t nt = 0;
         for (; w.take > 0 && !wait.dead; w.next(a)) {
-            // ---------------- codes to f16 rows: 8 rows x 4 vectors of 16 codes at a time, so
-            // that both the swizzled reads and the swizzled writes touch every bank once
-            static_assert(kConv * 8 == kTok, "one pass of the warps covers a block's rows");
-            const int len = a.kv_lens[w.n], row = cw * 8 + (lane & 7);
-            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t, rst.step()) {
-                const bool live = row < len - t * kTok;  // behind the sequence's end: anything may be there
+            const int len = a.kv_lens[w.n];
+            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t, ++nt, rst.step()) {
                 wait(&sm.full_stage[rst.slot], rst.round & 1);
+                const unsigned char *src = sm.stage[rst.slot] + j * kBlk;
+                uint4 c[8];
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j, rp.step()) {
-                    if (rp.round > 0)
-                        wait(&sm.empty[rp.slot], (rp.round - 1) & 1);
-                    uint4 c[2];
+                for (int i = 0; i < 8; ++i) {
+                    const int row = row0 + (i >> 1) * 8, ch = (i & 1) * 4 + chunk;
+                    c[i] = *reinterpret_cast<const uint4 *>(src + row * 128 + ((ch ^ (row & 7)) << 4));
+                    if (row >= len - t * kTok)  // behind the sequence's end: anything may be there
+                        c[i] = make_uint4(0, 0, 0, 0);
+                }
+                if (nt > 0)
+                    wait(&sm.empty[j], (nt - 1) & 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int chunk = i * 4 + (lane >> 3);
-                        c[i] = *reinterpret_cast<const uint4 *>(sm.stage[rst.slot] + j * kBlk + row * 128 +
-                                                                ((chunk ^ (row & 7)) << 4));
-                        if (!live)
-                            c[i] = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int chunk = lane >> 3;
-                        const uint2 x = decode4(c[i].x), y = decode4(c[i].y), z = decode4(c[i].z), u = decode4(c[i].w);
-                        unsigned char *p = sm.ring[rp.slot] + i * kBlk + row * 128;
-                        *reinterpret_cast<uint4 *>(p + (((2 * chunk) ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-                        *reinterpret_cast<uint4 *>(p + (((2 * chunk + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, u.x, u.y);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&sm.full[rp.slot]);
-                        if (j == kPairs - 1)
-                            mbar_arrive(&sm.empty_stage[rst.slot]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int row = row0 + (i >> 1) * 8;
+                    const uint2 x = decode4(c[i].x), y = decode4(c[i].y), z = decode4(c[i].z), u = decode4(c[i].w);
+                    unsigned char *p = sm.ring[j] + (i & 1) * kBlk + row * 128;
+                    *reinterpret_cast<uint4 *>(p + (((2 * chunk) ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
+                    *reinterpret_cast<uint4 *>(p + (((2 * chunk + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, u.x, u.y);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.full[j]);
+                    mbar_arrive(&sm.empty_stage[rst.slot]);
                 }
             }
         }
@@ -602,24 +616,12 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         constexpr int J = NC / 8;
         const int r0 = warp * 16 + (lane >> 2);
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)warp * 32, 0);
-        uint32_t nt = 0, nq = 0;
+        uint32_t nt = 0;
         Ring<SM::kRing> rp;
         // P^T and O^T of tile n: which buffer and round
         auto pv_wait = [&](uint32_t n) { wait(&sm.pv_done[n % SM::kPB], n / SM::kPB & 1); };
-        for (; w.take > 0; w.next(a), ++nq) {
+        for (; w.take > 0; w.next(a)) {
             const int len = a.kv_lens[w.n];
-            // e4m3: the scale of this warp's 16 rows of a tile (they lie in one page), which takes two
-            // loads: the page is asked for two tiles ahead, its scale one
-            auto page_of = [&](int t) {
-                const int p0 = t * kTok + warp * 16;
-                return kE4M3 && p0 < len ? a.block_table[(int64_t)w.n * a.max_pages + p0 / a.page_size] : -1;
-            };
-            auto scale_of = [&](int page) {
-                return kE4M3 && page >= 0 && page < a.num_pages ? a.cache_scale[(int64_t)page * a.G + w.g] : 1.0f;
-            };
-            int page_next = page_of(w.t);
-            float scale_next = scale_of(page_next);
-            page_next = page_of(w.t + 1);
             float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1], mo[kE4M3 ? 2 * J : 1], base[kE4M3 ? 2 * J : 1];
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
@@ -636,9 +638,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             }
             for (int t = w.t; t < w.t + w.take; ++t, ++nt) {
                 const uint32_t sb = nt & 1;
-                const float page_scale = scale_next;
-                scale_next = scale_of(page_next);
-                page_next = page_of(t + 2);
+                float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
+                if constexpr (kE4M3) {
+                    wait(&sm.full_scale[nt & 7], (nt >> 3) & 1);
+                    page_scale = sm.scale[nt & 7][warp * 16 / maps.rows];
+                }
                 const float lg = kE4M3 ? log2f(page_scale) : 0.0f;
                 wait(&sm.s_full[sb], (nt / 2) & 1);
                 tc::fence_after_sync();
@@ -850,6 +854,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             tc::fence_before_sync();
         }
     }
+    wait.report(a.status);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_slot;
-    Waits wait{a.status, false};
+    Waits wait{false};
 
     if (warp == 8) {
         // ---------------- copies
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.lse && row < lq)
             a.lse[r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    wait.report(a.status);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

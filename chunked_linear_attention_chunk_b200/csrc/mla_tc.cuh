@@ -9,15 +9,29 @@
 namespace kda {
 namespace mla {
 
-// Bounded waits of one role: after the first one that runs out (recorded in the status word) the
-// role waits no more, so a broken pipeline ends soon instead of at every barrier's limit.
+// Bounded waits of one role.  A try suspends the thread for some microseconds while the barrier is
+// not ready, so the limit is of the order of seconds.  After the first wait that runs out the role
+// waits no more, so a broken pipeline ends soon; `report` records it in the status word, once, at
+// the kernel's end (a few instructions a wait matter: the roles' loops share the instruction cache).
+constexpr uint32_t kWaitTries = 1u << 20;
 struct Waits {
-    unsigned int *status;
     bool dead;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity)
     {
-        if (!dead && !mbar_wait_bounded(bar, parity, status))
-            dead = true;
+        const uint32_t a = smem_u32(bar);
+        if (dead)
+            return;
+#pragma unroll 1
+        for (uint32_t n = 0; !mbar_try_wait(a, parity); ++n)
+            if (n == kWaitTries) {
+                dead = true;
+                break;
+            }
+    }
+    __device__ __forceinline__ void report(unsigned int *status) const
+    {
+        if (dead)
+            report_device_error(status, KDA_ERR_DEVICE_TIMEOUT);
     }
 };
 
@@ -70,6 +84,17 @@ struct Ring {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Four bytes global -> shared, and an arrival on `bar` (one of its count) once this thread's copies
+// so far have landed.
+__device__ __forceinline__ void cp_async_4(void *smem, const void *gmem)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // A barrier and a vote of the four softmax warps.

@@ -60,6 +60,8 @@ CASES = [
     ([3000, 10, 2500], 1, 16, 1, 192),         # sequences that several CTAs share
     ([260] * 40, 1, 16, 1, 64),
     ([70], 70, 3, 1, 64),                      # many new tokens
+    ([3000 + 37 * i for i in range(40)], 1, 32, 1, 64),  # many tiles a CTA, several pieces
+    ([2500 + 41 * i for i in range(30)], 2, 32, 1, 16),
 ]
 
 
