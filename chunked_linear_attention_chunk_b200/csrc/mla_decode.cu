@@ -12,16 +12,19 @@
 //   O^T [512 x NC] += C[:, 0:512]^T P^T         (M = 128 four times, K = 64; C read MN-major)
 // The same shared-memory tile is the A operand of both; only P^T (64 x NC) is written by threads.
 //
-// e4m3 rows: S^T is taken on the codes as they lie in the cache.  Q is split into two e4m3 terms
-// at a power-of-two scale of its own for each row, q = t (q1 + q2 / 16): q1 keeps four bits and q2
-// the next four, which is all a bfloat16 has (numbers below 2^-15 of their row's largest keep an
-// absolute 2^-23 of it), so the two terms are further columns of the product (N = 2 NC, kind::f8f6f4,
-// half the instructions of bfloat16) and S^T stays as exact as float32 sums are.  Weights span too
-// many magnitudes to be split like that: for O^T the codes are turned into f16 rows (exact, one
-// instruction a pair, where bfloat16 takes four) by eight warps, while the tensor cores and the
-// softmax work on S^T of the same tile.  A weight times its page's scale is brought into f16's
-// range by a running maximum of its own for each column, over score + log2(scale): it is 2^7 to
-// 2^15 at the maximum, keeps 11 bits down to 2^-21 of it, and 2^-32 of it at worst.
+// e4m3 rows: both products are taken on the codes as they lie in the cache (kind::f8f6f4), and
+// what is exact in bfloat16 becomes several 8-bit terms of the other operand.
+// Q is split into two e4m3 terms at a power-of-two scale of its own for each row, q = t (q1 + q2 /
+// 16): q1 keeps four bits and q2 the next four, which is all a bfloat16 has (numbers below 2^-15 of
+// their row's largest keep an absolute 2^-23 of it), so the terms are further columns of the
+// product and S^T stays as exact as float32 sums are.
+// A weight times its page's scale is brought into range by a running maximum of its own for each
+// column, over score + log2(scale) (2^7 to 2^15 at the maximum), and split into three e5m2 terms of
+// three bits each at one common scale: nine bits (a bfloat16 weight has eight) down to 2^-23 of the
+// maximum, and 2^-31 of it at worst.  At 32 columns the terms are 96 columns of one product, added
+// up at the end; at 64, where tensor memory has no room for that, three products into one sum.
+// Turning the codes into f16 rows in shared memory instead costs its bandwidth: 64 KB written and
+// read again a tile, 190 us where this takes 165 (256 sequences of 3000 to 5000 rows, 32 heads).
 //
 // One persistent CTA per SM takes an equal share of all 64-row tiles of all (sequence, group)
 // units in order, so a batch of any lengths is balanced without the host knowing them.  A unit
@@ -29,11 +32,11 @@
 // their log-sum-exp in the workspace, which a second launch joins in order (equal calls give
 // equal bits; the shares depend on the lengths and the SM count alone).
 //
-// Warps: 0-3 softmax (S^T in the 16-lane M = 64 layout, running maximum per column, O^T in
-// tensor memory rescaled only when a column's maximum grows by more than 2^8, which float32 sums
-// and a bfloat16 weight hold exactly as well); 4 copies (TMA: half a tile of bfloat16 rows or a
-// whole one of codes at a time); 5 issues S^T; 6 issues O^T and frees the rows; 7 loads Q; 8-15
-// (e4m3) Q's terms and the f16 rows.
+// Warps: 0-3 and 8-11 softmax, half the columns each (S^T in the 16-lane M = 64 layout, running
+// maximum per column, O^T in tensor memory rescaled only when a column's maximum grows by more than
+// 2^8, which float32 sums and a bfloat16 weight hold exactly as well); 4 copies (TMA: half a tile of
+// bfloat16 rows or a whole one of codes at a time); 5 issues S^T; 6 issues O^T and frees the rows;
+// 7 loads Q.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
@@ -46,9 +49,7 @@ namespace {
 
 using namespace mla;
 
-constexpr int kConv = 8;  // warps that turn codes into f16 rows
-template <bool kE4M3>
-constexpr int kThreads = kE4M3 ? 256 + kConv * 32 : 256;
+constexpr int kThreads = 384;
 constexpr int kTok = 64;                    // cached rows a tile
 constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kPairs = kDL / 128;           // 128 latent numbers: the M of one O^T product
@@ -117,42 +118,37 @@ struct Pieces {
 
 template <int NC, bool kE4M3>
 struct DecSmem {
-    // bfloat16: half tiles and rope blocks in flight.  e4m3: tiles of codes in flight, pairs of
-    // blocks of f16 rows held.
-    static constexpr int kRing = kE4M3 ? 4 : (NC == 64 ? 4 : 5);
+    // bfloat16: half tiles and rope blocks in flight; e4m3: tiles of codes
+    static constexpr int kRing = kE4M3 ? 1 : (NC == 64 ? 4 : 5);
     static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 2;
-    static constexpr int kStage = kE4M3 ? (NC == 64 ? 2 : 3) : 1;
-    static constexpr uint32_t kSlot = (kE4M3 ? 2 : 4) * kBlk;
+    static constexpr int kStage = kE4M3 ? (NC == 64 ? 3 : 4) : 1;
+    static constexpr uint32_t kSlot = kE4M3 ? 16 : 4 * kBlk;
     static constexpr uint32_t kCodes = 4 * kBlk + kBlk / 2;  // a tile of codes: 4 x 128, then 64
     static constexpr int kSW = kE4M3 ? 2 * NC : NC;          // columns of S^T
-    static constexpr int kPB = NC == 64 ? 1 : 2;             // buffers of P^T (one where a second has no room)
+    static constexpr int kPB = NC == 64 && !kE4M3 ? 1 : 2;   // buffers of P^T (one where a second has no room)
+    static constexpr uint32_t kP = kTok * NC * (kE4M3 ? 3 : 2);  // bytes of one
+    // parts of O^T: a weight's three terms side by side where tensor memory has the room, one sum of
+    // their three products where it has not
+    static constexpr int kParts = kE4M3 && NC == 32 ? 3 : 1;
     alignas(1024) unsigned char ring[kRing][kSlot];
     alignas(1024) unsigned char rope[kRopes][kE4M3 ? 16 : kBlk];
     // bfloat16: [9 blocks][NC rows][128 B]; e4m3: [4 blocks][2 NC rows][128 B], [2 NC rows][64 B]
     alignas(1024) unsigned char q[kE4M3 ? 2 * NC * kDC : NC * kDC * 2];
-    alignas(1024) unsigned char p[kPB][kTok * NC * 2];
+    alignas(1024) unsigned char p[kPB][kP];
     alignas(1024) unsigned char stage[kStage][kE4M3 ? kCodes : 16];
     alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
     float red_o[kE4M3 ? 4 : 1][NC];  // e4m3: maxima with the pages' scales
     float fac[NC], top[NC], top_o[NC];  // per column: rescaling factor, then 1 / sum; the maxima
-    float scale[kE4M3 ? 8 : 1][4];  // by tile: its boxes' page scales
+    float scale[kStage][4];  // of a tile's boxes: their pages' scales
     int row[NC];            // output row of a column, less the sequence's and group's first
     uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
-    uint64_t full_stage[kStage], empty_stage[kStage], full_scale[8];
+    uint64_t full_stage[kStage], empty_stage[kStage], full_scale[kStage];
     uint64_t s_full[2], s_empty[2], p_full[kPB], pv_done[kPB], q_full, q_empty;
     uint32_t tmem_slot;
     int64_t find[40];
     int64_t share[2];  // first tile and tiles of the CTA's share
     int first[4];      // n, g, t of its first tile; whether that is the unit's first
 };
-
-// Four e4m3 codes as f16 pairs: exact, NaN codes stay NaN.
-__device__ __forceinline__ uint2 decode4(uint32_t w)
-{
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    return make_uint2((uint32_t)a.x | ((uint32_t)a.y << 16), (uint32_t)b.x | ((uint32_t)b.y << 16));
-}
 
 // Two numbers as e4m3 codes of their first (lo 16 bits) and second term.
 __device__ __forceinline__ uint32_t terms2(float2 x)
@@ -209,22 +205,21 @@ __global__ void __launch_bounds__(256) mla_split_q_kernel(DecArgs a, int64_t row
 }
 
 template <int NC, bool kE4M3>
-__global__ void __launch_bounds__(kThreads<kE4M3>, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ DecMaps maps, DecArgs a)
 {
     extern __shared__ unsigned char raw[];
     using SM = DecSmem<NC, kE4M3>;
-    constexpr int kT = kThreads<kE4M3>;
     SM &sm = *reinterpret_cast<SM *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int share = blockIdx.x / a.CT, ct = blockIdx.x % a.CT, Hg = a.H / a.G, cols = a.Sq * Hg;
-    constexpr uint32_t kTmemCols = 2 * SM::kSW + 4 * NC <= 256 ? 256 : 512;
+    constexpr uint32_t kTmemCols = 2 * SM::kSW + kPairs * SM::kParts * NC <= 256 ? 256 : 512;
     constexpr uint32_t kColO = 2 * SM::kSW;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
     if (tid == 0) {
         for (int i = 0; i < SM::kRing; ++i) {
-            mbar_init(&sm.full[i], kE4M3 ? 2 : 1);
+            mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
         for (int i = 0; i < SM::kRopes; ++i) {
@@ -233,16 +228,15 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
         for (int i = 0; i < SM::kStage; ++i) {
             mbar_init(&sm.full_stage[i], 1);
-            mbar_init(&sm.empty_stage[i], 1 + kConv);
-        }
-        for (int i = 0; i < 8; ++i)
+            mbar_init(&sm.empty_stage[i], 1);
             mbar_init(&sm.full_scale[i], 4);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_empty[i], 4);
+            mbar_init(&sm.s_empty[i], 8);
         }
         for (int i = 0; i < SM::kPB; ++i) {
-            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.p_full[i], 8);
             mbar_init(&sm.pv_done[i], 1);
         }
         mbar_init(&sm.q_full, 1);
@@ -259,7 +253,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
     {
         int64_t mine = 0;
         bool bad = false;
-        for (int n = tid; n < a.N; n += kT) {
+        for (int n = tid; n < a.N; n += kThreads) {
             const int t = tiles_of(a, n);
             mine += t;
             bad |= t == 0 && a.kv_lens[n] != 0;
@@ -269,11 +263,11 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         }
         if (bad)
             report_device_error(a.status, KDA_ERR_INVALID_ARG);
-        const int64_t total = cta_sum<kT>(mine, sm.find) * a.G;
+        const int64_t total = cta_sum<kThreads>(mine, sm.find) * a.G;
         const int64_t per = total < 0x7fffffff - a.shares ? (uint32_t)(total + a.shares - 1) / (uint32_t)a.shares
                                                           : (total + a.shares - 1) / a.shares;
         const int64_t begin = min(total, share * per), end = min(total, begin + per);
-        const Item it = find_item<kT>(a.N, begin, [&](int n, bool &) { return tiles_of(a, n) * a.G; }, sm.find);
+        const Item it = find_item<kThreads>(a.N, begin, [&](int n, bool &) { return tiles_of(a, n) * a.G; }, sm.find);
         if (tid == 0) {
             const int tiles = begin < end ? tiles_of(a, it.seq) : 1;
             sm.share[0] = begin;
@@ -296,15 +290,10 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
         w.settle(a);
     Waits wait{false};
 
-    // e4m3: 512 threads start with 128 registers each; the softmax warps need more, the others less
-    // (208 + 64 + 2 x 96 for a thread of each warpgroup: below the 512 of the launch)
     if (warp == 4) {
-        if (kE4M3)
-            regs_dec<64>();
         // ---------------- copies
         const int ppt = kTok / maps.rows;  // copies a block
         int batch_n = -1, batch_0 = 0, ids = 0;
-        uint32_t nt = 0;
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
         Ring<SM::kStage> rst;
@@ -369,18 +358,16 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         rope(sm.stage[rst.slot] + 4 * kBlk, 64, &sm.full_stage[rst.slot]);
                         half(sm.stage[rst.slot], 0, &sm.full_stage[rst.slot]);
                     }
-                    // the page scales come on their own; the softmax is never eight tiles behind (S^T of a
-                    // tile waits for it to read the one two before, and three tiles are in flight)
+                    // the page scales come on their own (a place is free once its tile's P^T has been used)
                     if (!wait.dead && lane < 4) {
-                        float *dst = &sm.scale[nt & 7][lane];
+                        float *dst = &sm.scale[rst.slot][lane];
                         if (my_page >= 0)
                             cp_async_4(dst, a.cache_scale + (int64_t)my_page * a.G + w.g);
                         else
                             *dst = 1.0f;
-                        cp_async_arrive(&sm.full_scale[nt & 7]);
+                        cp_async_arrive(&sm.full_scale[rst.slot]);
                     }
                     __syncwarp();
-                    ++nt;
                     rst.step();
                 } else {
                     if (rr.round > 0)
@@ -404,8 +391,6 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             }
         }
     } else if (warp == 5) {
-        if (kE4M3)
-            regs_dec<64>();
         // ---------------- S^T = C Q^T
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
@@ -433,7 +418,6 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
                         for (int ks = 0; ks < 2; ++ks)
                             tc::mma_f8(d, cr.at(c0 + 4 * kBlk + ks * 32), qr.at(4 * SM::kSW * 128 + ks * 32), id, 1u);
-                        tc::commit(&sm.empty_stage[rst.slot]);
                         tc::commit(&sm.s_full[rs.slot]);
                     }
                     rst.step();
@@ -471,40 +455,51 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 tc::commit(&sm.q_empty);
         }
     } else if (warp == 6) {
-        if (kE4M3)
-            regs_dec<64>();
         // ---------------- O^T += C^T P^T, 128 latent numbers at a time
-        constexpr uint32_t id = kE4M3 ? tc::idesc_f16(128, NC, true, true) : tc::idesc_bf16(128, NC, true, true);
-        constexpr int kPerSlot = SM::kSlot / (2 * kBlk);
-        const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128), pd = p_desc<NC>(smem_u32(sm.p[0]));
+        const Desc pd = p_desc<NC, kE4M3>(smem_u32(sm.p[0]));
         Ring<SM::kRing> rp;
+        Ring<SM::kStage> rst;
         Ring<SM::kPB> rb;
         for (; w.take > 0 && !wait.dead; w.next(a))
             for (int t = 0; t < w.take && !wait.dead; ++t, rb.step()) {
                 wait(&sm.p_full[rb.slot], rb.round & 1);
                 tc::fence_after_sync();
-#pragma unroll
-                for (int j = 0; j < kPairs / kPerSlot; ++j, rp.step()) {
-                    if (kE4M3) {
-                        wait(&sm.full[rp.slot], rp.round & 1);
-                        tc::fence_after_sync();
-                    }
+                const uint32_t p0 = rb.slot * SM::kP;
+                if constexpr (kE4M3) {
+                    constexpr uint32_t id = tc::idesc_e4m3_e5m2_mn(128, SM::kParts * NC);
+                    constexpr int kTurns = 3 / SM::kParts;  // products of a term each, or one of all
+                    const Desc cd(smem_u32(sm.stage[0]), kBlk, 1024, tc::kSw128);
                     if (elect()) {
-                        const uint32_t c0 = rp.slot * SM::kSlot;
+                        const uint32_t c0 = rst.slot * SM::kCodes;
 #pragma unroll
-                        for (int k = 0; k < kPerSlot * 4; ++k)
-                            tc::mma_bf16(tmem + kColO + (j * kPerSlot + (k >> 2)) * NC,
-                                         cd.at(c0 + (k >> 2) * 2 * kBlk + (k & 3) * 2048), pd.at(rb.slot * kTok * NC * 2 + (k & 3) * kPStep<NC>), id,
-                                         t > 0 || (k & 3) > 0 ? 1u : 0u);
-                        tc::commit(&sm.empty[rp.slot]);
-                        if (j == kPairs / kPerSlot - 1)
-                            tc::commit(&sm.pv_done[rb.slot]);
+                        for (int j = 0; j < kPairs; ++j)
+#pragma unroll
+                            for (int k = 0; k < 2 * kTurns; ++k)
+                                tc::mma_f8(tmem + kColO + j * SM::kParts * NC, cd.at(c0 + j * kBlk + (k & 1) * 4096),
+                                           pd.at(p0 + (k >> 1) * kTok * NC + (k & 1) * 32 * NC), id, t > 0 || k > 0 ? 1u : 0u);
+                        tc::commit(&sm.empty_stage[rst.slot]);
+                        tc::commit(&sm.pv_done[rb.slot]);
                     }
+                    rst.step();
+                } else {
+                    constexpr uint32_t id = tc::idesc_bf16(128, NC, true, true);
+                    const Desc cd(smem_u32(sm.ring[0]), kBlk, 1024, tc::kSw128);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j, rp.step())
+                        if (elect()) {
+                            const uint32_t c0 = rp.slot * SM::kSlot;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                tc::mma_bf16(tmem + kColO + (2 * j + (k >> 2)) * NC,
+                                             cd.at(c0 + (k >> 2) * 2 * kBlk + (k & 3) * 2048),
+                                             pd.at(p0 + (k & 3) * 32 * NC), id, t > 0 || (k & 3) > 0 ? 1u : 0u);
+                            tc::commit(&sm.empty[rp.slot]);
+                            if (j == 1)
+                                tc::commit(&sm.pv_done[rb.slot]);
+                        }
                 }
             }
     } else if (warp == 7) {
-        if (kE4M3)
-            regs_dec<64>();
         // ---------------- Q of each piece: NC columns (token, head) x 576, K-major; e4m3: its terms, the
         // second behind the first.  Columns behind the last hold other rows of q or nothing; they
         // stay columns of their own.
@@ -567,57 +562,18 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 __syncwarp();
             }
         }
-    } else if (kE4M3 && warp >= 8) {
-        regs_dec<96>();
-        // ---------------- codes to f16 rows: two warps a pair of blocks (32 rows each), 8 rows x 4
-        // vectors of 16 codes at a time, so that both the swizzled reads and the swizzled writes touch
-        // every bank once
-        static_assert(!kE4M3 || (kConv == 2 * kPairs && SM::kRing == kPairs), "a pair keeps its warps and its place");
-        const int j = (warp - 8) >> 1, row0 = ((warp - 8) & 1) * 32 + (lane & 7), chunk = lane >> 3;
-        Ring<SM::kStage> rst;
-        uint32_t nt = 0;
-        for (; w.take > 0 && !wait.dead; w.next(a)) {
-            const int len = a.kv_lens[w.n];
-            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t, ++nt, rst.step()) {
-                wait(&sm.full_stage[rst.slot], rst.round & 1);
-                const unsigned char *src = sm.stage[rst.slot] + j * kBlk;
-                uint4 c[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = row0 + (i >> 1) * 8, ch = (i & 1) * 4 + chunk;
-                    c[i] = *reinterpret_cast<const uint4 *>(src + row * 128 + ((ch ^ (row & 7)) << 4));
-                    if (row >= len - t * kTok)  // behind the sequence's end: anything may be there
-                        c[i] = make_uint4(0, 0, 0, 0);
-                }
-                if (nt > 0)
-                    wait(&sm.empty[j], (nt - 1) & 1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = row0 + (i >> 1) * 8;
-                    const uint2 x = decode4(c[i].x), y = decode4(c[i].y), z = decode4(c[i].z), u = decode4(c[i].w);
-                    unsigned char *p = sm.ring[j] + (i & 1) * kBlk + row * 128;
-                    *reinterpret_cast<uint4 *>(p + (((2 * chunk) ^ (row & 7)) << 4)) = make_uint4(x.x, x.y, y.x, y.y);
-                    *reinterpret_cast<uint4 *>(p + (((2 * chunk + 1) ^ (row & 7)) << 4)) = make_uint4(z.x, z.y, u.x, u.y);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.full[j]);
-                    mbar_arrive(&sm.empty_stage[rst.slot]);
-                }
-            }
-        }
     } else {
-        // ---------------- softmax: rows 16 warp + lane / 4 (+ 8), columns 8 j + 2 (lane % 4) (+ 1)
-        if (kE4M3)
-            regs_inc<208>();
+        // ---------------- softmax: a group of four warps half the columns each; a thread rows
+        // 16 (warp % 4) + lane / 4 (+ 8), the group's columns 8 j + 2 (lane % 4) (+ 1)
         if (kE4M3)  // q's row scales
             asm volatile("griddepcontrol.wait;" ::: "memory");
-        constexpr int J = NC / 8;
-        const int r0 = warp * 16 + (lane >> 2);
-        const uint32_t lane_base = tc::taddr(tmem, (uint32_t)warp * 32, 0);
+        constexpr int kCols = NC / 2, J = kCols / 8;
+        const int group = warp >> 3, quarter = warp & 3, gtid = quarter * 32 + lane, r0 = quarter * 16 + (lane >> 2);
+        const uint32_t lane_base = tc::taddr(tmem, (uint32_t)quarter * 32, 0) + group * kCols;
+        auto col = [&](int i) { return group * kCols + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
         uint32_t nt = 0;
         Ring<SM::kRing> rp;
+        Ring<SM::kStage> rst;
         // P^T and O^T of tile n: which buffer and round
         auto pv_wait = [&](uint32_t n) { wait(&sm.pv_done[n % SM::kPB], n / SM::kPB & 1); };
         for (; w.take > 0; w.next(a)) {
@@ -626,31 +582,31 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 // columns behind the last: weights 0, and no say in when to rescale
-                m[i] = ct * NC + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1) < cols ? -INFINITY : INFINITY;
+                m[i] = ct * NC + col(i) < cols ? -INFINITY : INFINITY;
                 l[i] = 0.0f;
                 if (kE4M3) {
-                    const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                    const int c = col(i);
                     mo[i] = m[i];
                     base[i] = 0.0f;
                     qs[i] = ct * NC + c < cols
                                 ? a.q_scale[(int64_t)w.n * a.Sq * a.H + w.g * Hg + sm.row[c]] * a.scale_log2 : 0.0f;
                 }
             }
-            for (int t = w.t; t < w.t + w.take; ++t, ++nt) {
+            for (int t = w.t; t < w.t + w.take; ++t, ++nt, rst.step()) {
                 const uint32_t sb = nt & 1;
                 float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
                 if constexpr (kE4M3) {
-                    wait(&sm.full_scale[nt & 7], (nt >> 3) & 1);
-                    page_scale = sm.scale[nt & 7][warp * 16 / maps.rows];
+                    wait(&sm.full_scale[rst.slot], rst.round & 1);
+                    page_scale = sm.scale[rst.slot][quarter * 16 / maps.rows];
                 }
                 const float lg = kE4M3 ? log2f(page_scale) : 0.0f;
                 wait(&sm.s_full[sb], (nt / 2) & 1);
                 tc::fence_after_sync();
                 float s[J][4];
                 if constexpr (kE4M3)
-                    load_s2<NC>(lane_base + sb * SM::kSW, s);
+                    load_s2<kCols>(lane_base + sb * SM::kSW, NC, s);
                 else
-                    load_s<NC>(lane_base + sb * SM::kSW, s);
+                    load_s<kCols>(lane_base + sb * SM::kSW, s);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0)
@@ -666,7 +622,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         s[j][i] *= f;
                         s[j][2 + i] *= f;
                         if (edge) {
-                            const int cg = ct * NC + 8 * j + 2 * (lane & 3) + i;
+                            const int cg = ct * NC + col(k);
                             const int last = len - a.Sq + (a.Sq == 1 ? 0 : min(cg / Hg, a.Sq - 1));
                             if (t * kTok + r0 > last)
                                 s[j][i] = -INFINITY;
@@ -676,7 +632,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         const float most = (kE4M3 ? fminf(m[k], mo[k] - lg) : m[k]) + kGrow;
                         grow |= s[j][i] > most || s[j][2 + i] > most;
                     }
-                if (softmax_or(grow)) {
+                if (softmax_or(group, grow)) {
                     // new column maxima over the tile's 64 rows
                     float f[2 * J];
 #pragma unroll
@@ -686,15 +642,15 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                         for (int d = 4; d < 32; d <<= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
                         if (lane < 4) {
-                            sm.red[warp][8 * (i >> 1) + 2 * lane + (i & 1)] = x;
+                            sm.red[quarter][col(i)] = x;
                             if (kE4M3)
-                                sm.red_o[warp][8 * (i >> 1) + 2 * lane + (i & 1)] = x + lg;
+                                sm.red_o[quarter][col(i)] = x + lg;
                         }
                     }
-                    softmax_sync();
+                    softmax_sync(group);
 #pragma unroll
                     for (int i = 0; i < 2 * J; ++i) {
-                        const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                        const int c = col(i);
                         const float mn = fmaxf(fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c])),
                                                m[i]);
                         f[i] = m[i] == mn ? 1.0f : ex2(m[i] - mn);
@@ -708,22 +664,24 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                             // a weight's share of O^T is p scale base: in units of 2^(mo - m - kLift)
                             base[i] = ex2((mn == -INFINITY ? 0.0f : mn) - (on == -INFINITY ? 0.0f : on) + kLift);
                         }
-                        if (warp == 0 && lane < 4)
+                        if (quarter == 0 && lane < 4)
                             sm.fac[c] = f[i];
                     }
-                    softmax_sync();
+                    softmax_sync(group);
                     if (t > w.t) {
                         pv_wait(nt - 1);  // O^T of the tiles so far is complete
                         tc::fence_after_sync();
 #pragma unroll 1
-                        for (int b = 0; b < kPairs * NC / 16; ++b) {
+                        for (int b = 0; b < kPairs * SM::kParts * kCols / 16; ++b) {
+                            const int c0 = b * 16 % kCols;
+                            const uint32_t at = lane_base + kColO + b * 16 / kCols * NC + c0;
                             uint32_t y[16];
-                            tc::ld_32x32b_x16(lane_base + kColO + b * 16, y);
+                            tc::ld_32x32b_x16(at, y);
                             tc::wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.fac[b * 16 % NC + i]);
-                            tc::st_32x32b_x16(lane_base + kColO + b * 16, y);
+                                y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.fac[group * kCols + c0 + i]);
+                            tc::st_32x32b_x16(at, y);
                         }
                         tc::wait_st();
                     }
@@ -741,30 +699,47 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 unsigned char *pt = sm.p[nt % SM::kPB];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
-                    const int c = 8 * j + 2 * (lane & 3);
-                    uint32_t w0, w1;  // rows r0 and r0 + 8
+                    const int c = col(2 * j);
                     if constexpr (kE4M3) {
+                        // rounded to f16, then the leading three bits of what is left at a time, the last rounded
                         const float g[2] = {page_scale * base[2 * j], page_scale * base[2 * j + 1]};
-                        const __half2 h0 = __floats2half2_rn(s[j][0] * g[0], s[j][1] * g[1]);
-                        const __half2 h1 = __floats2half2_rn(s[j][2] * g[0], s[j][3] * g[1]);
-                        w0 = *reinterpret_cast<const uint32_t *>(&h0);
-                        w1 = *reinterpret_cast<const uint32_t *>(&h1);
+                        __half2 h[2] = {__floats2half2_rn(s[j][0] * g[0], s[j][1] * g[1]),
+                                        __floats2half2_rn(s[j][2] * g[0], s[j][3] * g[1])};
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            uint32_t u[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x = *reinterpret_cast<const uint32_t *>(&h[i]);
+                                u[i] = (k < 2 ? x : x + 0x00800080u) & 0xff00ff00u;
+                                h[i] = __hsub2(h[i], *reinterpret_cast<const __half2 *>(&u[i]));
+                            }
+                            const uint32_t v = __byte_perm(u[0], u[1], 0x7531);
+                            *reinterpret_cast<uint16_t *>(pt + k * kTok * NC + p_off<NC, true>(r0, c)) = (uint16_t)v;
+                            *reinterpret_cast<uint16_t *>(pt + k * kTok * NC + p_off<NC, true>(r0 + 8, c)) =
+                                (uint16_t)(v >> 16);
+                        }
                     } else {
-                        w0 = pack_bf16x2(s[j][0], s[j][1]);
-                        w1 = pack_bf16x2(s[j][2], s[j][3]);
+                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0, c)) = pack_bf16x2(s[j][0], s[j][1]);
+                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0 + 8, c)) = pack_bf16x2(s[j][2], s[j][3]);
                     }
-                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0, c)) = w0;
-                    *reinterpret_cast<uint32_t *>(pt + p_off<NC>(r0 + 8, c)) = w1;
                 }
-                if constexpr (!kE4M3) {
-                    // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
-                    const int rows = len - t * kTok;
+                // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
+                const int rows = len - t * kTok;
+                if constexpr (kE4M3) {
+                    if (rows < kTok) {
+                        wait(&sm.full_stage[rst.slot], rst.round & 1);
+                        for (int v = group * 128 + gtid; v < (kTok - rows) * 32; v += 256)
+                            *reinterpret_cast<uint4 *>(sm.stage[rst.slot] + (v >> 3 & 3) * kBlk + (rows + v / 32) * 128 +
+                                                       (v & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                } else {
                     if (rows < kTok) {
                         Ring<SM::kRing> rz = rp;
 #pragma unroll
                         for (int j = 0; j < 2; ++j, rz.step()) {
                             wait(&sm.full[rz.slot], rz.round & 1);
-                            for (int v = tid; v < (kTok - rows) * 32; v += 128)
+                            for (int v = group * 128 + gtid; v < (kTok - rows) * 32; v += 256)
                                 *reinterpret_cast<uint4 *>(sm.ring[rz.slot] + (v >> 3 & 3) * kBlk + (rows + v / 32) * 128 +
                                                            (v & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
@@ -781,32 +756,33 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
             // ---- the piece's sums, and its result
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
-                const int c = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+                const int c = col(i);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
                 if (lane < 4) {
-                    sm.red[warp][c] = l[i];
-                    if (warp == 0) {
+                    sm.red[quarter][c] = l[i];
+                    if (quarter == 0) {
                         sm.top[c] = m[i];
                         if (kE4M3)
                             sm.top_o[c] = mo[i];
                     }
                 }
             }
-            softmax_sync();
+            softmax_sync(group);
             const bool whole = w.whole();
             const int64_t unit = (int64_t)w.n * a.G + w.g, slot = (int64_t)blockIdx.x * 2 + (w.inside ? 1 : 0);
             const int64_t row0 = (int64_t)w.n * a.Sq * a.H + w.g * Hg;
-            if (tid < NC) {
-                const float sum = sm.red[0][tid] + sm.red[1][tid] + sm.red[2][tid] + sm.red[3][tid];
-                const float lse2 = sum == 0.0f ? -INFINITY : sm.top[tid] + log2f(sum);
-                const float unit = kE4M3 ? ex2((sm.top_o[tid] == -INFINITY ? 0.0f : sm.top_o[tid]) - sm.top[tid] - kLift) : 1.0f;
-                sm.fac[tid] = sum == 0.0f ? 0.0f : unit / sum;
+            if (gtid < kCols) {
+                const int c = group * kCols + gtid;
+                const float sum = sm.red[0][c] + sm.red[1][c] + sm.red[2][c] + sm.red[3][c];
+                const float lse2 = sum == 0.0f ? -INFINITY : sm.top[c] + log2f(sum);
+                const float unit = kE4M3 ? ex2((sm.top_o[c] == -INFINITY ? 0.0f : sm.top_o[c]) - sm.top[c] - kLift) : 1.0f;
+                sm.fac[c] = sum == 0.0f ? 0.0f : unit / sum;
                 if (!whole)
-                    a.part_lse[slot * NC + tid] = lse2;
-                else if (a.lse && ct * NC + tid < cols)
-                    a.lse[row0 + sm.row[tid]] = lse2 * kLn2;
+                    a.part_lse[slot * NC + c] = lse2;
+                else if (a.lse && ct * NC + c < cols)
+                    a.lse[row0 + sm.row[c]] = lse2 * kLn2;
             }
             if (tid == 0) {
                 int *mt = reinterpret_cast<int *>(a.meta + unit * a.CT + ct);
@@ -815,15 +791,18 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 if (w.t + w.take == w.tiles)
                     mt[1] = share;
             }
-            softmax_sync();
+            softmax_sync(group);
             pv_wait(nt - 1);
             tc::fence_after_sync();
-            const int dim = warp * 32 + lane, live = cols - ct * NC;
+            const int dim = gtid, live = cols - ct * NC;
 #pragma unroll 1
-            for (int b = 0; b < kPairs * NC / 16; ++b) {
-                uint32_t y[16];
-                tc::ld_32x32b_x16(lane_base + kColO + b * 16, y);
-                const int pair = b * 16 / NC, c0 = b * 16 % NC;
+            for (int b = 0; b < kPairs * kCols / 16; ++b) {
+                const int pair = b * 16 / kCols, c0 = group * kCols + b * 16 % kCols;
+                const uint32_t at = lane_base + kColO + pair * SM::kParts * NC + b * 16 % kCols;
+                uint32_t y[SM::kParts][16];
+#pragma unroll
+                for (int i = 0; i < SM::kParts; ++i)
+                    tc::ld_32x32b_x16(at + i * NC, y[i]);
                 float f[16];
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
@@ -831,7 +810,13 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    f[i] = f[i] == 0.0f ? 0.0f : __uint_as_float(y[i]) * f[i];
+                {
+                    float x = __uint_as_float(y[0][i]);
+#pragma unroll
+                    for (int k = 1; k < SM::kParts; ++k)
+                        x += __uint_as_float(y[k][i]);
+                    f[i] = f[i] == 0.0f ? 0.0f : x * f[i];
+                }
                 if (!whole) {
                     float *dst = a.part_o + ((slot * kPairs + pair) * (NC / 4) + c0 / 4) * 512 + dim * 4;
 #pragma unroll
@@ -850,7 +835,7 @@ __global__ void __launch_bounds__(kThreads<kE4M3>, 1)
                     }
                 }
             }
-            softmax_sync();  // sm.fac and sm.red are free again
+            softmax_sync(group);  // sm.fac and sm.red are free again
             tc::fence_before_sync();
         }
     }
@@ -992,7 +977,7 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
             return e;
     }
     cfg.gridDim = dim3(a.shares * a.CT);
-    cfg.blockDim = dim3(kThreads<kE4M3>);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps, a)) != cudaSuccess)
         return e;

@@ -97,70 +97,63 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// A barrier and a vote of the four softmax warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_or(bool x)
+// A barrier and a vote of one group of four softmax warps.
+__device__ __forceinline__ void softmax_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ bool softmax_or(int group, bool x)
 {
     int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.s32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
         "selp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((int)x)
+        : "r"((int)x), "r"(1 + group)
         : "memory");
     return r != 0;
 }
 
-// P^T of the decode: [64 rows][NC columns] bfloat16, MN-major with the swizzle of its row length.
-template <int NC>
+// P^T of the decode, MN-major with the swizzle of its row length: [64 rows][NC columns] bfloat16,
+// or three terms of [64 rows][NC columns] e5m2 one behind the other.
+template <int NC, bool k8>
 __device__ __forceinline__ uint32_t p_off(int row, int col)
 {
+    if (k8)
+        return row * NC + (((col >> 4) ^ (NC == 64 ? row >> 1 & 3 : row >> 2 & 1)) << 4) + (col & 15);
     return NC == 64 ? tc::mnmaj_sw128(row, col, 64) : tc::mnmaj_sw64(row, col);
 }
-template <int NC>
+template <int NC, bool k8>
 __device__ __forceinline__ Desc p_desc(uint32_t base)
 {
+    if (k8)  // at 32 columns the terms are the next 32-column atoms of one operand
+        return NC == 64 ? Desc(base, 64 * 64, 512, tc::kSw64) : Desc(base, 64 * 32, 256, tc::kSw32);
     return NC == 64 ? Desc(base, 64 * 128, 1024, tc::kSw128) : Desc(base, 0, 512, tc::kSw64);
 }
-template <int NC>
-constexpr uint32_t kPStep = NC * 2 * 16;  // bytes of 16 rows of P^T
 
-// A 64 x NC accumulator of an M = 64 product in fragment order (see ld_16x256b_x4).
-template <int NC>
-__device__ __forceinline__ void load_s(uint32_t taddr, float (&s)[NC / 8][4])
+// 16 or 32 columns of an M = 64 accumulator in fragment order (see ld_16x256b_x2).
+template <int kCols>
+__device__ __forceinline__ void load_s(uint32_t taddr, float (&s)[kCols / 8][4])
 {
-    uint32_t r[NC / 2];
-    if constexpr (NC == 64)
-        tc::ld_16x256b_x8(taddr, r);
-    else
+    uint32_t r[kCols / 2];
+    if constexpr (kCols == 32)
         tc::ld_16x256b_x4(taddr, r);
+    else
+        tc::ld_16x256b_x2(taddr, r);
     tc::wait_ld();
 #pragma unroll
-    for (int i = 0; i < NC / 2; ++i)
+    for (int i = 0; i < kCols / 2; ++i)
         s[i / 4][i % 4] = __uint_as_float(r[i]);
 }
 
-// Two such accumulators side by side, the second worth a sixteenth: their sum.
-template <int NC>
-__device__ __forceinline__ void load_s2(uint32_t taddr, float (&s)[NC / 8][4])
+// The same and a sixteenth of the columns `apart` further on: the two terms' sum.
+template <int kCols>
+__device__ __forceinline__ void load_s2(uint32_t taddr, uint32_t apart, float (&s)[kCols / 8][4])
 {
-    float t[NC / 8][4];
-    if constexpr (NC == 64) {
-        load_s<64>(taddr, s);
-        load_s<64>(taddr + 64, t);
-    } else {
-        float both[8][4];
-        load_s<64>(taddr, both);
+    float t[kCols / 8][4];
+    load_s<kCols>(taddr, s);
+    load_s<kCols>(taddr + apart, t);
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) {
-            s[i / 4][i % 4] = both[i / 4][i % 4];
-            t[i / 4][i % 4] = both[4 + i / 4][i % 4];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NC / 2; ++i)
+    for (int i = 0; i < kCols / 2; ++i)
         s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 0.0625f, s[i / 4][i % 4]);
 }
 

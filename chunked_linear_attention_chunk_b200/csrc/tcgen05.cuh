@@ -63,6 +63,12 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
            | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// e4m3 x e5m2 -> f32, both MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_mn(int M, int N)
+{
+    return idesc_e4m3(M, N) | (1u << 10) | (1u << 15) | (1u << 16);  // B format: e5m2 (1)
+}
+
 // ------------------------------------------------------------------ TMEM management
 // Allocate `ncols` TMEM columns (power of two >= 32); one full warp calls this.  The
 // TMEM base address is written to *slot (shared memory).
@@ -157,9 +163,18 @@ __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
-// Lanes 0..15 of the warp's quarter (an M = 64 accumulator's 16 rows) x 32 columns, in the
+// Lanes 0..15 of the warp's quarter (an M = 64 accumulator's 16 rows) x 16 columns, in the
 // fragment order of a 16 x 8 tile: r[4 j + 0, 1] are columns 8 j + 2 (lane % 4) + 0, 1 of row
 // lane / 4, r[4 j + 2, 3] the same columns of row lane / 4 + 8.
+__device__ __forceinline__ void ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// The same over 32 columns.
 __device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
@@ -167,21 +182,6 @@ __device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-// The same over 64 columns.
-__device__ __forceinline__ void ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
 }
