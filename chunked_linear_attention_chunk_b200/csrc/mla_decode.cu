@@ -65,7 +65,8 @@ struct DecArgs {
     __nv_bfloat16 *o;
     float *lse;
     float *part_o, *part_lse;  // [CTA][2][4][NC / 4][128][4] (pair, column / 4, number, column % 4), [CTA][2][NC]
-    int2 *meta;                // [unit][CT]: 2 * first share + (it starts inside that share), last share
+    int4 *meta;                // [share][CT]: the unit that starts in the share and goes on behind it, as
+                               // sequence, group, shares covered (0: there is none), which of the two slots
     // e4m3: q's terms [2][rows of q][576] and row scales
     unsigned char *q_terms;
     float *q_scale;
@@ -146,7 +147,7 @@ struct DecSmem {
     uint64_t s_full[2], s_empty[2], p_full[kPB], pv_done[kPB], q_full, q_empty;
     uint32_t tmem_slot;
     int64_t find[40];
-    int64_t share[2];  // first tile and tiles of the CTA's share
+    int64_t share[3];  // first tile and tiles of the CTA's share, tiles of a full one
     int first[4];      // n, g, t of its first tile; whether that is the unit's first
 };
 
@@ -218,6 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up meanwhile
     if (tid == 0) {
+        prefetch_map(&maps.latent);
+        prefetch_map(&maps.rope);
+        prefetch_map(&maps.q);
+        if (kE4M3)
+            prefetch_map(&maps.q_rope);
         for (int i = 0; i < SM::kRing; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
@@ -252,14 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this CTA's share: all tiles, then the unit that its first one falls in
     {
         int64_t mine = 0;
-        bool bad = false;
+        bool bad = false, none = false;
         for (int n = tid; n < a.N; n += kThreads) {
             const int t = tiles_of(a, n);
             mine += t;
             bad |= t == 0 && a.kv_lens[n] != 0;
-            if (t == 0 && n % a.shares == share)  // nobody's piece: the join writes its (empty) result
-                for (int g = 0; g < a.G; ++g)
-                    a.meta[((int64_t)n * a.G + g) * a.CT + ct] = make_int2(0, -1);
+            none |= t == 0 && n % a.shares == share;
         }
         if (bad)
             report_device_error(a.status, KDA_ERR_INVALID_ARG);
@@ -272,14 +276,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tiles = begin < end ? tiles_of(a, it.seq) : 1;
             sm.share[0] = begin;
             sm.share[1] = end - begin;
+            sm.share[2] = per;
             sm.first[0] = it.seq;
             sm.first[1] = it.k / tiles;
             sm.first[2] = it.k % tiles;
         }
+        // sequences that are nobody's piece are dealt out for their (empty) results
+        tc::fence_before_sync();
+        if (__syncthreads_or(none))
+            for (int n = share; n < a.N; n += a.shares)
+                if (tiles_of(a, n) == 0)
+                    for (int i = warp; i < a.G * min(NC, cols - ct * NC); i += kThreads / 32) {
+                        const int64_t row = (int64_t)n * a.Sq * a.H + i % a.G * Hg + sm.row[i / a.G];
+                        for (int v = lane; v < kDL / 8; v += 32)
+                            reinterpret_cast<uint4 *>(a.o + row * kDL)[v] = make_uint4(0, 0, 0, 0);
+                        if (lane == 0 && a.lse)
+                            a.lse[row] = -INFINITY;
+                    }
+        tc::fence_after_sync();
     }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
     const uint32_t tmem = sm.tmem_slot;
     Pieces w;
     w.n = sm.first[0], w.g = sm.first[1], w.t = sm.first[2];
@@ -572,11 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)quarter * 32, 0) + group * kCols;
         auto col = [&](int i) { return group * kCols + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
         uint32_t nt = 0;
+        bool go_on = false;  // a unit goes on behind the share that it starts in
         Ring<SM::kRing> rp;
         Ring<SM::kStage> rst;
         // P^T and O^T of tile n: which buffer and round
         auto pv_wait = [&](uint32_t n) { wait(&sm.pv_done[n % SM::kPB], n / SM::kPB & 1); };
-        for (; w.take > 0; w.next(a)) {
+        Pieces next = w;
+        for (; w.take > 0; w = next) {
             const int len = a.kv_lens[w.n];
             float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1], mo[kE4M3 ? 2 * J : 1], base[kE4M3 ? 2 * J : 1];
 #pragma unroll
@@ -594,14 +611,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int t = w.t; t < w.t + w.take; ++t, ++nt, rst.step()) {
                 const uint32_t sb = nt & 1;
-                float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
-                if constexpr (kE4M3) {
-                    wait(&sm.full_scale[rst.slot], rst.round & 1);
-                    page_scale = sm.scale[rst.slot][quarter * 16 / maps.rows];
-                }
-                const float lg = kE4M3 ? log2f(page_scale) : 0.0f;
-                wait(&sm.s_full[sb], (nt / 2) & 1);
+                // S^T, the page scales, and (where there are two buffers) that P^T's has been read
+                uint64_t *s_bar = &sm.s_full[sb];
+                const uint32_t s_par = nt / 2 & 1;
+                const bool old = SM::kPB == 2 && nt >= 2;
+                wait(s_bar, s_par, old ? &sm.pv_done[sb] : s_bar, old ? s_par ^ 1 : s_par,
+                     kE4M3 ? &sm.full_scale[rst.slot] : s_bar, kE4M3 ? rst.round & 1 : s_par);
                 tc::fence_after_sync();
+                float page_scale = 1.0f;  // of this warp's 16 rows, which lie in one page
+                if constexpr (kE4M3)
+                    page_scale = sm.scale[rst.slot][quarter * 16 / maps.rows];
                 float s[J][4];
                 if constexpr (kE4M3)
                     load_s2<kCols>(lane_base + sb * SM::kSW, NC, s);
@@ -611,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&sm.s_empty[sb]);
+                const float lg = kE4M3 ? log2f(page_scale) : 0.0f;
                 bool grow = false;
                 const bool edge = (t + 1) * kTok > len - a.Sq + 1;  // some column's last row is in this tile
 #pragma unroll
@@ -694,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[j][i] = ex2(s[j][i] - (mm == -INFINITY ? 0.0f : mm));
                         l[2 * j + (i & 1)] += s[j][i];
                     }
-                if (nt >= SM::kPB)
-                    pv_wait(nt - SM::kPB);  // this buffer of P^T has been read
+                if (SM::kPB == 1 && nt > 0)
+                    pv_wait(nt - 1);  // P^T's one buffer has been read
                 unsigned char *pt = sm.p[nt % SM::kPB];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -753,7 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     mbar_arrive(&sm.p_full[nt % SM::kPB]);
             }
-            // ---- the piece's sums, and its result
+            // ---- the piece's sums, and its result (the next one is looked up while the last products run)
+            next.next(a);
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 const int c = col(i);
@@ -784,12 +805,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (a.lse && ct * NC + c < cols)
                     a.lse[row0 + sm.row[c]] = lse2 * kLn2;
             }
-            if (tid == 0) {
-                int *mt = reinterpret_cast<int *>(a.meta + unit * a.CT + ct);
-                if (w.t == 0)
-                    mt[0] = 2 * share + (w.inside ? 1 : 0);
-                if (w.t + w.take == w.tiles)
-                    mt[1] = share;
+            if (w.t == 0 && !whole) {
+                go_on = true;
+                if (tid == 0)
+                    a.meta[blockIdx.x] = make_int4(w.n, w.g, 1 + (int)((w.tiles - w.take + sm.share[2] - 1) / sm.share[2]),
+                                                   w.inside ? 1 : 0);
             }
             softmax_sync(group);
             pv_wait(nt - 1);
@@ -838,6 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             softmax_sync(group);  // sm.fac and sm.red are free again
             tc::fence_before_sync();
         }
+        if (tid == 0 && !go_on)
+            a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     wait.report(a.status);
     tc::fence_before_sync();
@@ -847,25 +869,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial results of the units that several shares cover, and writes the empty result
-// of the units that none does.  128 threads, one latent number each, take four columns of one
-// unit and one pair; the shares' weights are formed once, by the first threads.
+// Joins the partial results of the unit that starts in share x and goes on behind it.  128 threads,
+// one latent number each, take four columns of kP pairs; the shares' weights are formed once, by the
+// first threads.
 constexpr int kJoinShares = 64;  // weights held at once
 
-template <int NC>
+template <int NC, int kP>
 __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
 {
     __shared__ __align__(16) float wgt[kJoinShares][4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, c0 = blockIdx.y * 4, pair = blockIdx.z;
-    const int64_t uc = blockIdx.x;  // unit * CT + ct
-    const int2 mt = a.meta[uc];
-    const int first = mt.x >> 1, count = mt.y - first + 1;
-    const int ct = (int)(uc % a.CT), Hg = a.H / a.G, left = a.Sq * Hg - ct * NC - c0;
-    if (count == 1 || left <= 0)
+    const int tid = threadIdx.x, c0 = blockIdx.y * 4, pair0 = blockIdx.z * kP;
+    const int4 mt = a.meta[blockIdx.x];
+    const int count = mt.z, ct = blockIdx.x % a.CT, Hg = a.H / a.G, left = a.Sq * Hg - ct * NC - c0;
+    if (count == 0 || left <= 0)
         return;
-    const int64_t unit = uc / a.CT, row0 = unit / a.G * a.Sq * a.H + unit % a.G * Hg;
-    auto slot_of = [&](int i) { return ((int64_t)(first + i) * a.CT + ct) * 2 + (i == 0 ? mt.x & 1 : 0); };
+    const int64_t row0 = (int64_t)mt.x * a.Sq * a.H + mt.y * Hg;
+    auto slot_of = [&](int i) { return ((int64_t)blockIdx.x + (int64_t)i * a.CT) * 2 + (i == 0 ? mt.w : 0); };
     // warp c: column c's largest lse and the sum of weights
     const int lane = tid & 31, c = tid >> 5;
     float top = -INFINITY;
@@ -878,7 +898,7 @@ __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
         const float x = __shfl_xor_sync(0xffffffffu, top, d);
         top = x > top || x != x ? x : top;
     }
-    float sum = 0.0f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.0f, acc[kP][4] = {};
     for (int i0 = 0; i0 < count; i0 += kJoinShares) {
         const int n = min(kJoinShares, count - i0);
         for (int i = lane; i < n; i += 32) {
@@ -887,15 +907,19 @@ __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
             sum += v;
         }
         __syncthreads();
-#pragma unroll 4
+#pragma unroll(kP == 1 ? 4 : 2)
         for (int i = 0; i < n; ++i) {
-            const float4 v = reinterpret_cast<const float4 *>(
-                a.part_o)[((slot_of(i0 + i) * kPairs + pair) * (NC / 4) + c0 / 4) * 128 + tid];
+            const float4 *part = reinterpret_cast<const float4 *>(a.part_o) +
+                                 ((slot_of(i0 + i) * kPairs + pair0) * (NC / 4) + c0 / 4) * 128 + tid;
             const float4 f = *reinterpret_cast<const float4 *>(wgt[i]);
-            acc[0] += f.x * v.x;
-            acc[1] += f.y * v.y;
-            acc[2] += f.z * v.z;
-            acc[3] += f.w * v.w;
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                const float4 v = part[p * (NC / 4) * 128];
+                acc[p][0] += f.x * v.x;
+                acc[p][1] += f.y * v.y;
+                acc[p][2] += f.z * v.z;
+                acc[p][3] += f.w * v.w;
+            }
         }
         __syncthreads();
     }
@@ -903,7 +927,7 @@ __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
     if (lane == 0)
         wgt[0][c] = sum;
     const int cg = ct * NC + c0 + c;
-    if (pair == 0 && a.lse && lane == 0 && c < left)
+    if (pair0 == 0 && a.lse && lane == 0 && c < left)
         a.lse[row0 + cg / Hg * a.H + cg % Hg] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     __syncthreads();
 #pragma unroll
@@ -911,7 +935,10 @@ __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
         const int kg = ct * NC + c0 + k;
         const float s = wgt[0][k];
         if (k < left)
-            a.o[(row0 + kg / Hg * a.H + kg % Hg) * kDL + pair * 128 + tid] = __float2bfloat16(s == 0.0f ? 0.0f : acc[k] / s);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                a.o[(row0 + kg / Hg * a.H + kg % Hg) * kDL + (pair0 + p) * 128 + tid] =
+                    __float2bfloat16(s == 0.0f ? 0.0f : acc[p][k] / s);
     }
 }
 
@@ -929,7 +956,7 @@ DecPlan plan(int N, int Sq, int H, int G)
     p.ct = (Sq * (H / G) + p.nc - 1) / p.nc;
     p.shares = num_sms() / p.ct > 0 ? num_sms() / p.ct : 1;
     const size_t slots = (size_t)p.shares * p.ct * 2;
-    p.part_lse = ((size_t)N * G * p.ct * sizeof(int2) + 255) / 256 * 256;
+    p.part_lse = ((size_t)p.shares * p.ct * sizeof(int4) + 255) / 256 * 256;
     p.part_o = p.part_lse + (slots * p.nc * 4 + 255) / 256 * 256;
     const size_t rows = (size_t)N * Sq * H;
     p.q_scale = p.part_o + slots * p.nc * kDL * 4;
@@ -982,11 +1009,14 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps, a)) != cudaSuccess)
         return e;
     // the join waits on the device for the launch before it to end, and is set up meanwhile
-    cfg.gridDim = dim3(a.N * a.G * a.CT, NC / 4, kPairs);
+    // (few units: each is cut into many shares, and a thread takes one pair of blocks of them)
+    const bool few = (int64_t)a.N * a.G * 4 <= a.shares;
+    cfg.gridDim = dim3(a.shares * a.CT, NC / 4, few ? kPairs : 1);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC>, a);
+    return few ? cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC, 1>, a)
+               : cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC, kPairs>, a);
 }
 
 }  // namespace
@@ -1003,7 +1033,7 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
     DecArgs a{N, Sq, H, G, num_pages, page_size, max_pages, p.ct, p.shares, scale * kLog2e,
               static_cast<const __nv_bfloat16 *>(q), cache_scale, block_table, kv_lens,
               static_cast<__nv_bfloat16 *>(o), lse, reinterpret_cast<float *>(ws + p.part_o),
-              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int2 *>(ws), ws + p.q_terms, reinterpret_cast<float *>(ws + p.q_scale),
+              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int4 *>(ws), ws + p.q_terms, reinterpret_cast<float *>(ws + p.q_scale),
               device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;

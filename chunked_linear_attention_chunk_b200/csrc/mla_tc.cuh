@@ -28,6 +28,28 @@ struct Waits {
                 break;
             }
     }
+    // Three barriers at once.  A ready wait takes some 300 cycles while copies and products keep
+    // shared memory busy; the three tests are in flight together.
+    __device__ __forceinline__ void operator()(uint64_t *x, uint32_t px, uint64_t *y, uint32_t py, uint64_t *z, uint32_t pz)
+    {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q, r;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+            "and.pred p, p, q;\n\t"
+            "and.pred p, p, r;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(x)), "r"(px), "r"(smem_u32(y)), "r"(py), "r"(smem_u32(z)), "r"(pz)
+            : "memory");
+        if (!ok) {
+            (*this)(x, px);
+            (*this)(y, py);
+            (*this)(z, pz);
+        }
+    }
     __device__ __forceinline__ void report(unsigned int *status) const
     {
         if (dead)
@@ -155,6 +177,12 @@ __device__ __forceinline__ void load_s2(uint32_t taddr, uint32_t apart, float (&
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i)
         s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 0.0625f, s[i / 4][i % 4]);
+}
+
+// A kernel's tensor map (a __grid_constant__ argument) into the descriptor cache.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
 // cuTensorMapEncodeTiled, reached through the runtime (the library does not link the driver).
