@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             softmax_sync(group);
             const bool whole = w.whole();
-            const int64_t unit = (int64_t)w.n * a.G + w.g, slot = (int64_t)blockIdx.x * 2 + (w.inside ? 1 : 0);
+            const int64_t slot = (int64_t)blockIdx.x * 2 + (w.inside ? 1 : 0);
             const int64_t row0 = (int64_t)w.n * a.Sq * a.H + w.g * Hg;
             if (gtid < kCols) {
                 const int c = group * kCols + gtid;
@@ -1010,7 +1010,7 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
         return e;
     // the join waits on the device for the launch before it to end, and is set up meanwhile
     // (few units: each is cut into many shares, and a thread takes one pair of blocks of them)
-    const bool few = (int64_t)a.N * a.G * 4 <= a.shares;
+    const bool few = (int64_t)a.N * a.G * 16 <= a.shares;
     cfg.gridDim = dim3(a.shares * a.CT, NC / 4, few ? kPairs : 1);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
