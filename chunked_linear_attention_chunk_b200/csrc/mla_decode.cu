@@ -305,8 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.settle(a);
     Waits wait{false};
 
-    if (warp == 4) {
-        // ---------------- copies
+    if (warp == 4 || warp == 7) {
+        // ---------------- copies: every other tile each (a tile's lookups, waits and copies take a warp
+        // longer than the tensor cores need for it).  Waiting for a place that the other warp filled
+        // last is sound: a warp's previous tile had all but the last round of that place consumed.
+        const uint32_t me = warp == 4 ? 0 : 1;
+        uint32_t nt = 0;
         const int ppt = kTok / maps.rows;  // copies a block
         int batch_n = -1, batch_0 = 0, ids = 0;
         Ring<SM::kRing> rp;
@@ -315,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; w.take > 0 && !wait.dead; w.next(a)) {
             const int len = a.kv_lens[w.n], pages = (len + a.page_size - 1) / a.page_size;
             const int32_t *row = a.block_table + (int64_t)w.n * a.max_pages;
-            int e = w.t * kTok / a.page_size, off = w.t * kTok % a.page_size;  // page entry, slot in it
-            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t) {
+            for (int t = w.t; t < w.t + w.take && !wait.dead; ++t, ++nt, rp.step(), rp.step(), rr.step(), rst.step()) {
+                if ((nt & 1) != me)
+                    continue;
+                int e = t * kTok / a.page_size, off = t * kTok % a.page_size;  // page entry, slot in it
                 // the pool rows of the tile's copies, from the table 32 entries at a time
                 int at[4], live = 0, my_page = -1;  // my_page: of box `lane`
 #pragma unroll
@@ -383,36 +389,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cp_async_arrive(&sm.full_scale[rst.slot]);
                     }
                     __syncwarp();
-                    rst.step();
                 } else {
+                    Ring<SM::kRing> rh = rp;
+                    if (rh.round > 0)  // (first: then the rope place is a round behind at most)
+                        wait(&sm.empty[rh.slot], (rh.round - 1) & 1);
                     if (rr.round > 0)
                         wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
                     if (!wait.dead && elect()) {
                         mbar_arrive_expect_tx(&sm.full_rope[rr.slot], bytes);
                         rope(sm.rope[rr.slot], 128, &sm.full_rope[rr.slot]);
+                        mbar_arrive_expect_tx(&sm.full[rh.slot], 4 * bytes);
+                        half(sm.ring[rh.slot], 0, &sm.full[rh.slot]);
                     }
-                    rr.step();
-#pragma unroll
-                    for (int j = 0; j < 2; ++j, rp.step()) {
-                        if (rp.round > 0)
-                            wait(&sm.empty[rp.slot], (rp.round - 1) & 1);
-                        if (!wait.dead && elect()) {
-                            mbar_arrive_expect_tx(&sm.full[rp.slot], 4 * bytes);
-                            half(sm.ring[rp.slot], 4 * j, &sm.full[rp.slot]);
-                        }
+                    rh.step();
+                    if (rh.round > 0)
+                        wait(&sm.empty[rh.slot], (rh.round - 1) & 1);
+                    if (!wait.dead && elect()) {
+                        mbar_arrive_expect_tx(&sm.full[rh.slot], 4 * bytes);
+                        half(sm.ring[rh.slot], 4, &sm.full[rh.slot]);
                     }
                 }
                 wait.dead = __any_sync(0xffffffffu, wait.dead);
             }
         }
     } else if (warp == 5) {
-        // ---------------- S^T = C Q^T
+        // ---------------- S^T = C Q^T.  Q of each piece: NC columns (token, head) x 576, K-major; e4m3: its
+        // terms, the second behind the first.  Columns behind the last hold other rows of q or
+        // nothing; they stay columns of their own.
+        if constexpr (kE4M3)
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that writes the terms
+        constexpr uint32_t kBytes = kE4M3 ? 2 * kDC : kDC * 2;  // of a column
         Ring<SM::kRing> rp;
         Ring<SM::kRopes> rr;
         Ring<SM::kStage> rst;
         Ring<2> rs;
         uint32_t nq = 0;
         for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
+            if (nq > 0)
+                wait(&sm.q_empty, (nq - 1) & 1);
+            if (wait.dead)
+                break;
+            if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
+                if (elect()) {
+                    const int r = w.n * cols + ct * NC;
+                    mbar_arrive_expect_tx(&sm.q_full, NC * kBytes);
+                    if constexpr (kE4M3) {
+                        tma_load_4d(sm.q, &maps.q, 0, r, 0, 0, &sm.q_full);
+                        tma_load_3d(sm.q + 4 * SM::kSW * 128, &maps.q_rope, 0, r, 0, &sm.q_full);
+                    } else {
+                        tma_load_3d(sm.q, &maps.q, 0, r, 0, &sm.q_full);
+                    }
+                }
+            } else {
+                const int n = (min(cols - ct * NC, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
+                const int row0 = w.n * a.Sq * a.H + w.g * Hg;
+                // a copy's destination is a multiple of 128 bytes: single rope rows of codes (64 bytes)
+                // are moved by the lanes instead
+                const bool by_hand = kE4M3 && maps.q_rows == 1;
+                if (by_hand) {
+                    for (int i = lane; i < 2 * n; i += 32) {
+                        const int c = i >> 1, k = i & 1, r = k * NC + c;
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            a.q_terms + ((int64_t)k * a.N * a.Sq * a.H + row0 + sm.row[c]) * kDC + kDL);
+                        unsigned char *dst = sm.q + 4 * SM::kSW * 128 + r * 64;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<uint4 *>(dst + ((v ^ ((r >> 1) & 3)) << 4)) = src[v];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const int copies = kE4M3 ? (by_hand ? 8 : 10) : kDC / 64;
+                if (elect())
+                    mbar_arrive_expect_tx(&sm.q_full,
+                                          (uint32_t)(n * maps.q_rows) * (by_hand ? kBytes - 2 * kDR : kBytes));
+                __syncwarp();
+                for (int i = lane; i < n * copies; i += 32) {
+                    const int c = i / copies * maps.q_rows, blk = i % copies;
+                    const int r = row0 + sm.row[c];
+                    if (!kE4M3)
+                        tma_load_3d(sm.q + blk * NC * 128 + c * 128, &maps.q, 0, r, blk, &sm.q_full);
+                    else if (blk < 8)
+                        tma_load_4d(sm.q + (blk >> 1) * SM::kSW * 128 + ((blk & 1) * NC + c) * 128, &maps.q, 0, r, blk & 1,
+                                    blk >> 1, &sm.q_full);
+                    else
+                        tma_load_3d(sm.q + 4 * SM::kSW * 128 + ((blk & 1) * NC + c) * 64, &maps.q_rope, 0, r, blk & 1,
+                                    &sm.q_full);
+                }
+                __syncwarp();
+            }
             wait(&sm.q_full, nq & 1);
             for (int t = 0; t < w.take && !wait.dead; ++t, rs.step()) {
                 if (rs.round > 0)
@@ -514,69 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                 }
             }
-    } else if (warp == 7) {
-        // ---------------- Q of each piece: NC columns (token, head) x 576, K-major; e4m3: its terms, the
-        // second behind the first.  Columns behind the last hold other rows of q or nothing; they
-        // stay columns of their own.
-        if constexpr (kE4M3)
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that writes the terms
-        constexpr uint32_t kBytes = kE4M3 ? 2 * kDC : kDC * 2;  // of a column
-        uint32_t nq = 0;
-        for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
-            if (nq > 0)
-                wait(&sm.q_empty, (nq - 1) & 1);
-            if (wait.dead)
-                break;
-            if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
-                if (elect()) {
-                    const int r = w.n * cols + ct * NC;
-                    mbar_arrive_expect_tx(&sm.q_full, NC * kBytes);
-                    if constexpr (kE4M3) {
-                        tma_load_4d(sm.q, &maps.q, 0, r, 0, 0, &sm.q_full);
-                        tma_load_3d(sm.q + 4 * SM::kSW * 128, &maps.q_rope, 0, r, 0, &sm.q_full);
-                    } else {
-                        tma_load_3d(sm.q, &maps.q, 0, r, 0, &sm.q_full);
-                    }
-                }
-            } else {
-                const int n = (min(cols - ct * NC, NC) + maps.q_rows - 1) / maps.q_rows;  // runs of q_rows heads
-                const int row0 = w.n * a.Sq * a.H + w.g * Hg;
-                // a copy's destination is a multiple of 128 bytes: single rope rows of codes (64 bytes)
-                // are moved by the lanes instead
-                const bool by_hand = kE4M3 && maps.q_rows == 1;
-                if (by_hand) {
-                    for (int i = lane; i < 2 * n; i += 32) {
-                        const int c = i >> 1, k = i & 1, r = k * NC + c;
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            a.q_terms + ((int64_t)k * a.N * a.Sq * a.H + row0 + sm.row[c]) * kDC + kDL);
-                        unsigned char *dst = sm.q + 4 * SM::kSW * 128 + r * 64;
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            *reinterpret_cast<uint4 *>(dst + ((v ^ ((r >> 1) & 3)) << 4)) = src[v];
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const int copies = kE4M3 ? (by_hand ? 8 : 10) : kDC / 64;
-                if (elect())
-                    mbar_arrive_expect_tx(&sm.q_full,
-                                          (uint32_t)(n * maps.q_rows) * (by_hand ? kBytes - 2 * kDR : kBytes));
-                __syncwarp();
-                for (int i = lane; i < n * copies; i += 32) {
-                    const int c = i / copies * maps.q_rows, blk = i % copies;
-                    const int r = row0 + sm.row[c];
-                    if (!kE4M3)
-                        tma_load_3d(sm.q + blk * NC * 128 + c * 128, &maps.q, 0, r, blk, &sm.q_full);
-                    else if (blk < 8)
-                        tma_load_4d(sm.q + (blk >> 1) * SM::kSW * 128 + ((blk & 1) * NC + c) * 128, &maps.q, 0, r, blk & 1,
-                                    blk >> 1, &sm.q_full);
-                    else
-                        tma_load_3d(sm.q + 4 * SM::kSW * 128 + ((blk & 1) * NC + c) * 64, &maps.q_rope, 0, r, blk & 1,
-                                    &sm.q_full);
-                }
-                __syncwarp();
-            }
-        }
     } else {
         // ---------------- softmax: a group of four warps half the columns each; a thread rows
         // 16 (warp % 4) + lane / 4 (+ 8), the group's columns 8 j + 2 (lane % 4) (+ 1)
