@@ -37,6 +37,8 @@ kda_status check_expanded(int N, int Tq, int Tk, int H, int dn, int dr, int dv, 
         return KDA_ERR_UNSUPPORTED;
     if (safe_prod({Tq, H, dn + dr}) < 0 || safe_prod({Tk, H, dn + dv}) < 0)
         return KDA_ERR_INVALID_ARG;
+    if (((int64_t)(Tq > Tk ? Tq : Tk) / 128 + N) * H > 0x7fffffff)  // blocks of a launch
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -53,9 +55,9 @@ kda_status check_cache(int N, int G, int dl, int dr, kda_dtype dtype, kda_dtype 
     if (dl != 512 || dr != 64 || dtype != KDA_BF16 || cache_dtype == KDA_F32 || !page_size_ok(page_size) || N > 65535 ||
         G > 1024)
         return KDA_ERR_UNSUPPORTED;
-    // rows of the pool and of a sequence are 32-bit
+    // rows of the pool and of a sequence are 32-bit, the latter up to the end of its last 64-row tile
     if (safe_prod({num_pages, page_size, G}) < 0 || (int64_t)num_pages * page_size * G > 0x7fffffff ||
-        (int64_t)max_pages * page_size > 0x7fffffff / G || safe_prod({num_pages, page_size, G, dl + dr}) < 0)
+        (int64_t)max_pages * page_size > 0x7fffffc0 / G || safe_prod({num_pages, page_size, G, dl + dr}) < 0)
         return KDA_ERR_UNSUPPORTED;
     if (!cache || !block_table || !kv_lens || (cache_dtype == KDA_E4M3) != (cache_scale != nullptr))
         return KDA_ERR_INVALID_ARG;

@@ -612,8 +612,6 @@ cudaError_t launch_side(const BwdMaps &maps, const BwdArgs &a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     const int64_t grid = ((int64_t)(kKeys ? a.Tk : a.Tq) / kRows + a.N) * a.H;  // at least the tiles of any N sequences
-    if (grid > 0x7fffffff)
-        return cudaErrorInvalidValue;
     mla_bwd_kernel<kKeys><<<(unsigned)grid, kThreads, smem, s>>>(maps, a);
     return cudaGetLastError();
 }

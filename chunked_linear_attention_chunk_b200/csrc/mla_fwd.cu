@@ -349,8 +349,6 @@ cudaError_t launch_mla_fwd(int N, const int32_t *cu_q, const int32_t *cu_k, int 
     if (e != cudaSuccess)
         return e;
     const int64_t items = (int64_t)Tq / (kTiles * kRows) + N;  // at least the tile pairs of any N sequences
-    if (items * H > 0x7fffffff)
-        return cudaErrorInvalidValue;
     mla_fwd_kernel<<<(unsigned)(items * H), kThreads, smem, s>>>(maps, a);
     return cudaGetLastError();
 }

@@ -407,8 +407,10 @@ kda_status kda_decode_step(int N, int H, int dk, int dv, kda_dtype dtype, const 
  *   absorbed (kda_mla_decode): queries are carried into the latent space by the caller, so that
  *     every head of a group attends to the same cached rows; decode steps over a paged cache,
  *     which kda_mla_cache_append fills.
- * Token tensors are bfloat16; scores, softmax statistics and sums are float32, a softmax weight
- * is rounded to bfloat16 where it enters a matrix product.
+ * Token tensors are bfloat16; scores, softmax statistics and sums are float32.  A softmax weight is
+ * rounded to bfloat16 where it enters a matrix product.  Over an 8-bit cache a weight times its
+ * page's scale keeps nine bits down to 2^-23 of the largest such product (and 2^-32 of that at
+ * worst), and a number of q eight bits down to 2^-15 of its row's largest (2^-24 at worst).
  *
  * kda_mla_fwd -- attention of packed sequences in the expanded form.  Sequence n has the queries
  * [cu_q[n], cu_q[n+1]) and the keys [cu_k[n], cu_k[n+1]) of its packed axis (cu_k beyond cu_q:
@@ -418,12 +420,14 @@ kda_status kda_decode_step(int N, int H, int dk, int dv, kda_dtype dtype, const 
  * the sequence; the last query sees every key).  A query that sees no key gets o = 0, lse = -inf.
  *   N          sequences (1 .. 65535); cu_q, cu_k: DEVICE int32 [N + 1], 4-byte aligned, first
  *              entry 0, non-decreasing, last entry at most Tq (Tk).  Rows behind the last
- *              sequence are neither read nor written.  Checked on the device: an invalid array
- *              records KDA_ERR_INVALID_ARG in the device status word and nothing is written.
- *   Tq, Tk     rows of the packed axes (0 .. 2^31 - 65); H heads (1 .. 65535).
+ *              sequence are not written and have no influence.  Checked on the device: an invalid
+ *              array records KDA_ERR_INVALID_ARG in the device status word and nothing is written.
+ *   Tq, Tk     rows of the packed axes (0 .. 2^31 - 65); H heads (1 .. 65535); UNSUPPORTED where
+ *              (max(Tq, Tk) / 128 + N) H passes 2^31 - 1.
  *   dn, dr, dv (128, 64, 128).  dtype: KDA_BF16.  scale: finite, > 0.
  *   q          [Tq, H, dn + dr];  kv: [Tk, H, dn + dv], a head's key part, then its value (the
- *              up-projection's output as it is);  k_rope: [Tk, dr].  No row behind cu_k[N] is read.
+ *              up-projection's output as it is);  k_rope: [Tk, dr].  Infinities and NaN stay within
+ *              their sequence and head, where they may reach queries that the mask hides them from.
  *   o          [Tq, H, dv] out;  lse: [Tq, H] float32 out, the natural logarithm of sum_j e^{s_ij},
  *              or NULL.  They overlap neither each other nor an input.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, ALIAS, CUDA.  Tq == 0 does nothing.
@@ -456,14 +460,16 @@ kda_status kda_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, 
  *   KDA_E4M3   rows are e4m3 codes; a row stands for code * cache_scale[page, group] (float32
  *              [num_pages, G], powers of two; kda_mla_cache_append writes them).
  *   page_size  16, 32, or a multiple of 64 up to 65536.
- *   block_table DEVICE int32 [N, max_pages]; entries past a sequence's last page are not read.  kv_lens:
- *              DEVICE int32 [N].  Both 4-byte aligned.
+ *   block_table DEVICE int32 [N, max_pages]; entries past a sequence's last page are not used, and
+ *              a page may be named more than once where it is only read.  kv_lens: DEVICE int32 [N].
+ *              Both 4-byte aligned.  num_pages page_size G <= 2^31 - 1, max_pages page_size G <= 2^31 - 64.
  *
  * kda_mla_decode -- Sq new tokens for each of N sequences in the absorbed form:
  *     s_j = scale q . c_j,  o = sum_j softmax_j(s) c_j[0:dl]
  *   over the first kv_lens[n] - Sq + 1 + i places of sequence n for its i-th new token (kv_lens
  *   counts the new tokens, whose rows are in the cache already).  A token that sees no row gets
- *   o = 0, lse = -inf.
+ *   o = 0, lse = -inf.  What rows behind kv_lens[n] hold has no influence; infinities and NaN in a
+ *   row that only some of a sequence's new tokens see may reach the others.
  *   q          [N, Sq, H, dl + dr] bfloat16 (1 <= Sq, H a multiple of G);  dl, dr: (512, 64).
  *   o          [N, Sq, H, dl] bfloat16 out;  lse: [N, Sq, H] float32 out or NULL.
  *   workspace  >= kda_mla_decode_workspace(N, Sq, H, G, dl, dr) bytes, 16-byte aligned: partial
@@ -479,7 +485,8 @@ kda_status kda_mla_bwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, 
  *   KDA_BF16   copies the rows.
  *   KDA_E4M3   a page's scale for a group becomes the larger of the smallest power of two s >= 2^-100
  *              with |x| <= 448 s for the new rows x of that page and, if the page held earlier rows of
- *              the sequence, its old scale; those rows' codes are rounded anew where the scale grew,
+ *              the sequence, its old scale; those rows' codes are rounded anew where the scale grew
+ *              (once for each time it does),
  *              and the new rows are stored as x / s, rounded to nearest even.  An infinity or a NaN
  *              among a page's new rows makes its scale NaN (and the attention over it).
  *   kv_new     [T_new, G, dl + dr] bfloat16;  cu_new: DEVICE int32 [N + 1] as cu_q above (rows
@@ -535,8 +542,8 @@ size_t kda_chunk_fwd_noalloc_max_scratch(void);
  * kda_device_status -- synchronise `stream`, then return and clear the current
  * device's kernel status word: KDA_OK; KDA_ERR_DEVICE_TIMEOUT if a kernel gave up on a
  * bounded wait since the last call; KDA_ERR_INVALID_ARG if kda_chunk_fwd_varlen found
- * its cu_seqlens invalid or a kda_mla_* call its offsets, lengths or
- * pages; KDA_ERR_DEVICE_BOUNDS if a debug-build index check failed;
+ * its cu_seqlens invalid or a kda_mla_* call its offsets, lengths or pages;
+ * KDA_ERR_DEVICE_BOUNDS if a debug-build index check failed;
  * KDA_ERR_CUDA if the synchronisation failed.  The first error
  * recorded since the last call is the one reported.
  */

@@ -130,6 +130,66 @@ def test_two_decodes_at_once():
         assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_long_tail_of_small_weights(e4m3):
+    """One row far above the rest: 40000 rows of weight 2^-19 or so of the largest, a twelfth of
+    the sum together, and one page between them whose scale is 2^10 times the others'."""
+    L, H = 40000, 16
+    q, c, sc, table, kv_lens = make([L], 1, H, 1, 64, e4m3, seed=75)
+    c[:, :, :, 512:] = 0.0
+    q[..., :512] = 0.0
+    q[..., 512:] = 0.25
+    c[int(table[0, 300]), 17, 0, 512:] = 8.0 if e4m3 else 0.0
+    if e4m3:
+        sc[table[0].long()] = 2.0 ** -7
+        sc[int(table[0, 300])] = 2.0 ** 3
+    else:
+        c[int(table[0, 300]), 17, 0, 512:] = 64.0
+    scale = 19 * math.log(2) / (64 * 0.25 * 64.0)
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, scale=scale, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, [L], scale)
+    ref.close(o, ro, mag, "o")
+    ref.lse_close(lse, rl, 32.0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_reads_a_page_twice_and_no_rows_at_all(e4m3):
+    q, c, sc, table, kv_lens = make([256, 130], 1, 16, 1, 64, e4m3, seed=76)
+    table[1, 1] = table[1, 0]
+    table[0, 3] = table[0, 1]
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, [256, 130], 192 ** -0.5)
+    ref.close(o, ro, mag, "o")
+    o, lse = kda.kda_mla_decode(q, c, table, torch.zeros_like(kv_lens), cache_scale=sc)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    assert kda.kda_device_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pool_past_32_bit_offsets(e4m3):
+    """Append to and attend over the last pages of a pool of more than 2^32 bytes and numbers."""
+    ps, pages, lens = 64, 2 ** 32 // (64 * 576) + 8, [100, 70]
+    g = torch.Generator(device="cuda").manual_seed(77)
+    cache = torch.empty(pages, ps, 1, 576, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16, device="cuda")
+    sc = torch.zeros(pages, 1, device="cuda") if e4m3 else None
+    table = torch.tensor([[pages - 1, pages - 3], [pages - 2, 0]], dtype=torch.int32, device="cuda")
+    rows = torch.randn(sum(lens), 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 100, 170], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kda.kda_mla_cache_append(rows, cu, zero, table, cache, cache_scale=sc)
+    kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for n, (a, b) in enumerate(((0, 100), (100, 170))):
+        held = ref.rows_of(cache, sc, table[n], b - a)
+        err = (held - rows[a:b].double()).abs().amax()
+        assert float(err) <= (2.0 ** -4 * 8 if e4m3 else 0.0)  # half a step of numbers below 8
+    q = (torch.randn(2, 1, 16, 576, generator=g, device="cuda") * 0.6).to(torch.bfloat16)
+    o, lse = kda.kda_mla_decode(q, cache, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, cache, sc, table, lens, 192 ** -0.5)
+    ref.close(o, ro, mag, "o")
+    ref.lse_close(lse, rl, 32.0)
+    assert kda.kda_device_status() == 0
+
+
 def test_decode_records_bad_lengths_and_pages():
     """Recorded in the status word; the other sequences' results stand."""
     lens = [100, 40, 64]

@@ -113,6 +113,16 @@ def test_append_validates(L):
         assert _app(L, **bad) == ALIAS, bad
 
 
+def test_sizes_past_32_bits_are_refused(L):
+    """More blocks than a launch takes; a sequence whose last tile would end behind 2^31 rows."""
+    assert _fwd(L, N=65535, H=65535) == UNSUPPORTED
+    assert _fwd(L, N=65535, Tq=1, H=40000, dt=kda.KDA_BF16) == UNSUPPORTED
+    assert _bwd(L, N=65535, H=65535) == UNSUPPORTED
+    for call in (_dec, _app):
+        assert call(L, ps=16, maxp=(1 << 27) - 1) == UNSUPPORTED
+        assert call(L, ps=32, G=2, maxp=1 << 25) == UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors():
     z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)
     cu = torch.tensor([0, 4], dtype=torch.int32)

@@ -210,6 +210,32 @@ def test_many_sequences():
         ref.close(got[name], r, m, name)
 
 
+def test_packed_axis_past_32_bit_offsets():
+    """The last sequence of packed axes of more than 2^31 numbers; the first one has queries
+    without keys, the second keys without queries."""
+    T, H, n = 150000, 88, 90
+    x, _, _ = make([n], [n], H, seed=51)
+    q = torch.empty(T + n, H, 192, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(T + n, H, 256, dtype=torch.bfloat16, device="cuda")
+    kr = torch.empty(T + n, 64, dtype=torch.bfloat16, device="cuda")
+    q[:T], kv[:T], kr[:T] = 1.0, 1.0, 1.0
+    q[T:], kv[T:], kr[T:] = x["q"], x["kv"], x["kr"]
+    cu_q, cu_k = (torch.tensor(c, dtype=torch.int32, device="cuda") for c in ([0, T, T, T + n], [0, 0, T, T + n]))
+    o, lse = kda.kda_mla_fwd(q, kv, kr, cu_q, cu_k)
+    ro, rl, mag = ref.fwd(x["q"], x["kv"], x["kr"], [0, n], [0, n], 192 ** -0.5, True)
+    ref.close(o[T:], ro, mag, "o")
+    ref.lse_close(lse[T:], rl, 16.0)
+    assert (o[T - 5:T] == 0).all() and torch.isneginf(lse[:T]).all()
+    dO = torch.ones_like(o)
+    dO[T:] = x["dO"]
+    got = kda.kda_mla_bwd(q, kv, kr, o, lse, dO, cu_q, cu_k)
+    want = ref.bwd(x["q"], x["kv"], x["kr"], o[T:], lse[T:], x["dO"], [0, n], [0, n], 192 ** -0.5, True)
+    for name, (r, m) in want.items():
+        ref.close(got[name][T:], r, m, name)
+        assert (got[name][T - 5:T] == 0).all()
+    assert kda.kda_device_status() == 0
+
+
 def test_no_rows():
     x, cq, ck = make([0, 0], [5, 0], 2, seed=49)
     o, lse = kda.kda_mla_fwd(x["q"], x["kv"], x["kr"], x["cu_q"], x["cu_k"])
