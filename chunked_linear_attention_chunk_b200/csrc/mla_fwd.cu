@@ -6,16 +6,20 @@
 // head against 2 x 256 B of K and V a key that 256 queries share.
 //
 // One CTA takes 256 queries of one head as two tiles of 128, so that one tile's softmax runs
-// while the tensor cores work for the other, and walks the keys 96 at a time:
-//   S = Q K^T        (M = 128, N = 96, K = 192; K and the heads' shared k_rope side by side)
-//   O += P V         (M = 128, N = 128, K = 96; P in tensor memory, V read MN-major)
-// 96 keys is the widest tile whose K and V double-buffer beside 96 KB of Q in shared memory (N =
-// 128 would leave V one stage); a 128 x 96 x 16 product takes about 58 cycles against 48 ideal.
-// Tensor memory: two S tiles (P overwrites its first half), two O tiles.
+// while the tensor cores work for the other, and walks the keys 80 at a time:
+//   S = Q K^T        (M = 128, N = 80, K = 192; K and the heads' shared k_rope side by side)
+//   O += P V         (M = 128, N = 128, K = 80; P in tensor memory, V read MN-major)
+// Tensor memory holds two O tiles, and 128 columns a tile for S and P.  80 keys are the most whose S
+// (80) and P (40) fit there side by side, so that S of the next step is taken as soon as the threads
+// have read this one's; with 96 keys P has to overwrite S and S waits for P V: 320 us against 297
+// (16 heads, 8192 tokens, causal; one warp issuing all products 375, since a warp feeds nothing to
+// the tensor cores in the 150 cycles that a ready barrier takes).  A 128 x 80 x 16 product takes 52
+// cycles (its operands' 6.5 KB of shared memory) against 40 ideal, so a step is 1890 cycles of
+// products at least; it measured 2100.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1, one row a thread, no exchange between threads; O is
 // rescaled only when a row's maximum grows by more than 2^8 (float32 sums and a bfloat16 weight
-// hold as well); 8 copies (TMA); 9 issues the products.
+// hold as well); 8 copies (TMA); 9 issues S, 10 issues O.
 #include "mla_common.cuh"
 #include "mla_tc.cuh"
 
@@ -25,10 +29,12 @@ namespace {
 
 using namespace mla;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kRows = 128;               // queries a tile
 constexpr int kTiles = 2;                // tiles a CTA
-constexpr int kKeys = 96;                // keys a step
+constexpr int kKeys = 80;                // keys a step
+constexpr int kV = 3;                    // stages of V
+constexpr uint32_t kP = kKeys;           // columns from S to P
 constexpr uint32_t kQBlk = kRows * 128;  // 64 numbers of 128 rows
 constexpr uint32_t kKBlk = kKeys * 128;
 constexpr float kGrow = 8.0f;            // log2 by which a maximum may grow without rescaling
@@ -51,9 +57,9 @@ struct FwdMaps {
 struct FwdSmem {
     alignas(1024) unsigned char q[kTiles][3 * kQBlk];
     alignas(1024) unsigned char k[2][3 * kKBlk];
-    alignas(1024) unsigned char v[2][2 * kKBlk];
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], v_tail;
-    uint64_t s_full[kTiles], p_full[kTiles], pv_done[kTiles];
+    alignas(1024) unsigned char v[kV][2 * kKBlk];
+    uint64_t q_full, k_full[2], k_empty[2], v_full[kV], v_empty[kV], v_tail;
+    uint64_t s_full[kTiles], s_read[kTiles], p_full[kTiles], pv_done[kTiles];
     uint32_t tmem_slot;
     int64_t find[40];
 };
@@ -77,11 +83,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 1);
             mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < kV; ++i) {
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.pv_done[i], 1);
+        }
+        for (int t = 0; t < kTiles; ++t) {
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.s_read[t], 4);
+            mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.pv_done[t], 1);
         }
         fence_mbar_init_cluster();
     }
@@ -124,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < kTiles; ++t)
                     tma_load_4d(sm.q[t], &maps.q, 0, q0 + i0 + t * kRows, h, 0, &sm.q_full);
             }
-            for (int j = 0; j < n_steps && !wait.dead; ++j) {
+            Ring<kV> rv;
+            for (int j = 0; j < n_steps && !wait.dead; ++j, rv.step()) {
                 const int s = j & 1, key = k0 + j * kKeys, live = lk - j * kKeys;
                 if (j >= 2)
                     wait(&sm.k_empty[s], (j / 2 - 1) & 1);
@@ -133,77 +145,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_4d(sm.k[s], &maps.kv, 0, key, h, 0, &sm.k_full[s]);
                     tma_load_2d(sm.k[s] + 2 * kKBlk, &maps.kr, 0, key, &sm.k_full[s]);
                 }
-                if (j >= 2)
-                    wait(&sm.v_empty[s], (j / 2 - 1) & 1);
-                uint64_t *bar = live < kKeys ? &sm.v_tail : &sm.v_full[s];
+                if (rv.round > 0)
+                    wait(&sm.v_empty[rv.slot], (rv.round - 1) & 1);
+                uint64_t *bar = live < kKeys ? &sm.v_tail : &sm.v_full[rv.slot];
                 if (!wait.dead && elect()) {
                     mbar_arrive_expect_tx(bar, 2 * kKBlk);
-                    tma_load_4d(sm.v[s], &maps.kv, 0, key, h, 2, bar);
+                    tma_load_4d(sm.v[rv.slot], &maps.kv, 0, key, h, 2, bar);
                 }
                 if (live < kKeys) {
                     // rows behind the sequence's end may hold anything (0 * NaN): zeros for O
                     wait(&sm.v_tail, 0);
                     for (int i = lane; i < (kKeys - live) * 16; i += 32)
-                        *reinterpret_cast<uint4 *>(sm.v[s] + (i & 8 ? kKBlk : 0) + (live + i / 16) * 128 + (i & 7) * 16) =
+                        *reinterpret_cast<uint4 *>(sm.v[rv.slot] + (i & 8 ? kKBlk : 0) + (live + i / 16) * 128 + (i & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (elect())
-                        mbar_arrive(&sm.v_full[s]);
+                        mbar_arrive(&sm.v_full[rv.slot]);
                 }
             }
         }
     } else if (warp == 9) {
-        // ---------------- products
-        constexpr uint32_t id_s = tc::idesc_bf16(kRows, kKeys, false, false), id_o = tc::idesc_bf16(kRows, kDV, false, true);
-        const Desc qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128), kd(smem_u32(sm.k[0]), 16, 1024, tc::kSw128),
-            vd(smem_u32(sm.v[0]), kKBlk, 1024, tc::kSw128);
-        auto scores = [&](int t, int j) {
-            if (elect()) {
-#pragma unroll
-                for (int ks = 0; ks < kDQ / 16; ++ks)
-                    tc::mma_bf16(tmem + t * 128, qd.at(t * 3 * kQBlk + (ks >> 2) * kQBlk + (ks & 3) * 32),
-                                 kd.at((j & 1) * 3 * kKBlk + (ks >> 2) * kKBlk + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
-                tc::commit(&sm.s_full[t]);
-            }
-        };
-        if (n_steps > 0) {
+        // ---------------- S, as soon as the tile's threads have read the one before
+        constexpr uint32_t id = tc::idesc_bf16(kRows, kKeys, false, false);
+        const Desc qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128), kd(smem_u32(sm.k[0]), 16, 1024, tc::kSw128);
+        if (n_steps > 0)
             wait(&sm.q_full, 0);
-            wait(&sm.k_full[0], 0);
-            tc::fence_after_sync();
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                if (steps[t] > 0)
-                    scores(t, 0);
-            if (elect())
-                tc::commit(&sm.k_empty[0]);
-        }
         for (int j = 0; j < n_steps && !wait.dead; ++j) {
-            const int s = j & 1;
-            wait(&sm.v_full[s], (j / 2) & 1);
-            if (j + 1 < n_steps)
-                wait(&sm.k_full[s ^ 1], ((j + 1) / 2) & 1);
+            wait(&sm.k_full[j & 1], (j / 2) & 1);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                if (j < steps[t]) {
-                    wait(&sm.p_full[t], j & 1);
-                    tc::fence_after_sync();
-                    if (elect()) {
+                if (j >= steps[t])
+                    continue;
+                if (j > 0)
+                    wait(&sm.s_read[t], (j - 1) & 1);
+                tc::fence_after_sync();
+                if (elect()) {
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            tc::mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8,
-                                            vd.at(s * 2 * kKBlk + ks * 2048), id_o, j > 0 || ks > 0 ? 1u : 0u);
-                        tc::commit(&sm.pv_done[t]);
-                    }
+                    for (int ks = 0; ks < kDQ / 16; ++ks)
+                        tc::mma_bf16(tmem + t * 128, qd.at(t * 3 * kQBlk + (ks >> 2) * kQBlk + (ks & 3) * 32),
+                                     kd.at((j & 1) * 3 * kKBlk + (ks >> 2) * kKBlk + (ks & 3) * 32), id, ks > 0 ? 1u : 0u);
+                    tc::commit(&sm.s_full[t]);
                 }
-                if (t == kTiles - 1 && elect())
-                    tc::commit(&sm.v_empty[s]);
-                // S takes the place of the P that the products just issued read: they run in order
-                if (j + 1 < steps[t])
-                    scores(t, j + 1);
             }
-            if (j + 1 < n_steps && elect())
-                tc::commit(&sm.k_empty[s ^ 1]);
+            if (elect())
+                tc::commit(&sm.k_empty[j & 1]);
+        }
+    } else if (warp == 10) {
+        // ---------------- O
+        constexpr uint32_t id = tc::idesc_bf16(kRows, kDV, false, true);
+        const Desc vd(smem_u32(sm.v[0]), kKBlk, 1024, tc::kSw128);
+        Ring<kV> rv;
+        for (int j = 0; j < n_steps && !wait.dead; ++j, rv.step()) {
+            wait(&sm.v_full[rv.slot], rv.round & 1);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (j >= steps[t])
+                    continue;
+                wait(&sm.p_full[t], j & 1);
+                tc::fence_after_sync();
+                if (elect()) {
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        tc::mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + kP + ks * 8,
+                                        vd.at(rv.slot * 2 * kKBlk + ks * 2048), id, j > 0 || ks > 0 ? 1u : 0u);
+                    tc::commit(&sm.pv_done[t]);
+                }
+            }
+            if (elect())
+                tc::commit(&sm.v_empty[rv.slot]);
         }
     } else {
         // ---------------- softmax: one row a thread
@@ -216,26 +226,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < n; ++j) {
             wait(&sm.s_full[t], j & 1);
             tc::fence_after_sync();
-            uint32_t x[3][32];
-#pragma unroll
-            for (int c = 0; c < 3; ++c)
-                tc::ld_32x32b_x32(s_addr + c * 32, x[c]);
+            uint32_t x[kKeys];
+            tc::ld_32x32b_x32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(x));
+            tc::ld_32x32b_x32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+            tc::ld_32x32b_x16(s_addr + 64, *reinterpret_cast<uint32_t(*)[16]>(x + 64));
             tc::wait_ld();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.s_read[t]);
             if ((j + 1) * kKeys - 1 > last_0) {
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    const uint32_t seen = bit_span(0, last + 1 - j * kKeys - c * 32);
+                for (int c = 0; c < kKeys; c += 32) {
+                    const uint32_t seen = bit_span(0, last + 1 - j * kKeys - c);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[c][i] = seen >> i & 1 ? x[c][i] : __float_as_uint(-INFINITY);
+                    for (int i = 0; i < 32 && c + i < kKeys; ++i)
+                        x[c + i] = seen >> i & 1 ? x[c + i] : __float_as_uint(-INFINITY);
                 }
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[c][i]));
+            for (int i = 0; i < kKeys; ++i)
+                mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
             const bool grow = top > m + kGrow;
             if (__any_sync(0xffffffffu, grow)) {
@@ -259,20 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float sub = m == -INFINITY ? 0.0f : m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t p[48];
+            uint32_t p[kKeys / 2];
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float e0 = ex2(fmaf(__uint_as_float(x[c][i]), a.scale_log2, -sub));
-                    const float e1 = ex2(fmaf(__uint_as_float(x[c][i + 1]), a.scale_log2, -sub));
-                    sum[i & 2] += e0;
-                    sum[(i & 2) + 1] += e1;
-                    p[c * 16 + i / 2] = pack_bf16x2(e0, e1);
-                }
+            for (int i = 0; i < kKeys; i += 2) {
+                const float e0 = ex2(fmaf(__uint_as_float(x[i]), a.scale_log2, -sub));
+                const float e1 = ex2(fmaf(__uint_as_float(x[i + 1]), a.scale_log2, -sub));
+                sum[i & 2] += e0;
+                sum[(i & 2) + 1] += e1;
+                p[i / 2] = pack_bf16x2(e0, e1);
+            }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tc::st_32x32b_x32(s_addr, *reinterpret_cast<const uint32_t(*)[32]>(p));
-            tc::st_32x32b_x16(s_addr + 32, *reinterpret_cast<const uint32_t(*)[16]>(p + 32));
+            if (j > 0) {
+                wait(&sm.pv_done[t], (j - 1) & 1);  // P's place has been read
+                tc::fence_after_sync();
+            }
+            tc::st_32x32b_x32(s_addr + kP, *reinterpret_cast<const uint32_t(*)[32]>(p));
+            tc::st_32x32b_x8(s_addr + kP + 32, *reinterpret_cast<const uint32_t(*)[8]>(p + 32));
             tc::wait_st();
             tc::fence_before_sync();
             __syncwarp();
