@@ -7,6 +7,9 @@
 // decides it and no two CTAs write the same page.  A thread keeps one 16-byte column of eight rows
 // (64 rows over 576 threads) in registers between the maximum and the rounding; longer pages read
 // the rest again, from L2.  Two CTAs an SM keep 147 KB in flight.
+// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 33-37 us (3.2 TB/s; the chain of
+// lookups, rows, maximum and stores of a page, four pages an SM one after the other); one row for
+// each of 256 sequences 8.2 us, most of it the launch.
 #include <cuda_fp8.h>
 
 #include "mla_common.cuh"

@@ -32,11 +32,19 @@
 // their log-sum-exp in the workspace, which a second launch joins in order (equal calls give
 // equal bits; the shares depend on the lengths and the SM count alone).
 //
+// Measured (one launch and its join, inputs larger than L2): 256 sequences of 3000 to 5000 rows, 32
+// heads: bfloat16 210-220 us, 5.5 TB/s; e4m3 147-155 us, 4.0 TB/s.  A tile of 64 e4m3 rows takes
+// 1450 cycles: 666 of S^T and 464 of O^T products (both bound by shared memory), the softmax's chain
+// of waits and stores next to them; in a loop the 1000 W limit holds the clock near 1.45 GHz, and
+// alone the call takes 128 us.  23 ragged sequences up to 40000 rows, 2 tokens each: 128-132 us.
+// Also measured, and slower: prefetching tiles into L2 ahead of the copies (249 and 203 us for the
+// two batches), fetching the next S^T while the weights are stored (220 and 155, ragged 135).
+//
 // Warps: 0-3 and 8-11 softmax, half the columns each (S^T in the 16-lane M = 64 layout, running
 // maximum per column, O^T in tensor memory rescaled only when a column's maximum grows by more than
-// 2^8, which float32 sums and a bfloat16 weight hold exactly as well); 4 copies (TMA: half a tile of
-// bfloat16 rows or a whole one of codes at a time); 5 issues S^T; 6 issues O^T and frees the rows;
-// 7 loads Q.
+// 2^8, which float32 sums and a bfloat16 weight hold exactly as well); 4 and 7 copies, every other
+// tile each (TMA: half a tile of bfloat16 rows or a whole one of codes at a time); 5 loads Q and
+// issues S^T; 6 issues O^T and frees the rows.
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
