@@ -4,12 +4,14 @@
 // Bound by bytes: a new row is read once (1152 B) and written once (1152 or 576 B); a page that
 // held earlier rows and whose scale grows is read and written once more.  One CTA takes one
 // (page that receives rows, group): the page is where the scale lives, so one CTA sees all that
-// decides it and no two CTAs write the same page.  A thread keeps one 16-byte column of eight rows
-// (64 rows over 576 threads) in registers between the maximum and the rounding; longer pages read
-// the rest again, from L2.  Two CTAs an SM keep 147 KB in flight.
-// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 33-37 us (3.2 TB/s; the chain of
-// lookups, rows, maximum and stores of a page, four pages an SM one after the other); one row for
-// each of 256 sequences 8.2 us, most of it the launch.
+// decides it and no two CTAs write the same page.  Up to 64 new rows are copied to shared memory
+// (bulk copies) and read there twice, for the maximum and for the rounding; longer pages read the
+// rest from global memory, the second time from L2.  Three CTAs an SM, so that some wait for rows
+// while others round theirs; nine warps each (eighteen: 33 us for the 29 below; rows held in
+// registers, two CTAs an SM: 37).
+// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 29 us (4.1 TB/s; a page is 8 us of
+// lookups, rows, maximum and stores), into a bfloat16 one 39 us (4.0 TB/s); one row for each of 256
+// sequences 8.2 us, most of it the launch.
 #include <cuda_fp8.h>
 
 #include "mla_common.cuh"
@@ -21,9 +23,10 @@ namespace {
 using namespace mla;
 
 constexpr int kVecs = kDC / 8;  // 16-byte vectors of a bfloat16 row
-constexpr int kPass = 8;        // rows the CTA takes at once
+constexpr int kPass = 4;        // rows the CTA takes at once
 constexpr int kThreads = kPass * kVecs;
-constexpr int kKeep = 8;        // passes held in registers: 64 rows
+constexpr int kStaged = 64;     // rows in shared memory
+constexpr int kBatch = 6;       // passes of earlier rows in flight
 
 struct AppendArgs {
     int N, T_new, G, max_pages, num_pages, page_size;
@@ -34,15 +37,12 @@ struct AppendArgs {
     unsigned int *status;
 };
 
-__device__ __forceinline__ uint32_t amax8(uint4 v)
+// The larger of m and the eight |x|, two halves of a word each, compared as integers: NaN is above
+// infinity, which is above all.
+__device__ __forceinline__ uint32_t amax8(uint32_t m, uint4 v)
 {
-    // |x| of two bfloat16 a word, compared as integers: NaN is above infinity, which is above all
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-    return m;
+    constexpr uint32_t k = 0x7fff7fffu;
+    return __vimax3_s16x2(__vimax3_s16x2(m, v.x & k, v.y & k), v.z & k, v.w & k);
 }
 
 // Two floats to two e4m3 codes, to nearest even (saturating; the caller's scale leaves |x| <= 448).
@@ -84,11 +84,17 @@ __device__ __forceinline__ float scale_for(uint32_t b)
 }
 
 template <bool kE4M3>
-__global__ void __launch_bounds__(kThreads, 2) mla_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 3) mla_append_kernel(AppendArgs a)
 {
+    extern __shared__ __align__(16) unsigned char staged_rows[];
     __shared__ int64_t sh[40];
     __shared__ uint32_t s_max[kThreads / 32];
+    __shared__ uint64_t landed;
     const int tid = threadIdx.x, ps = a.page_size;
+    if (kE4M3 && tid == 0) {
+        mbar_init(&landed, 1);
+        fence_mbar_init_cluster();
+    }
     // sequence n touches the pages of its places [len, len + new rows)
     const Item it = find_item<kThreads>(
         a.N, blockIdx.x,
@@ -119,28 +125,39 @@ __global__ void __launch_bounds__(kThreads, 2) mla_append_kernel(AppendArgs a)
     const int64_t row0 = ((int64_t)page * ps + slot0 + r0) * a.G + g;
     if constexpr (!kE4M3) {
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + row0 * kDC) + vec;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i * kPass + r0 < rows; ++i)
             dst[i * step] = src[i * step];
         return;
     }
-    uint4 keep[kKeep];
+    const int staged = min(rows, kStaged);
+    if (tid < 32) {
+        if (tid == 0)
+            mbar_arrive_expect_tx(&landed, staged * kDC * 2);
+        __syncwarp();
+        const __nv_bfloat16 *x = a.x + ((a.cu[n] + first) * a.G + g) * kDC;
+        if (a.G == 1) {
+            if (tid == 0)
+                bulk_g2s(staged_rows, x, staged * kDC * 2, &landed);
+        } else {
+            for (int i = tid; i < staged; i += 32)
+                bulk_g2s(staged_rows + i * kDC * 2, x + (int64_t)i * a.G * kDC, kDC * 2, &landed);
+        }
+    }
+    float *sp = a.cache_scale + (int64_t)page * a.G + g;
+    const float old = slot0 > 0 ? *sp : 0.0f;  // read by all before one thread writes it (barrier between)
     uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i)
-        if (i * kPass + r0 < rows)
-            keep[i] = src[i * step];
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i)
-        if (i * kPass + r0 < rows)
-            mx = max(mx, amax8(keep[i]));
-    for (int i = kKeep; i * kPass + r0 < rows; ++i)
-        mx = max(mx, amax8(src[i * step]));
+    for (int r = kStaged + r0; r < rows; r += kPass)
+        mx = amax8(mx, src[(int64_t)(r - r0) * a.G * kVecs]);
+    mbar_wait_bounded(&landed, 0, a.status);
+    const uint4 *held_new = reinterpret_cast<const uint4 *>(staged_rows) + tid;
+#pragma unroll 4
+    for (int i = 0; i * kPass + r0 < staged; ++i)
+        mx = amax8(mx, held_new[i * kThreads]);
+    mx = max(mx & 0xffffu, mx >> 16) << 16;  // the bits of a float32
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((tid & 31) == 0)
         s_max[tid >> 5] = mx;
-    float *sp = a.cache_scale + (int64_t)page * a.G + g;
-    const float old = slot0 > 0 ? *sp : 0.0f;  // read by all before one thread writes it (barrier between)
     __syncthreads();
     mx = 0;
 #pragma unroll
@@ -155,26 +172,27 @@ __global__ void __launch_bounds__(kThreads, 2) mla_append_kernel(AppendArgs a)
     if (slot0 > 0 && !(now == old)) {  // earlier rows of the page, at the larger scale
         const float f = old / now;
         unsigned char *held = codes + (((int64_t)page * ps + r0) * a.G + g) * kDC + vec * 8;
-        for (int i0 = 0; i0 * kPass + r0 < slot0; i0 += kKeep) {
-            uint2 u[kKeep];
+        for (int i0 = 0; i0 * kPass + r0 < slot0; i0 += kBatch) {
+            uint2 u[kBatch];
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i)
+            for (int i = 0; i < kBatch; ++i)
                 if ((i0 + i) * kPass + r0 < slot0)
                     u[i] = *reinterpret_cast<const uint2 *>(held + (i0 + i) * step * 8);
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i)
+            for (int i = 0; i < kBatch; ++i)
                 if ((i0 + i) * kPass + r0 < slot0)
                     *reinterpret_cast<uint2 *>(held + (i0 + i) * step * 8) = make_uint2(rescale4(u[i].x, f), rescale4(u[i].y, f));
         }
     }
     const float inv = 1.0f / now;  // exact: a power of two from 2^-100 to 2^120
     unsigned char *dst = codes + row0 * kDC + vec * 8;
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i)
-        if (i * kPass + r0 < rows)
-            *reinterpret_cast<uint2 *>(dst + i * step * 8) = quantise8(keep[i], inv);
-    for (int i = kKeep; i * kPass + r0 < rows; ++i)
-        *reinterpret_cast<uint2 *>(dst + i * step * 8) = quantise8(src[i * step], inv);
+#pragma unroll 4
+    for (int i = 0; i * kPass + r0 < staged; ++i)
+        *reinterpret_cast<uint2 *>(dst + i * step * 8) = quantise8(held_new[i * kThreads], inv);
+    for (int r = kStaged + r0; r < rows; r += kPass) {
+        const int64_t at = (int64_t)(r - r0) * a.G * kVecs;
+        *reinterpret_cast<uint2 *>(dst + at * 8) = quantise8(src[at], inv);
+    }
 }
 
 }  // namespace
@@ -190,7 +208,15 @@ cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, co
     // a sequence of m > 0 rows touches at most (m - 1) / page_size + 2 pages, and no more than m
     const int64_t most = (int64_t)T_new / page_size + 2 * (int64_t)N;
     const dim3 grid((unsigned)(most < T_new ? most : T_new), G);
-    (e4m3 ? mla_append_kernel<true> : mla_append_kernel<false>)<<<grid, kThreads, 0, s>>>(a);
+    if (e4m3) {
+        const int smem = kStaged * kDC * 2;
+        const cudaError_t e = cudaFuncSetAttribute(mla_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+        mla_append_kernel<true><<<grid, kThreads, smem, s>>>(a);
+    } else {
+        mla_append_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 
