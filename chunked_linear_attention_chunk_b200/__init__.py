@@ -610,8 +610,12 @@ def _mla_call(name, dev, *args):
 
 
 def _out(t, shape, dtype, dev, name):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+    if t is None:  # (empty_strided takes two thirds of empty's time)
+        stride, n = [], 1
+        for d in reversed(shape):
+            stride.append(n)
+            n *= d
+        return torch.empty_strided(shape, stride[::-1], dtype=dtype, device=dev)
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
     return t

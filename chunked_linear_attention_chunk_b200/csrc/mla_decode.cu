@@ -173,6 +173,9 @@ __device__ __forceinline__ uint32_t terms2(float2 x)
 // with an infinity or a NaN gets a NaN for its scale.
 __global__ void __launch_bounds__(256) mla_split_q_kernel(DecArgs a, int64_t rows)
 {
+    // the launches before this one are over; the next one may start (it reads what they wrote, and
+    // waits before it reads the terms)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -263,6 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = tid - 160, cg = ct * NC + c;
         sm.row[c] = cg / Hg * a.H + cg % Hg;
     }
+    if (!kE4M3)  // the launches before this one are over (e4m3: they were before the terms' launch went on)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     // this CTA's share: all tiles, then the unit that its first one falls in
     {
         int64_t mine = 0;
@@ -888,6 +893,7 @@ template <int NC, int kP>
 __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
 {
     __shared__ __align__(16) float wgt[kJoinShares][4];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, c0 = blockIdx.y * 4, pair0 = blockIdx.z * kP;
     const int4 mt = a.meta[blockIdx.x];
@@ -995,6 +1001,7 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.stream = s;
     cfg.attrs = &attr;
+    cfg.numAttrs = 1;  // every launch sets up while the one before it ends, and waits for it on the device
     if constexpr (kE4M3) {
         const int64_t extent[4] = {128, rows, 2, 4}, stride[3] = {kDC, rows * kDC, 128};
         const int box[4] = {128, maps.q_rows, all ? 2 : 1, all ? 4 : 1};
@@ -1003,10 +1010,10 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
         if ((e = make_map(&maps.q, a.q_terms, 1, 4, extent, stride, box)) != cudaSuccess ||
             (e = make_map(&maps.q_rope, a.q_terms + kDL, 1, 3, rope, stride, rope_box)) != cudaSuccess)
             return e;
-        mla_split_q_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, rows);
-        if ((e = cudaGetLastError()) != cudaSuccess)
+        cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+        cfg.blockDim = dim3(256);
+        if ((e = cudaLaunchKernelEx(&cfg, mla_split_q_kernel, a, rows)) != cudaSuccess)
             return e;
-        cfg.numAttrs = 1;  // set up while the terms are written
     } else {
         const int64_t extent[3] = {64, rows, kDC / 64}, stride[2] = {kDC * 2, 128};
         const int box[3] = {64, maps.q_rows, all ? kDC / 64 : 1};
@@ -1018,13 +1025,11 @@ cudaError_t launch_nc(DecMaps &maps, const DecArgs &a, cudaStream_t s)
     cfg.dynamicSmemBytes = smem;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, maps, a)) != cudaSuccess)
         return e;
-    // the join waits on the device for the launch before it to end, and is set up meanwhile
     // (few units: each is cut into many shares, and a thread takes one pair of blocks of them)
     const bool few = (int64_t)a.N * a.G * 16 <= a.shares;
     cfg.gridDim = dim3(a.shares * a.CT, NC / 4, few ? kPairs : 1);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
     return few ? cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC, 1>, a)
                : cudaLaunchKernelEx(&cfg, mla_decode_join_kernel<NC, kPairs>, a);
 }

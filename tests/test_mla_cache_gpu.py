@@ -113,6 +113,42 @@ def test_decode_repeatable_captured_and_on_another_stream(e4m3):
         assert torch.equal(cap[0], want[0]) and torch.equal(cap[1], want[1])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chained_steps_without_waiting(e4m3):
+    """Append, lengthen, decode, twenty times over with one workspace and in place: launches that
+    set up early see what the ones before them wrote, as with a synchronisation after each."""
+    held, new, H = [700, 5, 130], 1, 32
+    g = torch.Generator(device="cuda").manual_seed(78)
+    table, pages = table_for([n + 20 for n in held], 32, g)
+    rows = torch.randn(20, 3, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+    qs = (torch.randn(20, 3, 1, H, 576, generator=g, device="cuda") * 0.6).to(torch.bfloat16)
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    c0 = torch.randn(pages, 32, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+    ws = torch.empty(kda.kda_mla_decode_workspace(3, 1, H, 1), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        cache, sc = c0.clone(), None
+        if e4m3:
+            sc = torch.full((pages, 1), 2.0 ** -6, device="cuda")
+            cache = (c0.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+        lens = torch.tensor(held, dtype=torch.int32, device="cuda")
+        q, got = torch.empty_like(qs[0]), []
+        torch.cuda.synchronize()
+        for i in range(20):
+            kda.kda_mla_cache_append(rows[i], cu, lens, table, cache, cache_scale=sc)
+            lens += 1
+            q.copy_(qs[i])
+            for _ in range(2):
+                got.append(kda.kda_mla_decode(q, cache, table, lens, cache_scale=sc, workspace=ws))
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_two_decodes_at_once():
     """Calls on two streams with a workspace each."""
     a = make([2000, 90], 1, 16, 1, 64, False, seed=72)
