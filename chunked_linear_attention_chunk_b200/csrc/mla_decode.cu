@@ -19,9 +19,9 @@
 // their row's largest keep an absolute 2^-23 of it), so the terms are further columns of the
 // product and S^T stays as exact as float32 sums are.
 // A weight times its page's scale is brought into range by a running maximum of its own for each
-// column, over score + log2(scale) (2^7 to 2^15 at the maximum), and split into three e5m2 terms of
-// three bits each at one common scale: nine bits (a bfloat16 weight has eight) down to 2^-23 of the
-// maximum, and 2^-31 of it at worst.  At 32 columns the terms are 96 columns of one product, added
+// column, over score + log2(scale) (2^11 to 2^15 at the maximum), and split into three e5m2 terms of
+// three bits each at one common scale: nine bits (a bfloat16 weight has eight) down to 2^-19 of the
+// maximum, and 2^-28 of it at worst.  At 32 columns the terms are 96 columns of one product, added
 // up at the end; at 64, where tensor memory has no room for that, three products into one sum.
 // Turning the codes into f16 rows in shared memory instead costs its bandwidth: 64 KB written and
 // read again a tile, 190 us where this takes 165 (256 sequences of 3000 to 5000 rows, 32 heads).
@@ -62,7 +62,11 @@ constexpr int kTok = 64;                    // cached rows a tile
 constexpr uint32_t kBlk = kTok * 128;       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kPairs = kDL / 128;           // 128 latent numbers: the M of one O^T product
 constexpr float kGrow = 8.0f;               // log2 by which a maximum may grow without rescaling
-constexpr float kLift = 7.0f;               // e4m3: log2 of a weight at its maximum
+// e4m3: log2 of a weight (times its page's scale) at its maximum, and by how much that may grow: up
+// to 2^15 in all, below e5m2's largest.  A weight's last place is 2^-27 of the maximum, so a
+// million of them in one CTA's share are off by 2^-8 of it together; 13 and 2 rescale O^T so often
+// that the batch below takes 159 us for 151, and 7 and 8 lose long tails of small weights.
+constexpr float kLift = 11.0f, kGrowO = 4.0f;
 
 struct DecArgs {
     int N, Sq, H, G, num_pages, page_size, max_pages, CT, shares;
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (t * kTok + r0 + 8 > last)
                                 s[j][2 + i] = -INFINITY;
                         }
-                        const float most = (kE4M3 ? fminf(m[k], mo[k] - lg) : m[k]) + kGrow;
+                        const float most = kE4M3 ? fminf(m[k] + kGrow, mo[k] - lg + kGrowO) : m[k] + kGrow;
                         grow |= s[j][i] > most || s[j][2 + i] > most;
                     }
                 if (softmax_or(group, grow)) {

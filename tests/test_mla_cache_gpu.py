@@ -189,6 +189,34 @@ def test_decode_long_tail_of_small_weights(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_very_long_tail(e4m3):
+    """A row and 384000 rows behind it (sixty pages over and over) of weight 2^-20.5 of its: a fifth
+    of the sum.  As many sequences as SMs, so that each is one CTA's."""
+    H, ps, times = 2, 64, 100
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    q, c, sc, table, _ = make([61 * ps], 1, H, 1, ps, e4m3, seed=79)
+    c = c.float().abs().to(c.dtype)  # errors of equal weights add up
+    c[:, :, :, 512:] = 0.0
+    c[int(table[0, 60]), :, 0, :512] = 0.0
+    c[int(table[0, 60]), 17, 0, 512:] = 8.0
+    if e4m3:
+        sc[:] = 2.0 ** -3
+    q[..., :512] = 0.0
+    q[..., 512:] = 0.25
+    table = torch.cat([table[:, 60:], table[:, :60].repeat(1, times)], 1).contiguous()
+    L = table.shape[1] * ps
+    scale = 20.5 * math.log(2) / (64 * 0.25 * (1.0 if e4m3 else 8.0))
+    o, lse = kda.kda_mla_decode(q.expand(n, -1, -1, -1).contiguous(), c, table.expand(n, -1).contiguous(),
+                                torch.full((n,), L, dtype=torch.int32, device="cuda"), scale=scale, cache_scale=sc)
+    assert torch.equal(o, o[:1].expand_as(o))
+    ro, rl, mag = ref.decode(q, c, sc, table, [L], scale)
+    # SLACK counts sums of 576 products; the sum of 384000 weights, 64 at a time in float32, is off by
+    # at most 6000 * 2^-24 of itself
+    ref.close(o[:1], ro, mag + mag * 2 ** 8 * 6000 * 2.0 ** -24, "o")
+    ref.lse_close(lse[:1], rl, 32.0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_decode_reads_a_page_twice_and_no_rows_at_all(e4m3):
     q, c, sc, table, kv_lens = make([256, 130], 1, 16, 1, 64, e4m3, seed=76)
     table[1, 1] = table[1, 0]
