@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -583,14 +584,14 @@ def _mla_expanded(q, kv, k_rope, cu_q, cu_k, scale):
 # tensors, raw pointers, and the device made current only where it is not.
 def _mla_device(*ts):
     """The device that all tensors (None aside) are on; they must be contiguous CUDA tensors."""
-    dev = ts[0].device
+    index = ts[0].get_device()
     for t in ts:
-        if t is not None and not (t.is_contiguous() and t.device == dev):
+        if t is not None and not (t.get_device() == index and t.is_contiguous()):
             _check_cuda(t)
             raise ValueError("all tensors must be on one device")
-    if dev.type != "cuda":
+    if not ts[0].is_cuda:
         raise ValueError("libkda takes CUDA tensors only")
-    return dev
+    return ts[0].device
 
 
 def _adr(t):
@@ -609,13 +610,14 @@ def _mla_call(name, dev, *args):
         raise KdaError(st, name)
 
 
+@functools.lru_cache(maxsize=1024)
+def _strides(shape):
+    return tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
+
+
 def _out(t, shape, dtype, dev, name):
     if t is None:  # (empty_strided takes two thirds of empty's time)
-        stride, n = [], 1
-        for d in reversed(shape):
-            stride.append(n)
-            n *= d
-        return torch.empty_strided(shape, stride[::-1], dtype=dtype, device=dev)
+        return torch.empty_strided(shape, _strides(shape), dtype=dtype, device=dev)
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
     return t
