@@ -131,10 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- copies
         if (n_steps > 0) {
             if (elect()) {
-                mbar_arrive_expect_tx(&sm.q_full, kTiles * 3 * kQBlk);
+                mbar_arrive_expect_tx(&sm.q_full, ((steps[0] > 0) + (steps[1] > 0)) * 3 * kQBlk);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
-                    tma_load_4d(sm.q[t], &maps.q, 0, q0 + i0 + t * kRows, h, 0, &sm.q_full);
+                    if (steps[t] > 0)
+                        tma_load_4d(sm.q[t], &maps.q, 0, q0 + i0 + t * kRows, h, 0, &sm.q_full);
             }
             Ring<kV> rv;
             for (int j = 0; j < n_steps && !wait.dead; ++j, rv.step()) {
@@ -301,8 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) {
             wait(&sm.pv_done[t], (n - 1) & 1);
             tc::fence_after_sync();
-        } else if (n_steps > 0) {
-            wait(&sm.q_full, 0);  // the copy of a Q that nothing reads
         }
         const int tr = tid & (kRows - 1);
 #pragma unroll 1
