@@ -24,7 +24,7 @@
 // maximum, and 2^-28 of it at worst.  At 32 columns the terms are 96 columns of one product, added
 // up at the end; at 64, where tensor memory has no room for that, three products into one sum.
 // Turning the codes into f16 rows in shared memory instead costs its bandwidth: 64 KB written and
-// read again a tile, 190 us where this takes 165 (256 sequences of 3000 to 5000 rows, 32 heads).
+// read again a tile, 190 us where this took 165 (256 sequences of 3000 to 5000 rows, 32 heads).
 //
 // One persistent CTA per SM takes an equal share of all 64-row tiles of all (sequence, group)
 // units in order, so a batch of any lengths is balanced without the host knowing them.  A unit
@@ -33,12 +33,13 @@
 // equal bits; the shares depend on the lengths and the SM count alone).
 //
 // Measured (one launch and its join, inputs larger than L2): 256 sequences of 3000 to 5000 rows, 32
-// heads: bfloat16 210-220 us, 5.5 TB/s; e4m3 147-155 us, 4.0 TB/s.  A tile of 64 e4m3 rows takes
+// heads: bfloat16 210-220 us, 5.5 TB/s; e4m3 143-156 us, 4.0 TB/s.  A tile of 64 e4m3 rows takes
 // 1450 cycles: 666 of S^T and 464 of O^T products (both bound by shared memory), the softmax's chain
 // of waits and stores next to them; in a loop the 1000 W limit holds the clock near 1.45 GHz, and
 // alone the call takes 128 us.  23 ragged sequences up to 40000 rows, 2 tokens each: 128-132 us.
 // Also measured, and slower: prefetching tiles into L2 ahead of the copies (249 and 203 us for the
-// two batches), fetching the next S^T while the weights are stored (220 and 155, ragged 135).
+// two batches), fetching the next S^T while the weights are stored (220 and 155, ragged 135), half
+// tiles of codes as places, nine for the eight there are (154.7 for 152.4).
 //
 // Warps: 0-3 and 8-11 softmax, half the columns each (S^T in the 16-lane M = 64 layout, running
 // maximum per column, O^T in tensor memory rescaled only when a column's maximum grows by more than
