@@ -66,7 +66,7 @@ constexpr float kGrow = 8.0f;               // log2 by which a maximum may grow 
 // e4m3: log2 of a weight (times its page's scale) at its maximum, and by how much that may grow: up
 // to 2^15 in all, below e5m2's largest.  A weight's last place is 2^-27 of the maximum, so a
 // million of them in one CTA's share are off by 2^-8 of it together; 13 and 2 rescale O^T so often
-// that the batch below takes 159 us for 151, and 7 and 8 lose long tails of small weights.
+// that the 8-bit batch above takes 159 us for 151, and 7 and 8 lose long tails of small weights.
 constexpr float kLift = 11.0f, kGrowO = 4.0f;
 
 struct DecArgs {
@@ -1053,8 +1053,8 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
     DecArgs a{N, Sq, H, G, num_pages, page_size, max_pages, p.ct, p.shares, scale * kLog2e,
               static_cast<const __nv_bfloat16 *>(q), cache_scale, block_table, kv_lens,
               static_cast<__nv_bfloat16 *>(o), lse, reinterpret_cast<float *>(ws + p.part_o),
-              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int4 *>(ws), ws + p.q_terms, reinterpret_cast<float *>(ws + p.q_scale),
-              device_status_ptr()};
+              reinterpret_cast<float *>(ws + p.part_lse), reinterpret_cast<int4 *>(ws), ws + p.q_terms,
+              reinterpret_cast<float *>(ws + p.q_scale), device_status_ptr()};
     if (!a.status)
         return cudaErrorInvalidDevice;
     DecMaps maps{};

@@ -71,12 +71,6 @@ __device__ __forceinline__ bool elect()
     return r != 0;
 }
 
-// A warpgroup's share of the registers that the block was launched with.
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-
 // Shared-memory descriptors as a constant upper word (strides, swizzle) and a lower word that
 // steps with the address (`lo` + bytes / 16).
 struct Desc {

@@ -50,12 +50,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
-// f16 x f16 -> f32.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn)
-{
-    return idesc_bf16(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10));  // A and B formats: f16 (0)
-}
-
 // The same for kind::f8f6f4 with both operands e4m3, K-major (K = 32 codes an instruction).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
 {

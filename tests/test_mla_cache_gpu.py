@@ -126,27 +126,40 @@ def test_chained_steps_without_waiting(e4m3):
     c0 = torch.randn(pages, 32, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
     ws = torch.empty(kda.kda_mla_decode_workspace(3, 1, H, 1), dtype=torch.uint8, device="cuda")
 
+    cache, sc = c0.clone(), None
+    if e4m3:
+        c0 = (c0.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+        cache, sc = c0.clone(), torch.empty((pages, 1), device="cuda")
+    lens0 = torch.tensor(held, dtype=torch.int32, device="cuda")
+    lens, q = lens0.clone(), torch.empty_like(qs[0])
+
     def run(wait):
-        cache, sc = c0.clone(), None
+        got = []
+        cache.copy_(c0)
+        lens.copy_(lens0)
         if e4m3:
-            sc = torch.full((pages, 1), 2.0 ** -6, device="cuda")
-            cache = (c0.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
-        lens = torch.tensor(held, dtype=torch.int32, device="cuda")
-        q, got = torch.empty_like(qs[0]), []
-        torch.cuda.synchronize()
+            sc.fill_(2.0 ** -6)
         for i in range(20):
             kda.kda_mla_cache_append(rows[i], cu, lens, table, cache, cache_scale=sc)
-            lens += 1
+            lens.add_(1)
             q.copy_(qs[i])
             for _ in range(2):
                 got.append(kda.kda_mla_decode(q, cache, table, lens, cache_scale=sc, workspace=ws))
                 if wait:
                     torch.cuda.synchronize()
-        torch.cuda.synchronize()
         return got
 
-    for a, b in zip(run(False), run(True)):
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    want = run(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run(False)
+    graph.replay()
+    graph.replay()
+    for got in (run(False), captured):
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert kda.kda_device_status() == 0
 
 
 def test_two_decodes_at_once():
