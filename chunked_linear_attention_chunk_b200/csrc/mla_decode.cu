@@ -21,8 +21,8 @@
 // A weight times its page's scale is brought into range by a running maximum of its own for each
 // column, over score + log2(scale) (2^11 to 2^15 at the maximum), and split into three e5m2 terms of
 // three bits each at one common scale: nine bits (a bfloat16 weight has eight) down to 2^-19 of the
-// maximum, and 2^-28 of it at worst.  At 32 columns the terms are 96 columns of one product, added
-// up at the end; at 64, where tensor memory has no room for that, three products into one sum.
+// maximum, and 2^-28 of it at worst.  Up to 32 columns the terms are three times as many columns of
+// one product, added up at the end; at 64, where tensor memory has no room for that, three products into one sum.
 // Turning the codes into f16 rows in shared memory instead costs its bandwidth: 64 KB written and
 // read again a tile, 190 us where this took 165 (256 sequences of 3000 to 5000 rows, 32 heads).
 //
@@ -135,15 +135,16 @@ struct DecSmem {
     // bfloat16: half tiles and rope blocks in flight; e4m3: tiles of codes
     static constexpr int kRing = kE4M3 ? 1 : (NC == 64 ? 4 : 5);
     static constexpr int kRopes = kE4M3 || NC == 64 ? 1 : 2;
-    static constexpr int kStage = kE4M3 ? (NC == 64 ? 3 : 4) : 1;
+    static constexpr int kStage = kE4M3 ? (NC == 64 ? 3 : NC == 32 ? 4 : 5) : 1;
     static constexpr uint32_t kSlot = kE4M3 ? 16 : 4 * kBlk;
+    static_assert(kRing <= 4 * kRopes, "a warp that waits for a rope place knows the round before the last consumed");
     static constexpr uint32_t kCodes = 4 * kBlk + kBlk / 2;  // a tile of codes: 4 x 128, then 64
     static constexpr int kSW = kE4M3 ? 2 * NC : NC;          // columns of S^T
     static constexpr int kPB = NC == 64 && !kE4M3 ? 1 : 2;   // buffers of P^T (one where a second has no room)
-    static constexpr uint32_t kP = kTok * NC * (kE4M3 ? 3 : 2);  // bytes of one
+    static constexpr uint32_t kP = kTok * kPRow<NC, kE4M3> * (kE4M3 && NC > 16 ? 3 : 1);  // bytes of one
     // parts of O^T: a weight's three terms side by side where tensor memory has the room, one sum of
     // their three products where it has not
-    static constexpr int kParts = kE4M3 && NC == 32 ? 3 : 1;
+    static constexpr int kParts = kE4M3 && NC <= 32 ? 3 : 1;
     alignas(1024) unsigned char ring[kRing][kSlot];
     alignas(1024) unsigned char rope[kRopes][kE4M3 ? 16 : kBlk];
     // bfloat16: [9 blocks][NC rows][128 B]; e4m3: [4 blocks][2 NC rows][128 B], [2 NC rows][64 B]
@@ -574,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 2 * kTurns; ++k)
                                 tc::mma_f8(tmem + kColO + j * SM::kParts * NC, cd.at(c0 + j * kBlk + (k & 1) * 4096),
-                                           pd.at(p0 + (k >> 1) * kTok * NC + (k & 1) * 32 * NC), id, t > 0 || k > 0 ? 1u : 0u);
+                                           pd.at(p0 + (k >> 1) * kTok * NC + (k & 1) * 32 * kPRow<NC, true>), id,
+                                           t > 0 || k > 0 ? 1u : 0u);
                         tc::commit(&sm.empty_stage[rst.slot]);
                         tc::commit(&sm.pv_done[rb.slot]);
                     }
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16 (warp % 4) + lane / 4 (+ 8), the group's columns 8 j + 2 (lane % 4) (+ 1)
         if (kE4M3)  // q's row scales
             asm volatile("griddepcontrol.wait;" ::: "memory");
-        constexpr int kCols = NC / 2, J = kCols / 8;
+        constexpr int kCols = NC / 2, J = kCols / 8, kCh = kCols < 16 ? kCols : 16;  // kCh: columns of O^T at once
         const int group = warp >> 3, quarter = warp & 3, gtid = quarter * 32 + lane, r0 = quarter * 16 + (lane >> 2);
         const uint32_t lane_base = tc::taddr(tmem, (uint32_t)quarter * 32, 0) + group * kCols;
         auto col = [&](int i) { return group * kCols + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
@@ -712,16 +714,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pv_wait(nt - 1);  // O^T of the tiles so far is complete
                         tc::fence_after_sync();
 #pragma unroll 1
-                        for (int b = 0; b < kPairs * SM::kParts * kCols / 16; ++b) {
-                            const int c0 = b * 16 % kCols;
-                            const uint32_t at = lane_base + kColO + b * 16 / kCols * NC + c0;
-                            uint32_t y[16];
-                            tc::ld_32x32b_x16(at, y);
+                        for (int b = 0; b < kPairs * SM::kParts * kCols / kCh; ++b) {
+                            const int c0 = b * kCh % kCols;
+                            const uint32_t at = lane_base + kColO + b * kCh / kCols * NC + c0;
+                            uint32_t y[kCh];
+                            load_row<kCh>(at, y);
                             tc::wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
+                            for (int i = 0; i < kCh; ++i)
                                 y[i] = __float_as_uint(__uint_as_float(y[i]) * sm.fac[group * kCols + c0 + i]);
-                            tc::st_32x32b_x16(at, y);
+                            store_row<kCh>(at, y);
                         }
                         tc::wait_st();
                     }
@@ -755,13 +757,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 h[i] = __hsub2(h[i], *reinterpret_cast<const __half2 *>(&u[i]));
                             }
                             const uint32_t v = __byte_perm(u[0], u[1], 0x7531);
-                            *reinterpret_cast<uint16_t *>(pt + k * kTok * NC + p_off<NC, true>(r0, c)) = (uint16_t)v;
-                            *reinterpret_cast<uint16_t *>(pt + k * kTok * NC + p_off<NC, true>(r0 + 8, c)) =
-                                (uint16_t)(v >> 16);
+                            *reinterpret_cast<uint16_t *>(pt + p_off<NC, true>(r0, c, k)) = (uint16_t)v;
+                            *reinterpret_cast<uint16_t *>(pt + p_off<NC, true>(r0 + 8, c, k)) = (uint16_t)(v >> 16);
                         }
                     } else {
-                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0, c)) = pack_bf16x2(s[j][0], s[j][1]);
-                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0 + 8, c)) = pack_bf16x2(s[j][2], s[j][3]);
+                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0, c, 0)) = pack_bf16x2(s[j][0], s[j][1]);
+                        *reinterpret_cast<uint32_t *>(pt + p_off<NC, false>(r0 + 8, c, 0)) = pack_bf16x2(s[j][2], s[j][3]);
                     }
                 }
                 // rows behind the sequence's end may hold anything (0 * NaN): zeros for O^T
@@ -836,20 +837,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             const int dim = gtid, live = cols - ct * NC;
 #pragma unroll 1
-            for (int b = 0; b < kPairs * kCols / 16; ++b) {
-                const int pair = b * 16 / kCols, c0 = group * kCols + b * 16 % kCols;
-                const uint32_t at = lane_base + kColO + pair * SM::kParts * NC + b * 16 % kCols;
-                uint32_t y[SM::kParts][16];
+            for (int b = 0; b < kPairs * kCols / kCh; ++b) {
+                const int pair = b * kCh / kCols, c0 = group * kCols + b * kCh % kCols;
+                const uint32_t at = lane_base + kColO + pair * SM::kParts * NC + b * kCh % kCols;
+                uint32_t y[SM::kParts][kCh];
 #pragma unroll
                 for (int i = 0; i < SM::kParts; ++i)
-                    tc::ld_32x32b_x16(at + i * NC, y[i]);
-                float f[16];
+                    load_row<kCh>(at + i * NC, y[i]);
+                float f[kCh];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
+                for (int i = 0; i < kCh; i += 4)
                     *reinterpret_cast<float4 *>(f + i) = *reinterpret_cast<const float4 *>(sm.fac + c0 + i);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < kCh; ++i)
                 {
                     float x = __uint_as_float(y[0][i]);
 #pragma unroll
@@ -860,13 +861,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!whole) {
                     float *dst = a.part_o + ((slot * kPairs + pair) * (NC / 4) + c0 / 4) * 512 + dim * 4;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
+                    for (int i = 0; i < kCh; i += 4)
                         *reinterpret_cast<float4 *>(dst + i * 128) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
                 } else {
                     // a lane and its neighbour trade columns, so that each writes two numbers at once
                     __nv_bfloat16 *dst = a.o + row0 * kDL + pair * 128 + (dim & ~1);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
+                    for (int i = 0; i < kCh; i += 2) {
                         const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? f[i] : f[i + 1], 1);
                         const uint32_t v = lane & 1 ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
                         const int c = c0 + i + (lane & 1);
@@ -963,7 +964,14 @@ __global__ void __launch_bounds__(128) mla_decode_join_kernel(DecArgs a)
     }
 }
 
-int columns(int Sq, int H, int G) { return Sq * (H / G) <= 32 ? 32 : 64; }
+// Columns of a CTA.  Half as many cost less than half as much (products of 32 columns take 45 cycles
+// and of 16 about as long), but leave room for more rows in flight and shorten the softmax: 16
+// heads in 16 columns 124 us for 145 in 32 over the 8-bit batch, 205 for 214 over the bfloat16 one.
+int columns(int Sq, int H, int G)
+{
+    const int n = Sq * (H / G);
+    return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+}
 
 struct DecPlan {
     int nc, ct, shares;
@@ -1072,8 +1080,12 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
     if (e != cudaSuccess)
         return e;
     if (e4m3)
-        return p.nc == 32 ? launch_nc<32, true>(maps, a, s) : launch_nc<64, true>(maps, a, s);
-    return p.nc == 32 ? launch_nc<32, false>(maps, a, s) : launch_nc<64, false>(maps, a, s);
+        return p.nc == 16   ? launch_nc<16, true>(maps, a, s)
+               : p.nc == 32 ? launch_nc<32, true>(maps, a, s)
+                            : launch_nc<64, true>(maps, a, s);
+    return p.nc == 16   ? launch_nc<16, false>(maps, a, s)
+           : p.nc == 32 ? launch_nc<32, false>(maps, a, s)
+                        : launch_nc<64, false>(maps, a, s);
 }
 
 }  // namespace kda

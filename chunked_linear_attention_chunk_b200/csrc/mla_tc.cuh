@@ -129,32 +129,45 @@ __device__ __forceinline__ bool softmax_or(int group, bool x)
     return r != 0;
 }
 
-// P^T of the decode, MN-major with the swizzle of its row length: [64 rows][NC columns] bfloat16,
-// or three terms of [64 rows][NC columns] e5m2 one behind the other.
+// P^T of the decode, MN-major with the swizzle of its row length: [64 rows][NC columns] bfloat16, or
+// three terms of [64 rows][NC columns] e5m2 one behind the other (16 columns: side by side in rows of
+// 64 bytes).
 template <int NC, bool k8>
-__device__ __forceinline__ uint32_t p_off(int row, int col)
+constexpr uint32_t kPRow = k8 ? (NC == 16 ? 64 : NC) : 2 * NC;  // bytes of a row
+template <int NC, bool k8>
+__device__ __forceinline__ uint32_t p_off(int row, int col, int term)
 {
-    if (k8)
-        return row * NC + (((col >> 4) ^ (NC == 64 ? row >> 1 & 3 : row >> 2 & 1)) << 4) + (col & 15);
+    if (k8) {
+        if (NC == 16)
+            return row * 64 + ((term ^ (row >> 1 & 3)) << 4) + col;
+        return (term * 64 + row) * NC + (((col >> 4) ^ (NC == 64 ? row >> 1 & 3 : row >> 2 & 1)) << 4) + (col & 15);
+    }
+    if (NC == 16)
+        return row * 32 + (((col >> 3) ^ (row >> 2 & 1)) << 4) + (col & 7) * 2;
     return NC == 64 ? tc::mnmaj_sw128(row, col, 64) : tc::mnmaj_sw64(row, col);
 }
 template <int NC, bool k8>
 __device__ __forceinline__ Desc p_desc(uint32_t base)
 {
-    if (k8)  // at 32 columns the terms are the next 32-column atoms of one operand
-        return NC == 64 ? Desc(base, 64 * 64, 512, tc::kSw64) : Desc(base, 64 * 32, 256, tc::kSw32);
-    return NC == 64 ? Desc(base, 64 * 128, 1024, tc::kSw128) : Desc(base, 0, 512, tc::kSw64);
+    if (k8 && NC == 32)  // the terms are the next 32-column atoms of one operand
+        return Desc(base, 64 * 32, 256, tc::kSw32);
+    if (k8)
+        return Desc(base, 0, 512, tc::kSw64);
+    return NC == 64 ? Desc(base, 64 * 128, 1024, tc::kSw128)
+                    : NC == 32 ? Desc(base, 0, 512, tc::kSw64) : Desc(base, 0, 256, tc::kSw32);
 }
 
-// 16 or 32 columns of an M = 64 accumulator in fragment order (see ld_16x256b_x2).
+// 8, 16 or 32 columns of an M = 64 accumulator in fragment order (see ld_16x256b_x1).
 template <int kCols>
 __device__ __forceinline__ void load_s(uint32_t taddr, float (&s)[kCols / 8][4])
 {
     uint32_t r[kCols / 2];
     if constexpr (kCols == 32)
         tc::ld_16x256b_x4(taddr, r);
-    else
+    else if constexpr (kCols == 16)
         tc::ld_16x256b_x2(taddr, r);
+    else
+        tc::ld_16x256b_x1(taddr, r);
     tc::wait_ld();
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i)
@@ -171,6 +184,24 @@ __device__ __forceinline__ void load_s2(uint32_t taddr, uint32_t apart, float (&
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i)
         s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 0.0625f, s[i / 4][i % 4]);
+}
+
+// 8 or 16 columns of this thread's lane.
+template <int kCols>
+__device__ __forceinline__ void load_row(uint32_t taddr, uint32_t (&r)[kCols])
+{
+    if constexpr (kCols == 16)
+        tc::ld_32x32b_x16(taddr, r);
+    else
+        tc::ld_32x32b_x8(taddr, r);
+}
+template <int kCols>
+__device__ __forceinline__ void store_row(uint32_t taddr, const uint32_t (&r)[kCols])
+{
+    if constexpr (kCols == 16)
+        tc::st_32x32b_x16(taddr, r);
+    else
+        tc::st_32x32b_x8(taddr, r);
 }
 
 // A kernel's tensor map (a __grid_constant__ argument) into the descriptor cache.

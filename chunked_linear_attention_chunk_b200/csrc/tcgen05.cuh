@@ -145,6 +145,15 @@ __device__ __forceinline__ void ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32])
         : "memory");
 }
 
+// The warp's quarter of the lanes, one each, x 8 columns.
+__device__ __forceinline__ void ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // 16 consecutive columns of this thread's lane.
 __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
 {
@@ -157,9 +166,18 @@ __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
-// Lanes 0..15 of the warp's quarter (an M = 64 accumulator's 16 rows) x 16 columns, in the
+// Lanes 0..15 of the warp's quarter (an M = 64 accumulator's 16 rows) x 8 columns, in the
 // fragment order of a 16 x 8 tile: r[4 j + 0, 1] are columns 8 j + 2 (lane % 4) + 0, 1 of row
 // lane / 4, r[4 j + 2, 3] the same columns of row lane / 4 + 8.
+__device__ __forceinline__ void ld_16x256b_x1(uint32_t taddr, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// The same over 16 columns.
 __device__ __forceinline__ void ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
