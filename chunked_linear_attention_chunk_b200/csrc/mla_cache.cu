@@ -25,6 +25,7 @@ using namespace mla;
 constexpr int kVecs = kDC / 8;  // 16-byte vectors of a bfloat16 row
 constexpr int kPass = 4;        // rows the CTA takes at once
 constexpr int kThreads = kPass * kVecs;
+constexpr int kCopyThreads = 96;  // of a CTA that only looks up and copies (bfloat16)
 constexpr int kStaged = 64;     // rows in shared memory
 constexpr int kBatch = 6;       // passes of earlier rows in flight
 
@@ -84,19 +85,19 @@ __device__ __forceinline__ float scale_for(uint32_t b)
 }
 
 template <bool kE4M3>
-__global__ void __launch_bounds__(kThreads, 3) mla_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 3) mla_append_kernel(AppendArgs a)
 {
     extern __shared__ __align__(16) unsigned char staged_rows[];
     __shared__ int64_t sh[40];
     __shared__ uint32_t s_max[kThreads / 32];
     __shared__ uint64_t landed;
     const int tid = threadIdx.x, ps = a.page_size;
-    if (kE4M3 && tid == 0) {
+    if (tid == 0) {
         mbar_init(&landed, 1);
         fence_mbar_init_cluster();
     }
     // sequence n touches the pages of its places [len, len + new rows)
-    const Item it = find_item<kThreads>(
+    const Item it = find_item<kE4M3 ? kThreads : kCopyThreads>(
         a.N, blockIdx.x,
         [&](int n, bool &bad) {
             const int m = span_of(a.cu, n, a.T_new, bad).len(), len = a.kv_lens[n];
@@ -123,27 +124,45 @@ __global__ void __launch_bounds__(kThreads, 3) mla_append_kernel(AppendArgs a)
     const uint4 *src = reinterpret_cast<const uint4 *>(a.x + ((a.cu[n] + first + r0) * a.G + g) * kDC) + vec;
     const int64_t step = (int64_t)kPass * a.G * kVecs;  // vectors from a pass to the next
     const int64_t row0 = ((int64_t)page * ps + slot0 + r0) * a.G + g;
-    if constexpr (!kE4M3) {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.cache) + row0 * kDC) + vec;
-#pragma unroll 8
-        for (int i = 0; i * kPass + r0 < rows; ++i)
-            dst[i * step] = src[i * step];
+    // rows [r, r + count) of the new ones to shared memory, by the first warp
+    const __nv_bfloat16 *x = a.x + ((a.cu[n] + first) * a.G + g) * kDC;
+    auto fetch = [&](int r, int count) {
+        if (tid == 0)
+            mbar_arrive_expect_tx(&landed, count * kDC * 2);
+        __syncwarp();
+        if (a.G == 1) {
+            if (tid == 0)
+                bulk_g2s(staged_rows, x + (int64_t)r * kDC, count * kDC * 2, &landed);
+        } else {
+            for (int i = tid; i < count; i += 32)
+                bulk_g2s(staged_rows + i * kDC * 2, x + (int64_t)(r + i) * a.G * kDC, kDC * 2, &landed);
+        }
+    };
+    if constexpr (!kE4M3) {  // and from there to the cache
+        if (tid >= 32)
+            return;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.cache) + (((int64_t)page * ps + slot0) * a.G + g) * kDC;
+        for (int r = 0, k = 0; r < rows; r += kStaged, ++k) {
+            const int count = min(rows - r, kStaged);
+            fetch(r, count);
+            if (!mbar_wait_bounded(&landed, k & 1, a.status))
+                return;
+            if (a.G == 1) {
+                if (tid == 0)
+                    bulk_s2g(dst + (int64_t)r * kDC, staged_rows, count * kDC * 2);
+            } else {
+                for (int i = tid; i < count; i += 32)
+                    bulk_s2g(dst + (int64_t)(r + i) * a.G * kDC, staged_rows + i * kDC * 2, kDC * 2);
+            }
+            bulk_commit();
+            bulk_wait_all();  // also before the CTA's shared memory goes
+            __syncwarp();
+        }
         return;
     }
     const int staged = min(rows, kStaged);
-    if (tid < 32) {
-        if (tid == 0)
-            mbar_arrive_expect_tx(&landed, staged * kDC * 2);
-        __syncwarp();
-        const __nv_bfloat16 *x = a.x + ((a.cu[n] + first) * a.G + g) * kDC;
-        if (a.G == 1) {
-            if (tid == 0)
-                bulk_g2s(staged_rows, x, staged * kDC * 2, &landed);
-        } else {
-            for (int i = tid; i < staged; i += 32)
-                bulk_g2s(staged_rows + i * kDC * 2, x + (int64_t)i * a.G * kDC, kDC * 2, &landed);
-        }
-    }
+    if (tid < 32)
+        fetch(0, staged);
     float *sp = a.cache_scale + (int64_t)page * a.G + g;
     const float old = slot0 > 0 ? *sp : 0.0f;  // read by all before one thread writes it (barrier between)
     uint32_t mx = 0;
@@ -208,15 +227,12 @@ cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, co
     // a sequence of m > 0 rows touches at most (m - 1) / page_size + 2 pages, and no more than m
     const int64_t most = (int64_t)T_new / page_size + 2 * (int64_t)N;
     const dim3 grid((unsigned)(most < T_new ? most : T_new), G);
-    if (e4m3) {
-        const int smem = kStaged * kDC * 2;
-        const cudaError_t e = cudaFuncSetAttribute(mla_append_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-        mla_append_kernel<true><<<grid, kThreads, smem, s>>>(a);
-    } else {
-        mla_append_kernel<false><<<grid, kThreads, 0, s>>>(a);
-    }
+    auto kernel = e4m3 ? mla_append_kernel<true> : mla_append_kernel<false>;
+    const int smem = (page_size < kStaged ? page_size : kStaged) * kDC * 2;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    kernel<<<grid, e4m3 ? kThreads : kCopyThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
