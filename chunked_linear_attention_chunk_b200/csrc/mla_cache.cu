@@ -4,14 +4,14 @@
 // Bound by bytes: a new row is read once (1152 B) and written once (1152 or 576 B); a page that
 // held earlier rows and whose scale grows is read and written once more.  One CTA takes one
 // (page that receives rows, group): the page is where the scale lives, so one CTA sees all that
-// decides it and no two CTAs write the same page.  Up to 64 new rows are copied to shared memory
-// (bulk copies) and read there twice, for the maximum and for the rounding; longer pages read the
-// rest from global memory, the second time from L2.  Three CTAs an SM, so that some wait for rows
-// while others round theirs; nine warps each (eighteen: 33 us for the 29 below; rows held in
-// registers, two CTAs an SM: 37).
-// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 29 us (4.1 TB/s; a page is 8 us of
-// lookups, rows, maximum and stores), into a bfloat16 one 39 us (4.0 TB/s); one row for each of 256
-// sequences 6 us, most of it the launch.
+// decides it and no two CTAs write the same page.  Up to 64 new rows at a time come to shared memory
+// by bulk copies.  bfloat16 rows leave it the same way.  For codes they are read there twice, for
+// the maximum and for the rounding; longer pages read the rest from global memory, the second time
+// from L2.  Three CTAs an SM (more for smaller pages), so that some wait for rows while others round
+// theirs; nine warps each (eighteen: 33 us for the 27 below; rows held in registers, two CTAs an SM: 37).
+// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 27 us (4.3 TB/s; a page is 8 us of
+// lookups, rows, maximum and stores; 38 us with pages of 16), into a bfloat16 one 32 us (4.9 TB/s);
+// one row for each of 256 sequences 6 us, most of it the launch.
 #include <cuda_fp8.h>
 
 #include "mla_common.cuh"
@@ -85,7 +85,7 @@ __device__ __forceinline__ float scale_for(uint32_t b)
 }
 
 template <bool kE4M3>
-__global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 3) mla_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append_kernel(AppendArgs a)
 {
     extern __shared__ __align__(16) unsigned char staged_rows[];
     __shared__ int64_t sh[40];
