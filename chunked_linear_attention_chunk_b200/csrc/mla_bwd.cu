@@ -507,8 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[k] = seen >> k & 1 ? p[k] : 0.0f;
             }
             if (kKeys) {
+                // p's place is free: the sum of the step before has read it, or, in the first step,
+                // the warps that take v from there (S is issued without them) have their rows
                 if (i > 0)
                     wait(&sm.acc2_done[set ^ 1], ((i - 1) >> 1) & 1);
+                else
+                    wait(&sm.x_full, 0);
                 store_32(sm.p, r, half * 4, p);
                 fence_proxy_async_smem();
                 arrive(&sm.p_full[set]);

@@ -248,3 +248,28 @@ def test_no_rows():
     got = kda.kda_mla_bwd(x["q"], x["kv"], x["kr"], o, lse, x["dO"], x["cu_q"], x["cu_k"])
     assert (got["dq"] == 0).all()
     assert kda.kda_device_status() == 0
+
+
+def test_bwd_first_step_takes_no_place_early():
+    """The first step's weights share their place in shared memory with v on its way to tensor
+    memory.  Many tiles of one to three steps, beside another stream's work on the same memory
+    system: equal bits every time, and every tile against 64 bits."""
+    lens = [(37 * i) % 190 + 1 for i in range(60)]
+    x, cq, ck = make(lens, lens, 4, seed=52)
+    o, lse = kda.kda_mla_fwd(x["q"], x["kv"], x["kr"], x["cu_q"], x["cu_k"])
+    args = (x["q"], x["kv"], x["kr"], o, lse, x["dO"], x["cu_q"], x["cu_k"])
+    first = kda.kda_mla_bwd(*args)
+    for name, (r, m) in ref.bwd(x["q"], x["kv"], x["kr"], o, lse, x["dO"], cq, ck, 192 ** -0.5, True).items():
+        ref.close(first[name], r, m, name)
+    a = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    b = torch.empty_like(a)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                b.copy_(a)
+        got = [kda.kda_mla_bwd(*args) for _ in range(20)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g[n], first[n]) for g in got for n in first)
+    assert kda.kda_device_status() == 0
