@@ -229,7 +229,9 @@ cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, co
     const dim3 grid((unsigned)(most < T_new ? most : T_new), G);
     auto kernel = e4m3 ? mla_append_kernel<true> : mla_append_kernel<false>;
     const int smem = (page_size < kStaged ? page_size : kStaged) * kDC * 2;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the limit is the kernel's, shared by all host threads: the same one whatever this call's pages)
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStaged * kDC * 2);
     if (e != cudaSuccess)
         return e;
     kernel<<<grid, e4m3 ? kThreads : kCopyThreads, smem, s>>>(a);

@@ -360,6 +360,45 @@ def test_append_extremes():
     assert math.isnan(float(sc[3, 0])) and float(sc[5, 0]) == 1.0
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_appends_from_threads_with_pages_of_several_sizes(e4m3):
+    """Host threads that fill caches of different page sizes at once: every call is launched, and
+    every cache holds its rows."""
+    import threading
+    g = torch.Generator(device="cuda").manual_seed(82)
+    errors, made = [], []
+    for ps in (16, 64, 32, 128):
+        rows = torch.randn(ps, 1, 576, generator=g, device="cuda").to(torch.bfloat16)
+        cache = torch.zeros(1, ps, 1, 576, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16, device="cuda")
+        sc = torch.zeros(1, 1, device="cuda") if e4m3 else None
+        ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, ps], [0], [[0]])]
+        made.append((ps, rows, cache, sc, ints))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(made), timeout=60)
+
+    def body(ps, rows, cache, sc, ints):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for _ in range(4000):
+                    kda.kda_mla_cache_append(rows, ints[0], ints[1], ints[2], cache, cache_scale=sc)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below, in the test's own thread)
+            errors.append((ps, e))
+
+    threads = [threading.Thread(target=body, args=m) for m in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert kda.kda_device_status() == 0
+    for ps, rows, cache, sc, ints in made:
+        want_c, want_s = torch.zeros_like(cache, device="cpu"), None if sc is None else torch.zeros(1, 1)
+        ref.append(rows.cpu(), [0, ps], [0], ints[2].cpu(), want_c, want_s)
+        assert torch.equal(cache.cpu().view(torch.uint8), want_c.view(torch.uint8))
+
+
 def test_append_refuses_bad_tables():
     ps = 64
     g = torch.Generator(device="cuda").manual_seed(81)
