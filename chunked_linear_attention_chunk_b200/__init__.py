@@ -57,6 +57,7 @@ EXPORTS = (
     "kda_chunk_fwd_prep",
     "kda_chunk_fwd_scan",
     "kda_selftest_device_timeout",
+    "kda_selftest_append_timeout",
     "kda_chunk_fwd_varlen_workspace",
     "kda_chunk_fwd_varlen",
     "kda_gate_fwd_heads",
@@ -163,6 +164,8 @@ def lib() -> ctypes.CDLL:
     L.kda_mla_decode.restype = I
     L.kda_mla_cache_append.argtypes = [I, P, I, I, I, I, I, P, P, P, I, I, P, P, I, I, P]
     L.kda_mla_cache_append.restype = I
+    L.kda_selftest_append_timeout.argtypes = [ctypes.c_uint32, *L.kda_mla_cache_append.argtypes]
+    L.kda_selftest_append_timeout.restype = I
     _lib = L
     return L
 
@@ -750,6 +753,17 @@ def kda_selftest_device_timeout(limit_us: int = 20000, device=None) -> None:
     ``limit_us`` and records KDA_ERR_DEVICE_TIMEOUT (read it with kda_device_status)."""
     dev = device if device is not None else torch.cuda.current_device()
     _raise(lib().kda_selftest_device_timeout(int(limit_us), _stream(dev)), "kda_selftest_device_timeout")
+
+
+def kda_selftest_append_timeout(limit_us, kv_new, cu_new, kv_lens, block_table, cache, cache_scale=None) -> None:
+    """``kda_mla_cache_append`` whose new rows never land: the waits run out after ``limit_us`` and
+    record KDA_ERR_DEVICE_TIMEOUT; cache and cache_scale stay as they are."""
+    dev = _mla_device(kv_new, cu_new, kv_lens, block_table, cache, cache_scale)
+    code, (P, ps, G, dc), (N, pages) = _mla_cache(cache, cache_scale, block_table, kv_lens)
+    if kv_new.dtype != _BF16 or cu_new.dtype != _I32 or kv_new.shape[1:] != (G, dc) or cu_new.shape != (N + 1,):
+        raise ValueError("kv_new must be bfloat16 [T_new,G,576], cu_new int32 [N+1]")
+    _mla_call("kda_selftest_append_timeout", dev, int(limit_us), N, _adr(cu_new), kv_new.shape[0], G, *MLA_CACHE_DIMS,
+              KDA_BF16, _adr(kv_new), _adr(kv_lens), _adr(block_table), pages, code, _adr(cache), _adr(cache_scale), P, ps)
 
 
 def kda_status_string(status: int) -> str:

@@ -95,7 +95,8 @@ cudaError_t launch_decode(int N, int H, int D, kda_dtype dt, const void *q, cons
                           const void *a, const void *beta, float g_min, float *S, void *o, cudaStream_t s);
 
 // Latent attention.  Expanded form over packed sequences (head dims 128 + 64 and 128): forward
-// and gradients; absorbed form over a paged cache of 512 + 64 numbers a row; writing that cache.
+// and gradients; absorbed form over a paged cache of 512 + 64 numbers a row; writing that cache
+// (late_us > 0: the self-test, whose rows never land and whose waits last that long).
 cudaError_t launch_mla_fwd(int N, const int32_t *cu_q, const int32_t *cu_k, int Tq, int Tk, int H, bool causal,
                            float scale, const void *q, const void *kv, const void *k_rope, void *o, float *lse,
                            cudaStream_t s);
@@ -111,6 +112,6 @@ cudaError_t launch_mla_decode(int N, int Sq, int H, int G, float scale, const vo
                               cudaStream_t s);
 cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, const void *kv_new,
                               const int32_t *kv_lens, const int32_t *block_table, int max_pages, bool e4m3, void *cache,
-                              float *cache_scale, int num_pages, int page_size, cudaStream_t s);
+                              float *cache_scale, int num_pages, int page_size, uint32_t late_us, cudaStream_t s);
 
 }  // namespace kda

@@ -66,6 +66,38 @@ kda_status check_cache(int N, int G, int dl, int dr, kda_dtype dtype, kda_dtype 
     return KDA_OK;
 }
 
+kda_status append(uint32_t late_us, int N, const int32_t *cu_new, int T_new, int G, int dl, int dr, kda_dtype dtype,
+                  const void *kv_new, const int32_t *kv_lens, const int32_t *block_table, int max_pages,
+                  kda_dtype cache_dtype, void *cache, float *cache_scale, int num_pages, int page_size,
+                  kda_stream_t stream)
+{
+    if (T_new < 0 || !cu_new)
+        return KDA_ERR_INVALID_ARG;
+    const kda_status st = check_cache(N, G, dl, dr, dtype, cache_dtype, cache, cache_scale, num_pages, page_size,
+                                      block_table, max_pages, kv_lens);
+    if (st != KDA_OK)
+        return st;
+    if (T_new > kMaxPackedTokens || safe_prod({T_new, G, dl + dr}) < 0)
+        return KDA_ERR_UNSUPPORTED;
+    if (T_new == 0)
+        return KDA_OK;
+    if (!kv_new)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(kv_new) || !aligned4(cu_new))
+        return KDA_ERR_ALIGNMENT;
+    const int64_t row = (dl + dr) * (cache_dtype == KDA_BF16 ? 2 : 1);
+    if (any_alias({{kv_new, (int64_t)T_new * G * (dl + dr) * 2, false},
+                   {cu_new, (N + 1) * 4ll, false},
+                   {block_table, (int64_t)N * max_pages * 4, false},
+                   {kv_lens, N * 4ll, false},
+                   {cache, (int64_t)num_pages * page_size * G * row, true},
+                   {cache_scale, cache_scale ? (int64_t)num_pages * G * 4 : 0, true}}))
+        return KDA_ERR_ALIAS;
+    return from_cuda(launch_mla_append(N, cu_new, T_new, G, kv_new, kv_lens, block_table, max_pages,
+                                       cache_dtype == KDA_E4M3, cache, cache_scale, num_pages, page_size, late_us,
+                                       (cudaStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -194,31 +226,19 @@ kda_status kda_mla_cache_append(int N, const int32_t *cu_new, int T_new, int G, 
                                 kda_dtype cache_dtype, void *cache, float *cache_scale, int num_pages, int page_size,
                                 kda_stream_t stream)
 {
-    if (T_new < 0 || !cu_new)
+    return append(0, N, cu_new, T_new, G, dl, dr, dtype, kv_new, kv_lens, block_table, max_pages, cache_dtype, cache,
+                  cache_scale, num_pages, page_size, stream);
+}
+
+kda_status kda_selftest_append_timeout(uint32_t limit_us, int N, const int32_t *cu_new, int T_new, int G, int dl, int dr,
+                                       kda_dtype dtype, const void *kv_new, const int32_t *kv_lens,
+                                       const int32_t *block_table, int max_pages, kda_dtype cache_dtype, void *cache,
+                                       float *cache_scale, int num_pages, int page_size, kda_stream_t stream)
+{
+    if (limit_us < 1 || limit_us > 2000000u)
         return KDA_ERR_INVALID_ARG;
-    const kda_status st = check_cache(N, G, dl, dr, dtype, cache_dtype, cache, cache_scale, num_pages, page_size,
-                                      block_table, max_pages, kv_lens);
-    if (st != KDA_OK)
-        return st;
-    if (T_new > kMaxPackedTokens || safe_prod({T_new, G, dl + dr}) < 0)
-        return KDA_ERR_UNSUPPORTED;
-    if (T_new == 0)
-        return KDA_OK;
-    if (!kv_new)
-        return KDA_ERR_INVALID_ARG;
-    if (!aligned16(kv_new) || !aligned4(cu_new))
-        return KDA_ERR_ALIGNMENT;
-    const int64_t row = (dl + dr) * (cache_dtype == KDA_BF16 ? 2 : 1);
-    if (any_alias({{kv_new, (int64_t)T_new * G * (dl + dr) * 2, false},
-                   {cu_new, (N + 1) * 4ll, false},
-                   {block_table, (int64_t)N * max_pages * 4, false},
-                   {kv_lens, N * 4ll, false},
-                   {cache, (int64_t)num_pages * page_size * G * row, true},
-                   {cache_scale, cache_scale ? (int64_t)num_pages * G * 4 : 0, true}}))
-        return KDA_ERR_ALIAS;
-    return from_cuda(launch_mla_append(N, cu_new, T_new, G, kv_new, kv_lens, block_table, max_pages,
-                                       cache_dtype == KDA_E4M3, cache, cache_scale, num_pages, page_size,
-                                       (cudaStream_t)stream));
+    return append(limit_us, N, cu_new, T_new, G, dl, dr, dtype, kv_new, kv_lens, block_table, max_pages, cache_dtype,
+                  cache, cache_scale, num_pages, page_size, stream);
 }
 
 }  // extern "C"

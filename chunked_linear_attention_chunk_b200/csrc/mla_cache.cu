@@ -36,6 +36,7 @@ struct AppendArgs {
     void *cache;
     float *cache_scale;
     unsigned int *status;
+    unsigned long long limit_ns;  // kLate: how long a wait for rows lasts
 };
 
 // The larger of m and the eight |x|, two halves of a word each, compared as integers: NaN is above
@@ -84,9 +85,12 @@ __device__ __forceinline__ float scale_for(uint32_t b)
     return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
 }
 
-template <bool kE4M3>
+// kLate: the self-test of what follows when rows do not land in time (their copies are left out).
+// Nothing may be written then: the scale and the earlier rows of the page are not this call's alone.
+template <bool kE4M3, bool kLate>
 __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append_kernel(AppendArgs a)
 {
+    const unsigned long long limit = kLate ? a.limit_ns : kWaitLimitNs;
     extern __shared__ __align__(16) unsigned char staged_rows[];
     __shared__ int64_t sh[40];
     __shared__ uint32_t s_max[kThreads / 32];
@@ -130,6 +134,8 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
         if (tid == 0)
             mbar_arrive_expect_tx(&landed, count * kDC * 2);
         __syncwarp();
+        if (kLate)
+            return;
         if (a.G == 1) {
             if (tid == 0)
                 bulk_g2s(staged_rows, x + (int64_t)r * kDC, count * kDC * 2, &landed);
@@ -145,8 +151,10 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
         for (int r = 0, k = 0; r < rows; r += kStaged, ++k) {
             const int count = min(rows - r, kStaged);
             fetch(r, count);
-            if (!mbar_wait_bounded(&landed, k & 1, a.status))
+            if (!mbar_wait_bounded(&landed, k & 1, a.status, limit)) {
+                mbar_wait_bounded(&landed, k & 1, a.status, limit);  // copies on their way, before the CTA ends
                 return;
+            }
             if (a.G == 1) {
                 if (tid == 0)
                     bulk_s2g(dst + (int64_t)r * kDC, staged_rows, count * kDC * 2);
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
     uint32_t mx = 0;
     for (int r = kStaged + r0; r < rows; r += kPass)
         mx = amax8(mx, src[(int64_t)(r - r0) * a.G * kVecs]);
-    mbar_wait_bounded(&landed, 0, a.status);
+    const bool late = !mbar_wait_bounded(&landed, 0, a.status, limit);
     const uint4 *held_new = reinterpret_cast<const uint4 *>(staged_rows) + tid;
 #pragma unroll 4
     for (int i = 0; i * kPass + r0 < staged; ++i)
@@ -177,7 +185,10 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((tid & 31) == 0)
         s_max[tid >> 5] = mx;
-    __syncthreads();
+    if (__syncthreads_or(late)) {
+        mbar_wait_bounded(&landed, 0, a.status, limit);  // copies on their way, before the CTA ends
+        return;
+    }
     mx = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w)
@@ -218,16 +229,17 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
 
 cudaError_t launch_mla_append(int N, const int32_t *cu_new, int T_new, int G, const void *kv_new,
                               const int32_t *kv_lens, const int32_t *block_table, int max_pages, bool e4m3, void *cache,
-                              float *cache_scale, int num_pages, int page_size, cudaStream_t s)
+                              float *cache_scale, int num_pages, int page_size, uint32_t late_us, cudaStream_t s)
 {
     AppendArgs a{N, T_new, G, max_pages, num_pages, page_size, cu_new, kv_lens, block_table,
-                 static_cast<const __nv_bfloat16 *>(kv_new), cache, cache_scale, device_status_ptr()};
+                 static_cast<const __nv_bfloat16 *>(kv_new), cache, cache_scale, device_status_ptr(), late_us * 1000ull};
     if (!a.status)
         return cudaErrorInvalidDevice;
     // a sequence of m > 0 rows touches at most (m - 1) / page_size + 2 pages, and no more than m
     const int64_t most = (int64_t)T_new / page_size + 2 * (int64_t)N;
     const dim3 grid((unsigned)(most < T_new ? most : T_new), G);
-    auto kernel = e4m3 ? mla_append_kernel<true> : mla_append_kernel<false>;
+    auto kernel = late_us > 0 ? (e4m3 ? mla_append_kernel<true, true> : mla_append_kernel<false, true>)
+                              : (e4m3 ? mla_append_kernel<true, false> : mla_append_kernel<false, false>);
     const int smem = (page_size < kStaged ? page_size : kStaged) * kDC * 2;
     // (the limit is the kernel's, shared by all host threads: the same one whatever this call's pages)
     const cudaError_t e =

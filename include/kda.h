@@ -560,6 +560,18 @@ kda_status kda_device_status(kda_stream_t stream);
  */
 kda_status kda_selftest_device_timeout(uint32_t limit_us, kda_stream_t stream);
 
+/*
+ * kda_selftest_append_timeout -- kda_mla_cache_append on a bad day: the copies of its new rows
+ * never start, so that each CTA's wait for them runs out after `limit_us` microseconds (1 ..
+ * 2 000 000; a second wait for copies on their way lasts as long).  It records
+ * KDA_ERR_DEVICE_TIMEOUT and leaves cache and cache_scale as they were.  Other arguments, checks
+ * and errors as kda_mla_cache_append.
+ */
+kda_status kda_selftest_append_timeout(uint32_t limit_us, int N, const int32_t *cu_new, int T_new, int G, int dl, int dr,
+                                       kda_dtype dtype, const void *kv_new, const int32_t *kv_lens,
+                                       const int32_t *block_table, int max_pages, kda_dtype cache_dtype, void *cache,
+                                       float *cache_scale, int num_pages, int page_size, kda_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kda_status_string(kda_status status);
 

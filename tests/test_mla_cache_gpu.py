@@ -399,6 +399,35 @@ def test_appends_from_threads_with_pages_of_several_sizes(e4m3):
         assert torch.equal(cache.cpu().view(torch.uint8), want_c.view(torch.uint8))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_whose_rows_do_not_land_writes_nothing(e4m3):
+    """The waits run out (20 ms) and say so; cache, scales and the next call are as before."""
+    held, new, ps = [5, 0, 31, 64], [40, 100, 2, 1], 32
+    g = torch.Generator(device="cuda").manual_seed(83)
+    table, pages = table_for([a + b for a, b in zip(held, new)], ps, g)
+    cu = torch.tensor([0, 40, 140, 142, 143], dtype=torch.int32, device="cuda")
+    held_t = torch.tensor(held, dtype=torch.int32, device="cuda")
+    rows = (torch.randn(143, 2, 576, generator=g, device="cuda") * 8).to(torch.bfloat16)
+    c = torch.randn(pages, ps, 2, 576, generator=g, device="cuda").to(torch.bfloat16)
+    sc = None
+    if e4m3:
+        sc = torch.full((pages, 2), 2.0 ** -6, device="cuda")
+        c = (c.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn)
+    before_c, before_s = c.clone(), None if sc is None else sc.clone()
+    assert kda.kda_device_status() == 0
+    kda.kda_selftest_append_timeout(20000, rows, cu, held_t, table, c, cache_scale=sc)
+    assert kda.kda_device_status() == 6  # KDA_ERR_DEVICE_TIMEOUT
+    assert torch.equal(c.view(torch.uint8), before_c.view(torch.uint8))
+    assert sc is None or torch.equal(sc, before_s)
+    want_c, want_s = c.cpu().clone(), None if sc is None else sc.cpu().clone()
+    ref.append(rows.cpu(), cu.tolist(), held, table.cpu(), want_c, want_s)
+    kda.kda_mla_cache_append(rows, cu, held_t, table, c, cache_scale=sc)
+    torch.cuda.synchronize()
+    assert kda.kda_device_status() == 0
+    assert torch.equal(c.cpu().view(torch.uint8), want_c.view(torch.uint8))
+    assert sc is None or torch.equal(sc.cpu(), want_s)
+
+
 def test_append_refuses_bad_tables():
     ps = 64
     g = torch.Generator(device="cuda").manual_seed(81)

@@ -113,6 +113,14 @@ def test_append_validates(L):
         assert _app(L, **bad) == ALIAS, bad
 
 
+def test_append_selftest_validates(L):
+    for limit in (0, 2000001):
+        assert L.kda_selftest_append_timeout(limit, 3, P(0), 20, 1, 512, 64, kda.KDA_BF16, P(1), P(2), P(3), 4, kda.KDA_BF16,
+                                             P(4), None, 10, 64, None) == INVALID
+    assert L.kda_selftest_append_timeout(5, 3, P(0), 20, 1, 512, 64, kda.KDA_BF16, P(1), P(2), P(3), 4, kda.KDA_E4M3, P(4),
+                                         None, 10, 64, None) == INVALID
+
+
 def test_sizes_past_32_bits_are_refused(L):
     """More blocks than a launch takes; a sequence whose last tile would end behind 2^31 rows."""
     assert _fwd(L, N=65535, H=65535) == UNSUPPORTED
