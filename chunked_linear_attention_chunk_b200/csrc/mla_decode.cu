@@ -401,11 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the page scales come on their own (a place is free once its tile's P^T has been used)
                     if (!wait.dead && lane < 4) {
                         float *dst = &sm.scale[rst.slot][lane];
-                        if (my_page >= 0)
+                        if (my_page >= 0) {
                             cp_async_4(dst, a.cache_scale + (int64_t)my_page * a.G + w.g);
-                        else
+                            cp_async_arrive(&sm.full_scale[rst.slot]);
+                        } else {  // no page there: a plain store, which a plain arrival follows
                             *dst = 1.0f;
-                        cp_async_arrive(&sm.full_scale[rst.slot]);
+                            mbar_arrive(&sm.full_scale[rst.slot]);
+                        }
                     }
                     __syncwarp();
                 } else {

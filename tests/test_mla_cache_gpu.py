@@ -242,6 +242,25 @@ def test_decode_reads_a_page_twice_and_no_rows_at_all(e4m3):
     assert kda.kda_device_status() == 0
 
 
+@pytest.mark.parametrize("H,ps", [(16, 16), (32, 16), (64, 16), (16, 32)])
+def test_decode_scales_of_places_without_a_page(H, ps):
+    """Tiles that a sequence's pages fill only in part, each in a CTA that held a NaN page's scales
+    before: the NaN stays with its own sequence.  Twelve sequences a CTA, every other one of NaN
+    pages, the ones between of one page."""
+    n = 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    lens = [64 if i % 2 == 0 else 1 + i % ps for i in range(n)]
+    q, c, sc, table, kv_lens = make(lens, 1, H, 1, ps, True, seed=84)
+    sc[table[::2, :64 // ps].reshape(-1).long()] = math.nan
+    some = [1, 3, n // 2 + 1, n - 1]
+    for _ in range(20):
+        o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+        assert torch.isnan(o[::2]).all() and torch.isfinite(o[1::2]).all() and torch.isfinite(lse[1::2]).all()
+    ro, rl, mag = ref.decode(q[some], c, sc, table[some], [lens[i] for i in some], 192 ** -0.5)
+    ref.close(o[some], ro, mag, "o")
+    ref.lse_close(lse[some], rl, 32.0)
+    assert kda.kda_device_status() == 0
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_pool_past_32_bit_offsets(e4m3):
     """Append to and attend over the last pages of a pool of more than 2^32 bytes and numbers."""
