@@ -15,9 +15,11 @@
 // e4m3 rows: both products are taken on the codes as they lie in the cache (kind::f8f6f4), and
 // what is exact in bfloat16 becomes several 8-bit terms of the other operand.
 // Q is split into two e4m3 terms at a power-of-two scale of its own for each row, q = t (q1 + q2 /
-// 16): q1 keeps four bits and q2 the next four, which is all a bfloat16 has (numbers below 2^-15 of
-// their row's largest keep an absolute 2^-23 of it), so the terms are further columns of the
-// product and S^T stays as exact as float32 sums are.
+// 32) with the row's largest in [128 t, 256 t): q1 keeps four bits and q2 the next four, which is all
+// a bfloat16 has, so the terms are further columns of the product and S^T stays as exact as float32
+// sums are.  32 is the most that q1's rounding (up to 8 t) allows: 8 * 32 < 448.  e4m3's smallest
+// step, 2^-9, is then 2^-14 t of q, so a number keeps its eight bits from 2^-7 t up (2^-14 of the
+// row's largest at least) and is off by 2^-15 t below that (2^-22 of the largest at most).
 // A weight times its page's scale is brought into range by a running maximum of its own for each
 // column, over score + log2(scale) (2^11 to 2^15 at the maximum), and split into three e5m2 terms of
 // three bits each at one common scale: nine bits (a bfloat16 weight has eight) down to 2^-19 of the
@@ -171,7 +173,7 @@ __device__ __forceinline__ uint32_t terms2(float2 x)
     const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
     const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
     const __nv_fp8x2_storage_t b =
-        __nv_cvt_float2_to_fp8x2(make_float2((x.x - f.x) * 16.0f, (x.y - f.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+        __nv_cvt_float2_to_fp8x2(make_float2((x.x - f.x) * kTerm2, (x.y - f.y) * kTerm2), __NV_SATFINITE, __NV_E4M3);
     return (uint32_t)a | ((uint32_t)b << 16);
 }
 

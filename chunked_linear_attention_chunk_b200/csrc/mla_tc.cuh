@@ -174,7 +174,10 @@ __device__ __forceinline__ void load_s(uint32_t taddr, float (&s)[kCols / 8][4])
         s[i / 4][i % 4] = __uint_as_float(r[i]);
 }
 
-// The same and a sixteenth of the columns `apart` further on: the two terms' sum.
+// A row of q is t (q1 + q2 / kTerm2) in e4m3 terms.
+constexpr float kTerm2 = 32.0f;
+
+// The same and the columns `apart` further on, divided by kTerm2: the two terms' sum.
 template <int kCols>
 __device__ __forceinline__ void load_s2(uint32_t taddr, uint32_t apart, float (&s)[kCols / 8][4])
 {
@@ -183,7 +186,7 @@ __device__ __forceinline__ void load_s2(uint32_t taddr, uint32_t apart, float (&
     load_s<kCols>(taddr + apart, t);
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i)
-        s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 0.0625f, s[i / 4][i % 4]);
+        s[i / 4][i % 4] = fmaf(t[i / 4][i % 4], 1.0f / kTerm2, s[i / 4][i % 4]);
 }
 
 // 8 or 16 columns of this thread's lane.

@@ -410,7 +410,7 @@ kda_status kda_decode_step(int N, int H, int dk, int dv, kda_dtype dtype, const 
  * Token tensors are bfloat16; scores, softmax statistics and sums are float32.  A softmax weight is
  * rounded to bfloat16 where it enters a matrix product.  Over an 8-bit cache a weight times its
  * page's scale keeps nine bits down to 2^-19 of the largest such product (and 2^-28 of that at
- * worst), and a number of q eight bits down to 2^-15 of its row's largest (2^-24 at worst).
+ * worst), and a number of q eight bits down to 2^-14 of its row's largest (2^-22 of it at worst).
  *
  * kda_mla_fwd -- attention of packed sequences in the expanded form.  Sequence n has the queries
  * [cu_q[n], cu_q[n+1]) and the keys [cu_k[n], cu_k[n+1]) of its packed axis (cu_k beyond cu_q:

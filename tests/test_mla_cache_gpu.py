@@ -242,6 +242,37 @@ def test_decode_reads_a_page_twice_and_no_rows_at_all(e4m3):
     assert kda.kda_device_status() == 0
 
 
+@pytest.mark.parametrize("kind", ["steps", "random"])
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_decode_q_far_below_its_largest_number(kind, H):
+    """Over an 8-bit cache a number of q is off by at most 2^-22 of its row's largest.  That one
+    meets zeros here, and the others, 2^-10 to 2^-30 of it, decide the scores; all of a row's cached
+    numbers have one sign, so errors add up."""
+    L = 300
+    q, c, sc, table, kv_lens = make([L], 1, H, 1, 64, True, seed=85)
+    g = torch.Generator(device="cuda").manual_seed(86)
+    c = c.float().abs().nan_to_num(0.0).to(torch.float8_e4m3fn)
+    c[..., 5] = 0.0
+    sc.fill_(2.0 ** -7)
+    if kind == "steps":  # 3, 7, 11 or 15 steps of 2^-21
+        k = torch.randint(0, 4, (1, 1, H, 576), generator=g, device="cuda")
+        x = (4 * k + 3) * 2.0 ** -21
+    else:
+        x = torch.rand(1, 1, H, 576, generator=g, device="cuda") * torch.exp2(
+            -torch.randint(10, 30, (1, 1, H, 576), generator=g, device="cuda").float())
+    x[..., 5] = torch.where(torch.arange(H, device="cuda") % 2 == 0, 1.0, 1.9921875)
+    q = x.to(torch.bfloat16)
+    scale = 2.0 ** 11 if kind == "steps" else 32.0
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, scale=scale, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, [L], scale)
+    rows = ref.rows_of(c, sc, table[0], L)[:, 0].abs()
+    some = q.double().abs()[0, 0] * (torch.arange(576, device="cuda") != 5)
+    s_abs = (rows @ some.T).amax(0) * scale  # per head
+    off = scale * 2.0 ** -22 * q[0, 0, :, 5].double() * rows.sum(1).max() + 576 * 2.0 ** -24 * s_abs
+    assert ((lse.double() - rl).abs()[0, 0] <= off + 2.0 ** -20 * (1 + rl.abs()[0, 0])).all()
+    ref.close(o, ro, mag * (1 + 2 ** 8 * torch.expm1(2 * off)[:, None]), "o")
+
+
 @pytest.mark.parametrize("H,ps", [(16, 16), (32, 16), (64, 16), (16, 32)])
 def test_decode_scales_of_places_without_a_page(H, ps):
     """Tiles that a sequence's pages fill only in part, each in a CTA that held a NaN page's scales
