@@ -154,8 +154,8 @@ struct DecSmem {
     alignas(1024) unsigned char p[kPB][kP];
     alignas(1024) unsigned char stage[kStage][kE4M3 ? kCodes : 16];
     alignas(16) float red[4][NC];  // per warp: column maxima, then column sums
-    float red_o[kE4M3 ? 4 : 1][NC];  // e4m3: maxima with the pages' scales
-    float fac[NC], top[NC], top_o[NC];  // per column: rescaling factor, then 1 / sum; the maxima
+    float page_lg[2][4];  // e4m3: log2 of the warps' page scales
+    float fac[NC], top[NC], ahead[NC];  // per column: rescaling factor, then 1 / sum; the maximum; e4m3: see there
     float scale[kStage][4];  // of a tile's boxes: their pages' scales
     int row[NC];            // output row of a column, less the sequence's and group's first
     uint64_t full[kRing], empty[kRing], full_rope[kRopes], empty_rope[kRopes];
@@ -621,7 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         Pieces next = w;
         for (; w.take > 0; w = next) {
             const int len = a.kv_lens[w.n];
-            float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1], mo[kE4M3 ? 2 * J : 1], base[kE4M3 ? 2 * J : 1];
+            // e4m3: the maximum of score + log2(page scale) is m + ahead (kept apart, for scores whose last
+            // place is above 1), and a weight's share of O^T is p scale base, in units of 2^(m + ahead - kLift)
+            float m[2 * J], l[2 * J], qs[kE4M3 ? 2 * J : 1], ahead[kE4M3 ? 2 * J : 1], base[kE4M3 ? 2 * J : 1];
 #pragma unroll
             for (int i = 0; i < 2 * J; ++i) {
                 // columns behind the last: weights 0, and no say in when to rescale
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l[i] = 0.0f;
                 if (kE4M3) {
                     const int c = col(i);
-                    mo[i] = m[i];
+                    ahead[i] = 0.0f;
                     base[i] = 0.0f;
                     qs[i] = ct * NC + c < cols
                                 ? a.q_scale[(int64_t)w.n * a.Sq * a.H + w.g * Hg + sm.row[c]] * a.scale_log2 : 0.0f;
@@ -675,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (t * kTok + r0 + 8 > last)
                                 s[j][2 + i] = -INFINITY;
                         }
-                        const float most = kE4M3 ? fminf(m[k] + kGrow, mo[k] - lg + kGrowO) : m[k] + kGrow;
+                        // (rounded down: what passes is no further above m, wherever m is)
+                        const float most = kE4M3 ? __fadd_rd(m[k], fminf(kGrow, ahead[k] - lg + kGrowO)) : m[k] + kGrow;
                         grow |= s[j][i] > most || s[j][2 + i] > most;
                     }
                 if (softmax_or(group, grow)) {
@@ -687,12 +690,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if (lane < 4) {
+                        if (lane < 4)
                             sm.red[quarter][col(i)] = x;
-                            if (kE4M3)
-                                sm.red_o[quarter][col(i)] = x + lg;
-                        }
                     }
+                    if (kE4M3 && lane == 0)
+                        sm.page_lg[group][quarter] = lg;
                     softmax_sync(group);
 #pragma unroll
                     for (int i = 0; i < 2 * J; ++i) {
@@ -700,16 +702,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mn = fmaxf(fmaxf(fmaxf(sm.red[0][c], sm.red[1][c]), fmaxf(sm.red[2][c], sm.red[3][c])),
                                                m[i]);
                         f[i] = m[i] == mn ? 1.0f : ex2(m[i] - mn);
-                        m[i] = mn;
                         l[i] *= f[i];
                         if (kE4M3) {
-                            const float on = fmaxf(
-                                fmaxf(fmaxf(sm.red_o[0][c], sm.red_o[1][c]), fmaxf(sm.red_o[2][c], sm.red_o[3][c])), mo[i]);
-                            f[i] = mo[i] == on ? 1.0f : ex2(mo[i] - on);
-                            mo[i] = on;
-                            // a weight's share of O^T is p scale base: in units of 2^(mo - m - kLift)
-                            base[i] = ex2((mn == -INFINITY ? 0.0f : mn) - (on == -INFINITY ? 0.0f : on) + kLift);
+                            const float held = m[i] == -INFINITY ? -INFINITY : m[i] == mn ? ahead[i] : m[i] - mn + ahead[i];
+                            float most = held;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                most = fmaxf(most, sm.red[k][c] - (mn == -INFINITY ? 0.0f : mn) + sm.page_lg[group][k]);
+                            ahead[i] = most == -INFINITY ? 0.0f : most;
+                            f[i] = ex2(held - ahead[i]);
+                            base[i] = ex2(kLift - ahead[i]);
                         }
+                        m[i] = mn;
                         if (quarter == 0 && lane < 4)
                             sm.fac[c] = f[i];
                     }
@@ -742,6 +746,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 if (SM::kPB == 1 && nt > 0)
                     pv_wait(nt - 1);  // P^T's one buffer has been read
+                // base is at most 2^111 (a page of zeros has a scale of 2^-100): of a page scale above 2^16 the
+                // rest goes to the weights, or its product with base would pass float32's range
+                if (kE4M3 && page_scale > 65536.0f) {
+                    const float part = page_scale * (1.0f / 65536.0f);
+                    page_scale = 65536.0f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[j][i] *= part;
+                }
                 unsigned char *pt = sm.p[nt % SM::kPB];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -811,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (quarter == 0) {
                         sm.top[c] = m[i];
                         if (kE4M3)
-                            sm.top_o[c] = mo[i];
+                            sm.ahead[c] = ahead[i];
                     }
                 }
             }
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c = group * kCols + gtid;
                 const float sum = sm.red[0][c] + sm.red[1][c] + sm.red[2][c] + sm.red[3][c];
                 const float lse2 = sum == 0.0f ? -INFINITY : sm.top[c] + log2f(sum);
-                const float unit = kE4M3 ? ex2((sm.top_o[c] == -INFINITY ? 0.0f : sm.top_o[c]) - sm.top[c] - kLift) : 1.0f;
+                const float unit = kE4M3 ? ex2(sm.ahead[c] - kLift) : 1.0f;
                 sm.fac[c] = sum == 0.0f ? 0.0f : unit / sum;
                 if (!whole)
                     a.part_lse[slot * NC + c] = lse2;

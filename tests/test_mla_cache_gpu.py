@@ -273,6 +273,44 @@ def test_decode_q_far_below_its_largest_number(kind, H):
     ref.close(o, ro, mag * (1 + 2 ** 8 * torch.expm1(2 * off)[:, None]), "o")
 
 
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("ps", [16, 64])
+@pytest.mark.parametrize("power", [10, 24, 25, 26, 40, 80])
+def test_decode_zeros_beside_large_numbers(H, ps, power):
+    """Rows of zeros (scale 2^-100) beside rows of numbers near 2^power whose scores are far below
+    or level with them, as the append writes them: their weights, down to 0, times their scale stay
+    numbers."""
+    L = 4 * ps
+    g = torch.Generator(device="cuda").manual_seed(87)
+    table = torch.randperm(12, generator=g, device="cuda").to(torch.int32).reshape(3, 4)
+    rows = torch.zeros(3, L, 1, 576, device="cuda")
+    rows[1:, ps:2 * ps] = (1 + torch.rand(2, ps, 1, 576, generator=g, device="cuda")) * 2.0 ** power
+    rows[0] = (1 + torch.rand(L, 1, 576, generator=g, device="cuda")) * 2.0 ** power  # no zeros: one row, of
+    rows[0, L // 2 + 3] *= 0.25                                                       # the least, far above the rest
+    rows[2, 3 * ps - 7:] = torch.randn(ps + 7, 1, 576, generator=g, device="cuda")
+    cache = torch.zeros(12, ps, 1, 576, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.zeros(12, 1, device="cuda")
+    cu = torch.arange(4, dtype=torch.int32, device="cuda") * L
+    kda.kda_mla_cache_append(rows.reshape(-1, 1, 576).to(torch.bfloat16), cu, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                             table, cache, cache_scale=sc)
+    q = -torch.rand(3, 1, H, 576, generator=g, device="cuda")
+    q[:, :, ::2] = -q[:, :, ::2] * 2.0 ** -power  # every other head: scores of a few hundred, level with the rest
+    q = q.to(torch.bfloat16)
+    scale = 192 ** -0.5
+    o, lse = kda.kda_mla_decode(q, cache, table, torch.full((3,), L, dtype=torch.int32, device="cuda"), scale=scale,
+                                cache_scale=sc)
+    ro, rl, mag = ref.decode(q, cache, sc, table, [L] * 3, scale)
+    # every other head's scores reach 576 * 2 / 13.9 = 83: their float32 sums move e^s by 576 * 2^-24 * 83
+    ref.close(o[:, :, ::2], ro[:, :, ::2], mag[:, :, ::2] * (1 + 2 ** 8 * math.expm1(576 * 2.0 ** -24 * 83)), "o, level")
+    ref.lse_close(lse[:, :, ::2], rl[:, :, ::2], 83.0)
+    # the other heads' large rows have scores of -2^power and less: weights of 0, but for the first sequence's least
+    assert torch.isfinite(o[:, :, 1::2]).all()
+    ref.close(o[:, :, 1::2], ro[:, :, 1::2], mag[:, :, 1::2], "o, far below")
+    ref.lse_close(lse[1:, :, 1::2], rl[1:, :, 1::2], 83.0)
+    ref.lse_close(lse[:1, :, 1::2], rl[:1, :, 1::2], float(rl[:1, :, 1::2].abs().max()))
+    assert kda.kda_device_status() == 0
+
+
 @pytest.mark.parametrize("H,ps", [(16, 16), (32, 16), (64, 16), (16, 32)])
 def test_decode_scales_of_places_without_a_page(H, ps):
     """Tiles that a sequence's pages fill only in part, each in a CTA that held a NaN page's scales
