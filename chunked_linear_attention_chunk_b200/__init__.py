@@ -57,6 +57,7 @@ EXPORTS = (
     "kda_chunk_fwd_prep",
     "kda_chunk_fwd_scan",
     "kda_selftest_device_timeout",
+    "kda_selftest_role_timeout",
     "kda_selftest_append_timeout",
     "kda_chunk_fwd_varlen_workspace",
     "kda_chunk_fwd_varlen",
@@ -164,6 +165,8 @@ def lib() -> ctypes.CDLL:
     L.kda_mla_decode.restype = I
     L.kda_mla_cache_append.argtypes = [I, P, I, I, I, I, I, P, P, P, I, I, P, P, I, I, P]
     L.kda_mla_cache_append.restype = I
+    L.kda_selftest_role_timeout.argtypes = [ctypes.c_uint32, P]
+    L.kda_selftest_role_timeout.restype = I
     L.kda_selftest_append_timeout.argtypes = [ctypes.c_uint32, *L.kda_mla_cache_append.argtypes]
     L.kda_selftest_append_timeout.restype = I
     _lib = L
@@ -753,6 +756,12 @@ def kda_selftest_device_timeout(limit_us: int = 20000, device=None) -> None:
     ``limit_us`` and records KDA_ERR_DEVICE_TIMEOUT (read it with kda_device_status)."""
     dev = device if device is not None else torch.cuda.current_device()
     _raise(lib().kda_selftest_device_timeout(int(limit_us), _stream(dev)), "kda_selftest_device_timeout")
+
+
+def kda_selftest_role_timeout(tries: int = 4096, device=None) -> None:
+    """The same for the waits of the latent-attention kernels, which run out after ``tries``."""
+    dev = device if device is not None else torch.cuda.current_device()
+    _raise(lib().kda_selftest_role_timeout(int(tries), _stream(dev)), "kda_selftest_role_timeout")
 
 
 def kda_selftest_append_timeout(limit_us, kv_new, cu_new, kv_lens, block_table, cache, cache_scale=None) -> None:

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- copies of Y1
         asm volatile("griddepcontrol.wait;" ::: "memory");  // keys: the launch that writes D and lse
         Ring<SM::kY1> r1;
-        for (int i = 0; i < steps && !wait.dead; ++i, r1.step()) {
+        for (int i = 0; i < steps; ++i, r1.step()) {
             const int first = y_first + i * kStep, live = ly - first, y = (kKeys ? q0 : k0) + first;
             float cl[kStep / 32], cd[kStep / 32];
             if (kKeys)
@@ -266,10 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&sm.y1_empty[r1.slot], (r1.round - 1) & 1);
             else if (!kKeys && r1.slot == SM::kY1 - 2)
                 wait(&sm.x_full, 0);
-            if (wait.dead)
-                break;
             uint64_t *bar = live < kStep ? &sm.tail[0] : &sm.y1_full[r1.slot];
-            if (elect()) {
+            if (elect() && !wait.dead) {
                 mbar_arrive_expect_tx(bar, 3 * kYBlk);
                 tma_load_4d(sm.y1[r1.slot], &maps.y1, 0, y, h, 0, bar);
                 if (!kKeys)
@@ -296,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<SM::kY1> r1;
         if (steps > 0)
             wait(kKeys ? &sm.x_landed : &sm.x_full, 0);
-        for (int i = 0; i < steps && !wait.dead; ++i, r1.step()) {
+        for (int i = 0; i < steps; ++i, r1.step()) {
             wait(&sm.y1_full[r1.slot], r1.round & 1);
             if (i > 0)
                 wait(&sm.s_read, (i - 1) & 1);
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto fetch = [&](int i, int slot) {
             const int first = y_first + i * kStep, live = ly - first;
             uint64_t *bar = live < kStep ? &sm.tail[1] : &sm.y2_full[slot];
-            if (elect()) {
+            if (elect() && !wait.dead) {
                 mbar_arrive_expect_tx(bar, 2 * kYBlk);
                 tma_load_4d(sm.y2[slot], &maps.y2, 0, (kKeys ? q0 : k0) + first, h, kKeys ? 0 : 2, bar);
             }
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<SM::kY2> r2, rf;
         if (steps > 0)
             wait(&sm.x_full, 0);
-        for (int i = 0; i < steps && !wait.dead; ++i, r2.step()) {
+        for (int i = 0; i < steps; ++i, r2.step()) {
             wait(&sm.y2_full[r2.slot], r2.round & 1);
             if (i > 0)
                 wait(&sm.dp_read, (i - 1) & 1);
@@ -354,8 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i - 1 + SM::kY2 < steps) {
                     if (kKeys)
                         wait(&sm.y2_empty[rf.slot], rf.round & 1);
-                    if (!wait.dead)
-                        fetch(i - 1 + SM::kY2, rf.slot);
+                    fetch(i - 1 + SM::kY2, rf.slot);
                 }
                 rf.step();
             }
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ed(smem_u32(sm.e), 16, 1024, tc::kSw128), pd(smem_u32(sm.p), 16, 1024, tc::kSw128);
         Ring<SM::kY1> r1;
         Ring<SM::kY2> r2;
-        for (int i = 0; i < steps && !wait.dead; ++i, r1.step(), r2.step()) {
+        for (int i = 0; i < steps; ++i, r1.step(), r2.step()) {
             const uint32_t buf = i & 1, par = (i >> 1) & 1;
             if (kKeys) {
                 wait(&sm.y2_full[r2.slot], r2.round & 1);
@@ -600,10 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    wait.report(a.status);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
+    wait.finish(a.status);
     if (warp == kElemWarps)
         tc::tmem_dealloc(tmem, 512);
 }

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (kE4M3) {
                     if (rst.round > 0)
                         wait(&sm.empty_stage[rst.slot], (rst.round - 1) & 1);
-                    if (!wait.dead && elect()) {
+                    if (elect() && !wait.dead) {
                         mbar_arrive_expect_tx(&sm.full_stage[rst.slot], 4 * bytes + bytes / 2);
                         rope(sm.stage[rst.slot] + 4 * kBlk, 64, &sm.full_stage[rst.slot]);
                         half(sm.stage[rst.slot], 0, &sm.full_stage[rst.slot]);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wait(&sm.empty[rh.slot], (rh.round - 1) & 1);
                     if (rr.round > 0)
                         wait(&sm.empty_rope[rr.slot], (rr.round - 1) & 1);
-                    if (!wait.dead && elect()) {
+                    if (elect() && !wait.dead) {
                         mbar_arrive_expect_tx(&sm.full_rope[rr.slot], bytes);
                         rope(sm.rope[rr.slot], 128, &sm.full_rope[rr.slot]);
                         mbar_arrive_expect_tx(&sm.full[rh.slot], 4 * bytes);
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rh.step();
                     if (rh.round > 0)
                         wait(&sm.empty[rh.slot], (rh.round - 1) & 1);
-                    if (!wait.dead && elect()) {
+                    if (elect() && !wait.dead) {
                         mbar_arrive_expect_tx(&sm.full[rh.slot], 4 * bytes);
                         half(sm.ring[rh.slot], 4, &sm.full[rh.slot]);
                     }
@@ -447,13 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<SM::kStage> rst;
         Ring<2> rs;
         uint32_t nq = 0;
-        for (; w.take > 0 && !wait.dead; w.next(a), ++nq) {
+        for (; w.take > 0; w.next(a), ++nq) {
             if (nq > 0)
                 wait(&sm.q_empty, (nq - 1) & 1);
-            if (wait.dead)
-                break;
             if (maps.q_rows == NC) {  // one group: a sequence's columns are rows in order
-                if (elect()) {
+                if (elect() && !wait.dead) {
                     const int r = w.n * cols + ct * NC;
                     mbar_arrive_expect_tx(&sm.q_full, NC * kBytes);
                     if constexpr (kE4M3) {
@@ -483,11 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 const int copies = kE4M3 ? (by_hand ? 8 : 10) : kDC / 64;
-                if (elect())
+                if (elect() && !wait.dead)
                     mbar_arrive_expect_tx(&sm.q_full,
                                           (uint32_t)(n * maps.q_rows) * (by_hand ? kBytes - 2 * kDR : kBytes));
                 __syncwarp();
-                for (int i = lane; i < n * copies; i += 32) {
+                for (int i = lane; i < n * copies && !wait.dead; i += 32) {
                     const int c = i / copies * maps.q_rows, blk = i % copies;
                     const int r = row0 + sm.row[c];
                     if (!kE4M3)
@@ -502,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             wait(&sm.q_full, nq & 1);
-            for (int t = 0; t < w.take && !wait.dead; ++t, rs.step()) {
+            for (int t = 0; t < w.take; ++t, rs.step()) {
                 if (rs.round > 0)
                     wait(&sm.s_empty[rs.slot], (rs.round - 1) & 1);
                 const uint32_t d = tmem + rs.slot * SM::kSW;
@@ -563,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<SM::kRing> rp;
         Ring<SM::kStage> rst;
         Ring<SM::kPB> rb;
-        for (; w.take > 0 && !wait.dead; w.next(a))
-            for (int t = 0; t < w.take && !wait.dead; ++t, rb.step()) {
+        for (; w.take > 0; w.next(a))
+            for (int t = 0; t < w.take; ++t, rb.step()) {
                 wait(&sm.p_full[rb.slot], rb.round & 1);
                 tc::fence_after_sync();
                 const uint32_t p0 = rb.slot * SM::kP;
@@ -901,10 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0 && !go_on)
             a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
-    wait.report(a.status);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
+    wait.finish(a.status);
     if (warp == 4)
         tc::tmem_dealloc(tmem, kTmemCols);
 }

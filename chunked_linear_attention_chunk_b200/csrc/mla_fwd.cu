@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_4d(sm.q[t], &maps.q, 0, q0 + i0 + t * kRows, h, 0, &sm.q_full);
             }
             Ring<kV> rv;
-            for (int j = 0; j < n_steps && !wait.dead; ++j, rv.step()) {
+            for (int j = 0; j < n_steps; ++j, rv.step()) {
                 const int s = j & 1, key = k0 + j * kKeys, live = lk - j * kKeys;
                 if (j >= 2)
                     wait(&sm.k_empty[s], (j / 2 - 1) & 1);
-                if (!wait.dead && elect()) {
+                if (elect() && !wait.dead) {
                     mbar_arrive_expect_tx(&sm.k_full[s], 3 * kKBlk);
                     tma_load_4d(sm.k[s], &maps.kv, 0, key, h, 0, &sm.k_full[s]);
                     tma_load_2d(sm.k[s] + 2 * kKBlk, &maps.kr, 0, key, &sm.k_full[s]);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (rv.round > 0)
                     wait(&sm.v_empty[rv.slot], (rv.round - 1) & 1);
                 uint64_t *bar = live < kKeys ? &sm.v_tail : &sm.v_full[rv.slot];
-                if (!wait.dead && elect()) {
+                if (elect() && !wait.dead) {
                     mbar_arrive_expect_tx(bar, 2 * kKBlk);
                     tma_load_4d(sm.v[rv.slot], &maps.kv, 0, key, h, 2, bar);
                 }
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Desc qd(smem_u32(sm.q[0]), 16, 1024, tc::kSw128), kd(smem_u32(sm.k[0]), 16, 1024, tc::kSw128);
         if (n_steps > 0)
             wait(&sm.q_full, 0);
-        for (int j = 0; j < n_steps && !wait.dead; ++j) {
+        for (int j = 0; j < n_steps; ++j) {
             wait(&sm.k_full[j & 1], (j / 2) & 1);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id = tc::idesc_bf16(kRows, kDV, false, true);
         const Desc vd(smem_u32(sm.v[0]), kKBlk, 1024, tc::kSw128);
         Ring<kV> rv;
-        for (int j = 0; j < n_steps && !wait.dead; ++j, rv.step()) {
+        for (int j = 0; j < n_steps; ++j, rv.step()) {
             wait(&sm.v_full[rv.slot], rv.round & 1);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
@@ -333,10 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.lse && row < lq)
             a.lse[r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    wait.report(a.status);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
+    wait.finish(a.status);
     if (warp == 8)
         tc::tmem_dealloc(tmem, 512);
 }

@@ -10,12 +10,19 @@ namespace kda {
 namespace mla {
 
 // Bounded waits of one role.  A try suspends the thread for some microseconds while the barrier is
-// not ready, so the limit is of the order of seconds.  After the first wait that runs out the role
-// waits no more, so a broken pipeline ends soon; `report` records it in the status word, once, at
-// the kernel's end (a few instructions a wait matter: the roles' loops share the instruction cache).
+// not ready, so the limit is of the order of seconds (some 3 us and 3 s measured).  After the first wait
+// that runs out the role waits no more, so a broken pipeline ends soon; `finish` records it in the
+// status word, once, at the kernel's end (a few instructions a wait matter: the roles' loops share the
+// instruction cache).
+// The lanes of a warp may disagree about a wait that ran out as its barrier completed, so a role whose
+// lanes act together (elect) runs its loop to the end, with nothing to wait for, and what must not
+// follow such a wait (a copy) asks for `dead` behind the election.  (Leaving the loop by a vote of the
+// lanes cost the issuing warps 1 % of the forward and the backward.)
 constexpr uint32_t kWaitTries = 1u << 20;
+constexpr unsigned long long kDrainNs = 10000000ull;
 struct Waits {
     bool dead;
+    uint32_t tries = kWaitTries;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity)
     {
         const uint32_t a = smem_u32(bar);
@@ -23,7 +30,7 @@ struct Waits {
             return;
 #pragma unroll 1
         for (uint32_t n = 0; !mbar_try_wait(a, parity); ++n)
-            if (n == kWaitTries) {
+            if (n == tries) {
                 dead = true;
                 break;
             }
@@ -50,10 +57,17 @@ struct Waits {
             (*this)(z, pz);
         }
     }
-    __device__ __forceinline__ void report(unsigned int *status) const
+    // The CTA's roles are over: all threads call.  Where one gave up, copies and products may still be
+    // on their way into shared and tensor memory, which go with the CTA: they get some milliseconds.
+    __device__ __forceinline__ void finish(unsigned int *status) const
     {
         if (dead)
             report_device_error(status, KDA_ERR_DEVICE_TIMEOUT);
+        tc::fence_before_sync();
+        if (__syncthreads_or(dead))
+            for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kDrainNs;)
+                __nanosleep(1000);
+        tc::fence_after_sync();
     }
 };
 

@@ -561,6 +561,15 @@ kda_status kda_device_status(kda_stream_t stream);
 kda_status kda_selftest_device_timeout(uint32_t limit_us, kda_stream_t stream);
 
 /*
+ * kda_selftest_role_timeout -- the same for the latent-attention kernels, whose waits give up after
+ * a number of tries (1048576; each lasts up to some microseconds).  A warp waits as their roles do,
+ * on barriers that nothing completes, with `tries` (1 .. 1048576) for a limit, and records
+ * KDA_ERR_DEVICE_TIMEOUT (KDA_ERR_DEVICE_BOUNDS if it went on after a wait that ran out).
+ * Errors: INVALID_ARG (limit out of range), CUDA.
+ */
+kda_status kda_selftest_role_timeout(uint32_t tries, kda_stream_t stream);
+
+/*
  * kda_selftest_append_timeout -- kda_mla_cache_append on a bad day: the copies of its new rows
  * never start, so that each CTA's wait for them runs out after `limit_us` microseconds (1 ..
  * 2 000 000; a second wait for copies on their way lasts as long).  It records

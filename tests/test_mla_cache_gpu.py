@@ -584,3 +584,30 @@ def test_prefill_append_decode_together(e4m3):
         ref.close(od, ro, mag, "o")
         ref.lse_close(ld, rl, 32.0)
     assert kda.kda_device_status() == 0
+
+
+def test_role_waits_run_out_and_the_context_survives():
+    """The waits of the kernels' roles, on barriers that nothing completes, with a short limit: the
+    timeout is recorded, nothing acts on what did not come, and the next call is sound.  The time of
+    a try, and with it the real limit of 2^20, is of the order of seconds at most."""
+    assert kda.kda_device_status() == 0
+    kda.kda_selftest_role_timeout(1)  # warm-up
+    assert kda.kda_device_status() == 6  # KDA_ERR_DEVICE_TIMEOUT
+    ms = []
+    for tries in (1 << 10, 1 << 14):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        kda.kda_selftest_role_timeout(tries)
+        b.record()
+        assert kda.kda_device_status() == 6
+        ms.append(a.elapsed_time(b))
+        assert ms[-1] > 10.0  # what was on its way gets 10 ms to land
+    # three waits run out in a call: the time of one of 2^20 tries from that of 2^14 - 2^10 more in each
+    limit_s = (ms[1] - ms[0]) * 1e-3 / 3 * (1 << 20) / ((1 << 14) - (1 << 10))
+    assert 0.0 < limit_s < 30.0, (ms, limit_s)
+    print("limit of a role's wait: %.2f s" % limit_s)
+    q, c, sc, table, kv_lens = make([100], 1, 16, 1, 64, True, seed=88)
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, [100], 192 ** -0.5)
+    ref.close(o, ro, mag, "o")
+    assert kda.kda_device_status() == 0

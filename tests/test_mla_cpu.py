@@ -113,6 +113,11 @@ def test_append_validates(L):
         assert _app(L, **bad) == ALIAS, bad
 
 
+def test_role_selftest_validates(L):
+    for tries in (0, (1 << 20) + 1):
+        assert L.kda_selftest_role_timeout(tries, None) == INVALID
+
+
 def test_append_selftest_validates(L):
     for limit in (0, 2000001):
         assert L.kda_selftest_append_timeout(limit, 3, P(0), 20, 1, 512, 64, kda.KDA_BF16, P(1), P(2), P(3), 4, kda.KDA_BF16,
