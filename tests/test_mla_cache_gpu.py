@@ -76,6 +76,31 @@ def test_decode_matches_64_bits(lens, Sq, H, G, ps, e4m3):
     assert kda.kda_device_status() == 0
 
 
+GROUPS = [
+    # several latent groups, and more columns a group than one tile holds
+    ([130, 5], 1, 144, 2, 64),                 # 72 columns, runs of 8 heads
+    ([70, 300], 3, 96, 2, 32),                 # 144 columns
+    ([200], 20, 15, 3, 16),                    # 100 columns, single heads
+    ([90, 0, 17], 2, 64, 4, 64),               # 32 columns
+    ([400, 33], 1, 12, 4, 16),                 # 3 columns
+    ([65, 1000], 5, 35, 5, 128),               # 35 columns
+    ([500], 80, 64, 2, 64),                    # 2560 columns: 40 tiles
+    ([260, 90], 300, 32, 1, 64),               # 9600 columns: more tiles than SMs; more tokens than rows
+    ([150 + 7 * i for i in range(30)], 1, 32, 16, 32),
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens,Sq,H,G,ps", GROUPS)
+def test_decode_groups_and_column_tiles(lens, Sq, H, G, ps, e4m3):
+    q, c, sc, table, kv_lens = make(lens, Sq, H, G, ps, e4m3, seed=89 + len(lens) + H)
+    o, lse = kda.kda_mla_decode(q, c, table, kv_lens, cache_scale=sc)
+    ro, rl, mag = ref.decode(q, c, sc, table, lens, 192 ** -0.5)
+    ref.close(o, ro, mag, "o")
+    ref.lse_close(lse, rl, 32.0)
+    assert kda.kda_device_status() == 0
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("std", [0.0, 6.0])
 def test_decode_flat_and_peaked(std, e4m3):
