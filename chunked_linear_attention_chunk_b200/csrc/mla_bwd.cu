@@ -225,12 +225,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
     const int lx = kKeys ? lk : lq, ly = kKeys ? lq : lk;
     // with a causal mask the first keys and the last queries have the most to do: they go first
-    const int r0 = (kKeys ? it.k : (lx + kRows - 1) / kRows - 1 - it.k) * kRows, rows = min(kRows, lx - r0);
+    const int r0 = (kKeys ? it.k : (lx + kRows - 1) / kRows - 1 - it.k) * kRows;
+    int rows = min(kRows, lx - r0);
     const int off = lk - lq;  // causal: key j is visible to query i from i = j - off on
     // Y rows [y_first, y_end)
     const int y_first = kKeys && a.causal ? max(0, r0 - off) : 0;
     const int y_end = !kKeys && a.causal ? min(ly, r0 + rows + off) : ly;
-    const int steps = y_first < y_end ? (y_end - y_first + kStep - 1) / kStep : 0;
+    int steps = y_first < y_end ? (y_end - y_first + kStep - 1) / kStep : 0;
+    if (!rows_in(r0, rows, lx, kKeys ? k0 : q0, kKeys ? a.Tk : a.Tq) ||
+        (steps > 0 && !rows_in(y_first, y_end - y_first, ly, kKeys ? q0 : k0, kKeys ? a.Tq : a.Tk))) {
+        report_device_error(a.status, KDA_ERR_DEVICE_BOUNDS);
+        rows = steps = 0;
+    }
 
     if (warp == kElemWarps && steps > 0 && elect()) {
         const int x = (kKeys ? k0 : q0) + r0;

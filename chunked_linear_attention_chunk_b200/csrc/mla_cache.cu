@@ -124,6 +124,11 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
     const int slot0 = it.k == 0 ? len % ps : 0;                         // first slot written
     const int64_t first = it.k == 0 ? 0 : (int64_t)it.k * ps - len % ps;  // its row among the sequence's
     const int rows = (int)min((int64_t)(ps - slot0), m - first);
+    if (!rows_in(slot0, rows, ps, (int64_t)page * ps, (int64_t)a.num_pages * ps) ||
+        !rows_in(first, rows, m, a.cu[n], a.T_new)) {
+        report_device_error(a.status, KDA_ERR_DEVICE_BOUNDS);
+        return;
+    }
     const int r0 = tid / kVecs, vec = tid % kVecs;  // this thread's first row and its vector
     const uint4 *src = reinterpret_cast<const uint4 *>(a.x + ((a.cu[n] + first + r0) * a.G + g) * kDC) + vec;
     const int64_t step = (int64_t)kPass * a.G * kVecs;  // vectors from a pass to the next

@@ -114,6 +114,14 @@ __device__ __forceinline__ Span span_of(const int32_t *__restrict__ cu, int n, i
     return s;
 }
 
+// Debug builds: whether a CTA's rows [row, row + rows) of a sequence of `len` rows that starts at
+// `first` lie in the sequence and on its packed axis of T.  (Offsets, lengths and pages that come from
+// device arrays are checked in every build.)
+__device__ __forceinline__ bool rows_in(int64_t row, int64_t rows, int64_t len, int64_t first, int64_t T)
+{
+    return !kDebugChecks || (row >= 0 && rows > 0 && row + rows <= len && first >= 0 && first + len <= T);
+}
+
 // 2^x by the hardware's approximation (2 ulp; results below the normal range flush to 0).
 __device__ __forceinline__ float ex2(float x)
 {

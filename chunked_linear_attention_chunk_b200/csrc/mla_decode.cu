@@ -324,6 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.inside = false;
     if (w.left > 0)
         w.settle(a);
+    if (w.take > 0 && (!rows_in(w.t, w.take, w.tiles, 0, w.tiles) || !rows_in(w.n, 1, a.N, 0, a.N) ||
+                       !rows_in(w.g, 1, a.G, 0, a.G))) {
+        report_device_error(a.status, KDA_ERR_DEVICE_BOUNDS);
+        w.take = 0;
+    }
     Waits wait{false};
 
     if (warp == 4 || warp == 7) {

@@ -111,6 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q0 = a.cu_q[it.seq], k0 = a.cu_k[it.seq], lq = a.cu_q[it.seq + 1] - q0, lk = a.cu_k[it.seq + 1] - k0;
     // with a causal mask the last queries see the most keys: they go first
     const int i0 = ((lq + kTiles * kRows - 1) / (kTiles * kRows) - 1 - it.k) * kTiles * kRows;
+    if (!rows_in(i0, min(kTiles * kRows, lq - i0), lq, q0, a.Tq) || (kDebugChecks && (k0 < 0 || k0 + lk > a.Tk))) {
+        report_device_error(a.status, KDA_ERR_DEVICE_BOUNDS);
+        return;
+    }
     int steps[kTiles], n_steps = 0;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {

@@ -29,3 +29,13 @@ def test_parity_tests_pass_on_the_debug_build():
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", *sel], cwd=ROOT, env=env,
                        capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+
+
+def test_latent_attention_passes_on_the_debug_build():
+    build.build(debug_checks=True)
+    env = dict(os.environ, KDA_DEBUG_CHECKS="1")
+    sel = ["tests/test_mla_gpu.py", "tests/test_mla_cache_gpu.py"]
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-p", "no:cacheprovider", "-k",
+                        "matches or groups or many_sequences or reads_a_page or records or refuses or invalid", *sel],
+                       cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
