@@ -466,6 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.lse2[(int64_t)h * a.Tq + q0 + r0 + r] = lse2;
             }
         }
+        // the first step's p goes where v lands: not before the warps that take v from there have their
+        // rows (S is issued without them; the later steps wait for the sum of the one before)
+        if (kKeys && set == 0 && steps > 0)
+            wait(&sm.x_full, 0);
         for (int i = set; i < steps; i += 2) {
             const int y = y_first + i * kStep;  // place of the step's first column
             const uint32_t par = (i >> 1) & 1;
@@ -510,12 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[k] = seen >> k & 1 ? p[k] : 0.0f;
             }
             if (kKeys) {
-                // p's place is free: the sum of the step before has read it, or, in the first step,
-                // the warps that take v from there (S is issued without them) have their rows
                 if (i > 0)
                     wait(&sm.acc2_done[set ^ 1], ((i - 1) >> 1) & 1);
-                else
-                    wait(&sm.x_full, 0);
                 store_32(sm.p, r, half * 4, p);
                 fence_proxy_async_smem();
                 arrive(&sm.p_full[set]);
