@@ -28,10 +28,10 @@
 // head by head, for the other.  dk_rope's parts are added over the heads, in order, by a third
 // launch.
 //
-// Measured: 16 heads, 8192 tokens, causal: 420 us for dq and 540 us for dk and dv (1090-1120 us a call in
-// a loop, where the 1000 W limit holds the clock near 1.5 GHz): 0.82 PFLOP/s of the formulas' 832
-// multiply-adds a pair, 1.13 of those taken; the tensor pipe is active 70 % of the time.  Six packed
-// documents of 100 to 1500 tokens: 208-217 us; there a CTA's first 250 KB (2 to 3 us) and its last
+// Measured: 16 heads, 8192 tokens, causal: 414 us for dq and 547 us for dk and dv by themselves, 1120-1140
+// us a call in a loop, where the 1000 W limit holds the clock near 1.5 GHz: 0.79 PFLOP/s of the formulas'
+// 832 multiply-adds a pair, 1.1 of those taken; the tensor pipe is active 74 and 68 % of the time.  Six
+// packed documents of 100 to 1500 tokens: 215-219 us; there a CTA's first 250 KB (2 to 3 us) and its last
 // stores weigh as much as its ten steps (0.82 and 1.09 us each).
 //
 // Warps: 0-15 elementwise; 16 copies (TMA) of X and Y1; 17 S; 18 the sums; 19 dP and copies of Y2.

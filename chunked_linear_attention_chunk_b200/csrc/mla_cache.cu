@@ -9,8 +9,8 @@
 // the maximum and for the rounding; longer pages read the rest from global memory, the second time
 // from L2.  Three CTAs an SM (more for smaller pages), so that some wait for rows while others round
 // theirs; nine warps each (eighteen: 33 us for the 27 below; rows held in registers, two CTAs an SM: 37).
-// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 27 us (4.3 TB/s; a page is 8 us of
-// lookups, rows, maximum and stores; 38 us with pages of 16), into a bfloat16 one 32 us (4.9 TB/s);
+// Measured: 16 prompts of 500 to 8000 rows into an 8-bit cache 27.5 us (4.7 TB/s; a page is 8 us of
+// lookups, rows, maximum and stores; 39 us with pages of 16), into a bfloat16 one 32 us (5.4 TB/s);
 // one row for each of 256 sequences 6 us, most of it the launch.
 #include <cuda_fp8.h>
 

@@ -35,10 +35,10 @@
 // equal bits; the shares depend on the lengths and the SM count alone).
 //
 // Measured (one launch and its join, inputs larger than L2): 256 sequences of 3000 to 5000 rows, 32
-// heads: bfloat16 210-220 us, 5.5 TB/s; e4m3 143-156 us, 4.0 TB/s.  A tile of 64 e4m3 rows takes
+// heads: bfloat16 217-220 us, 5.5 TB/s; e4m3 147-157 us, 4.0 TB/s.  A tile of 64 e4m3 rows takes
 // 1450 cycles: 666 of S^T and 464 of O^T products (both bound by shared memory), the softmax's chain
 // of waits and stores next to them; in a loop the 1000 W limit holds the clock near 1.45 GHz, and
-// alone the call takes 128 us.  23 ragged sequences up to 40000 rows, 2 tokens each: 128-132 us.
+// alone the launch takes 122 us.  23 ragged sequences up to 40000 rows, 2 tokens each: 131-133 us.
 // Also measured, and slower: prefetching tiles into L2 ahead of the copies (249 and 203 us for the
 // two batches), fetching the next S^T while the weights are stored (220 and 155, ragged 135), half
 // tiles of codes as places, nine for the eight there are (154.7 for 152.4).
@@ -142,7 +142,7 @@ struct DecSmem {
     static_assert(kRing <= 4 * kRopes, "a warp that waits for a rope place knows the round before the last consumed");
     static constexpr uint32_t kCodes = 4 * kBlk + kBlk / 2;  // a tile of codes: 4 x 128, then 64
     static constexpr int kSW = kE4M3 ? 2 * NC : NC;          // columns of S^T
-    static constexpr int kPB = NC == 64 && !kE4M3 ? 1 : 2;   // buffers of P^T (one where a second has no room)
+    static constexpr int kPB = NC == 64 && !kE4M3 ? 1 : 2;   // buffers of P^T (one where a second is 1 KB too much)
     static constexpr uint32_t kP = kTok * kPRow<NC, kE4M3> * (kE4M3 && NC > 16 ? 3 : 1);  // bytes of one
     // parts of O^T: a weight's three terms side by side where tensor memory has the room, one sum of
     // their three products where it has not
