@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kE4M3 ? kThreads : kCopyThreads, 4) mla_append
         for (int r = 0, k = 0; r < rows; r += kStaged, ++k) {
             const int count = min(rows - r, kStaged);
             fetch(r, count);
-            if (!mbar_wait_bounded(&landed, k & 1, a.status, limit)) {
+            if (__any_sync(0xffffffffu, !mbar_wait_bounded(&landed, k & 1, a.status, limit))) {
                 mbar_wait_bounded(&landed, k & 1, a.status, limit);  // copies on their way, before the CTA ends
                 return;
             }
